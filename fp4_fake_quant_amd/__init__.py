@@ -9,11 +9,12 @@ given are allocated with torch (device memory is torch's job here); every
 computation runs in the library's HIP kernels.
 """
 
+import contextlib
 import ctypes
 
 import torch
 
-from ._lib import GgufTensor, LoraDesc, LoraExpertsDesc, StTensor, TensorDesc, lib
+from ._lib import AdamwHyper, AdamwTensor, GgufTensor, LoraDesc, LoraExpertsDesc, StTensor, TensorDesc, lib
 
 QF_OK = 0
 QF_QDQ_A, QF_QDQ_W, QF_FP4_CORES, QF_MX_NOCLIP = 1, 2, 4, 8
@@ -512,6 +513,111 @@ def qf_lora_adapter_grads(G, A, B, dA=None, dB=None, accumulate=False, ws=None):
     _check(lib().qf_lora_adapter_grads(_p(G), _p(A), _p(B), rows, cols, r, _p(dA), _p(dB), int(bool(accumulate)),
                                        _p(ws), ws.numel() * ws.element_size(), _stream()), "qf_lora_adapter_grads")
     return dA, dB
+
+
+# --------------------------------------------------------------- AdamW ----
+ADAMW_BLOCK = 256
+
+
+def _same_gpu(*tensors):
+    """The one GPU that holds every given tensor (None entries are skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise TypeError("tensors must live on the GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors live on {dev} and {t.device}")
+    return dev
+
+
+def _on(dev):
+    """Makes dev the current device for a call (its current stream is then the call's)."""
+    if dev is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _flat(t, name, dtype, n):
+    if t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def adamw_state(n, state_bits=32, device="cuda"):
+    """Zeroed moments of a tensor of n elements: dict(m, v) in fp32, or dict(m, v, m_scale,
+    v_scale) for 8-bit states."""
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits is 8 or 32")
+    kind = torch.uint8 if state_bits == 8 else torch.float32
+    s = {k: torch.zeros(n, dtype=kind, device=device) for k in ("m", "v")}
+    if state_bits == 8:
+        blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+        s.update({k: torch.zeros(blocks, dtype=torch.float32, device=device) for k in ("m_scale", "v_scale")})
+    return s
+
+
+class AdamwBatch:
+    """Descriptors of the tensors that qf_adamw_step updates, built once and reusable.
+
+    items: list of dict(p, g, m, v, m_scale=None, v_scale=None, p16=None, weight_decay=0.0) of
+    contiguous device tensors with the same element count: p float32, g float32 or bfloat16,
+    m and v float32 (state_bits 32) or uint8 with float32 scales per 256 elements (8), p16
+    bfloat16.  The tensors must keep their storage while the batch is used.
+    """
+
+    def __init__(self, items, state_bits=32):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits is 8 or 32")
+        self.items, self.state_bits, self.n = items, state_bits, len(items)
+        self.arr = (AdamwTensor * max(len(items), 1))()
+        self.device = _same_gpu(*[t for it in items for t in it.values() if isinstance(t, torch.Tensor)])
+        state = torch.uint8 if state_bits == 8 else torch.float32
+        seen = set()
+        for i, it in enumerate(items):
+            n = it["p"].numel()
+            if n and it["p"].data_ptr() in seen:
+                raise ValueError("a tensor may appear once per batch")
+            seen.add(it["p"].data_ptr())
+            d = self.arr[i]
+            d.p = _flat(it["p"], "p", torch.float32, n)
+            if it["g"].dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError("g must be float32 or bfloat16")
+            d.g = _flat(it["g"], "g", it["g"].dtype, n)
+            d.g_bf16 = int(it["g"].dtype == torch.bfloat16)
+            d.m, d.v = _flat(it["m"], "m", state, n), _flat(it["v"], "v", state, n)
+            if state_bits == 8:
+                blocks = (n + ADAMW_BLOCK - 1) // ADAMW_BLOCK
+                d.m_scale = _flat(it["m_scale"], "m_scale", torch.float32, blocks)
+                d.v_scale = _flat(it["v_scale"], "v_scale", torch.float32, blocks)
+            if it.get("p16") is not None:
+                d.p16 = _flat(it["p16"], "p16", torch.bfloat16, n)
+            d.n, d.weight_decay = n, float(it.get("weight_decay", 0.0))
+        self.ref = ctypes.byref(self.arr)
+
+
+def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_lr=None, d_step=None,
+                  d_grad_scale=None, d_skip=None):
+    """One AdamW step of every tensor of an AdamwBatch, in place.  step counts from 1.  d_lr
+    (float32 [1]) and d_step (int64 [1]) on the device replace lr and step (a captured step
+    reads them on every replay); d_grad_scale (float32 [1]) multiplies the gradients; nothing
+    is written where d_skip (int32 or uint32 [1]) is not 0.  seed: of the 8-bit states'
+    stochastic rounding."""
+    dev = _same_gpu(d_lr, d_step, d_grad_scale, d_skip)
+    if dev is not None and batch.device is not None and dev != batch.device:
+        raise ValueError(f"device scalars live on {dev}, the tensors on {batch.device}")
+    for t, name, kinds in ((d_lr, "d_lr", (torch.float32,)), (d_step, "d_step", (torch.int64,)),
+                           (d_grad_scale, "d_grad_scale", (torch.float32,)),
+                           (d_skip, "d_skip", (torch.int32, torch.uint32))):
+        if t is not None and (t.dtype not in kinds or t.numel() != 1):
+            raise TypeError(f"{name} must be one {kinds[0]} on the device")
+    h = AdamwHyper(float(lr), float(beta1), float(beta2), float(eps), int(step), _p(d_lr), _p(d_step),
+                   _p(d_grad_scale), _p(d_skip), int(seed) & 0xFFFFFFFF)
+    with _on(batch.device):
+        _check(lib().qf_adamw_step(batch.ref, batch.n, batch.state_bits, ctypes.byref(h), _stream()), "qf_adamw_step")
 
 
 # ------------------------------------------------------------- dequant ----

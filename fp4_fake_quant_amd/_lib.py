@@ -58,6 +58,20 @@ class GgufTensor(ctypes.Structure):
                 ("type", ctypes.c_uint32), ("data", c_void_p), ("nbytes", ctypes.c_uint64)]
 
 
+class AdamwTensor(ctypes.Structure):
+    """Mirror of qf_adamw_tensor in include/qf.h."""
+    _fields_ = [("p", c_void_p), ("g", c_void_p), ("m", c_void_p), ("v", c_void_p),
+                ("m_scale", c_void_p), ("v_scale", c_void_p), ("p16", c_void_p), ("n", c_i64),
+                ("weight_decay", ctypes.c_double), ("g_bf16", ctypes.c_int32)]
+
+
+class AdamwHyper(ctypes.Structure):
+    """Mirror of qf_adamw_hyper in include/qf.h."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", c_i64), ("d_lr", c_void_p), ("d_step", c_void_p),
+                ("d_grad_scale", c_void_p), ("d_skip", c_void_p), ("seed", c_u32)]
+
+
 # name -> (restype, argtypes); every entry point declared in include/qf.h
 SIGNATURES = {
     "qf_version": (c_u32, []),
@@ -123,6 +137,7 @@ SIGNATURES = {
                                               c_void_p]),
     "qf_linear_forward_mxfp4": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_i64, c_i64, c_i64, c_i64,
                                         ctypes.c_uint, c_void_p, c_i64, c_void_p, c_i64, c_void_p]),
+    "qf_adamw_step": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
     "qf_noalloc_scratch_bytes": (c_size_t, []),
     "qf_nvfp4_tensor_scale_grouped_noalloc": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "qf_write_safetensors": (c_int, [ctypes.c_char_p, c_void_p, c_int, c_void_p, c_void_p, c_int]),

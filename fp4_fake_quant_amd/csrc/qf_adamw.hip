@@ -1,0 +1,343 @@
+// AdamW over many tensors: the step that turns the fp32 gradients of the straight-through
+// estimator and of the adapters into the next latent weights and their bf16 copies.
+//
+// Arithmetic (include/qf.h): separate fp32 roundings in the stated order (the build never
+// contracts a product and a sum), IEEE division and square root, so that a plain sequence of
+// elementwise fp32 operations gives the same bits.  8-bit states are E4M3 codes with an fp32
+// scale per 256-element block, stochastically rounded: with round-to-nearest a slow moving
+// average stands still (b2 = 0.999 moves sqrt(v) by 0.05% a step, half an E4M3 step is up to
+// 6%), with 16 random bits its expectation is right to 2^-16 of a step.
+//
+// One wave owns whole 256-element blocks, 4 consecutive elements per lane: every fp32 load
+// and store instruction of a wave covers 1 KiB of contiguous memory, and a block's largest
+// magnitude is one cross-lane reduction.
+#include <algorithm>
+#include <string.h>
+
+#include "qf_device.h"
+#include "qf_kernels.h"
+
+namespace qf {
+
+constexpr int AW_WG = 256;
+constexpr int AW_BLOCK = QF_ADAMW_BLOCK;           // elements per 8-bit block: 64 lanes x 4
+constexpr int AW_PER_WAVE = 4;                     // blocks in flight per wave
+constexpr int AW_CHUNK = AW_WG / 64 * AW_PER_WAVE * AW_BLOCK;
+constexpr float AW_MIN_MAX = 7.888609052210118e-31f;   // 2^-100: smaller block maxima store zeros
+
+static_assert(AW_BLOCK == 256, "a wave of 64 lanes holds one block, 4 elements per lane");
+
+// 32-bit finaliser: xor-shifts and two odd multipliers.
+__host__ __device__ inline uint32_t aw_hash(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x7FEB352Du;
+  x ^= x >> 15;
+  x *= 0x846CA68Bu;
+  return x ^ (x >> 16);
+}
+
+// b^t by repeated squaring in 64 bits.
+__host__ __device__ inline double aw_pow(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+__host__ __device__ inline void aw_scalars(AdamwScalars& s, double lr, double beta1, double beta2, int64_t step,
+                                           uint32_t seed) {
+  if (step < 1) step = 1;
+  s.lr = lr;
+  s.size = (float)(lr / (1.0 - aw_pow(beta1, step)));
+  s.root = (float)(1.0 / __builtin_sqrt(1.0 - aw_pow(beta2, step)));
+  s.key = aw_hash(seed ^ aw_hash((uint32_t)step));
+}
+
+__device__ __forceinline__ uint32_t aw_wave_max(uint32_t v) {
+  v = umax(v, dpp_xor1(v));
+  v = umax(v, dpp_xor2(v));
+  v = umax(v, dpp_hmirror(v));
+  v = umax(v, dpp_mirror(v));
+  v = umax(v, swz_xor16(v));
+  return umax((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 32));
+}
+
+// E4M3 magnitude code of y >= 0 (at most 448), rounded up with probability (distance to the
+// code below) / step: rnd holds 16 random bits, added below the kept mantissa bits.
+__device__ __forceinline__ uint32_t aw_e4m3_stochastic(float y, uint32_t rnd) {
+  const uint32_t small = (uint32_t)(int)__builtin_floorf(y * 512.0f + (float)rnd * 0x1p-16f);
+  const uint32_t large = ((__float_as_uint(y) + (rnd << 4)) >> 20) - 960u;
+  return umin(y < 0.015625f ? small : large, 0x7Eu);
+}
+
+struct AwScale {
+  float scale, inv;
+};
+__device__ __forceinline__ AwScale aw_block_scale(uint32_t top_bits) {
+  const float top = __uint_as_float(top_bits);
+  const bool dead = top < AW_MIN_MAX;               // false for a NaN: it stays visible in the scale
+  AwScale o;
+  o.scale = dead ? 0.0f : top * (1.0f / 448.0f);
+  o.inv = dead ? 0.0f : 1.0f / o.scale;
+  return o;
+}
+
+// Four consecutive elements of an array with n left from here (n >= 4 in all but a tensor's
+// last lanes); missing ones read as zero.
+__device__ __forceinline__ float4 aw_load4(const float* p, uint32_t left) {
+  if (left >= 4) return *reinterpret_cast<const float4*>(p);
+  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (left > 0) o.x = p[0];
+  if (left > 1) o.y = p[1];
+  if (left > 2) o.z = p[2];
+  return o;
+}
+__device__ __forceinline__ float4 aw_load4(const uint16_t* p, uint32_t left) {
+  uint2 w = {0u, 0u};
+  if (left >= 4) {
+    w = *reinterpret_cast<const uint2*>(p);
+  } else {
+    if (left > 0) w.x = p[0];
+    if (left > 1) w.x |= (uint32_t)p[1] << 16;
+    if (left > 2) w.y = p[2];
+  }
+  return {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+}
+__device__ __forceinline__ uint32_t aw_load4(const uint8_t* p, uint32_t left) {
+  if (left >= 4) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t w = 0;
+  if (left > 0) w = p[0];
+  if (left > 1) w |= (uint32_t)p[1] << 8;
+  if (left > 2) w |= (uint32_t)p[2] << 16;
+  return w;
+}
+__device__ __forceinline__ void aw_store4(float* p, const float (&v)[4], uint32_t left) {
+  if (left >= 4) {
+    *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
+    return;
+  }
+  for (uint32_t i = 0; i < 3; ++i)
+    if (i < left) p[i] = v[i];
+}
+__device__ __forceinline__ void aw_store4(uint16_t* p, const float (&v)[4], uint32_t left) {
+  const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+  if (left >= 4) {
+    *reinterpret_cast<uint2*>(p) = uint2{lo, hi};
+    return;
+  }
+  if (left > 0) p[0] = (uint16_t)lo;
+  if (left > 1) p[1] = (uint16_t)(lo >> 16);
+  if (left > 2) p[2] = (uint16_t)hi;
+}
+__device__ __forceinline__ void aw_store4(uint8_t* p, uint32_t w, uint32_t left) {
+  if (left >= 4) {
+    *reinterpret_cast<uint32_t*>(p) = w;
+    return;
+  }
+  for (uint32_t i = 0; i < 3; ++i)
+    if (i < left) p[i] = (uint8_t)(w >> (8 * i));
+}
+
+template <int BITS, typename G>
+__global__ __launch_bounds__(AW_WG) void k_adamw(AdamwArgs a) {
+  if (a.skip && *a.skip) return;
+  const uint32_t wg = blockIdx.x;
+  int ti = -1;
+#pragma unroll
+  for (int i = 0; i < AW_TENSORS; ++i) ti += wg >= a.begin[i];
+  const AdamwTensor& t = a.t[ti];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * AW_PER_WAVE;   // first block of the wave
+  const uint32_t n = t.n;
+
+  float4 p[AW_PER_WAVE], g[AW_PER_WAVE], m[AW_PER_WAVE], v[AW_PER_WAVE];
+  uint32_t mc[AW_PER_WAVE], vc[AW_PER_WAVE];
+  float ms[AW_PER_WAVE], vs[AW_PER_WAVE];
+#pragma unroll
+  for (int j = 0; j < AW_PER_WAVE; ++j) {
+    const uint32_t at = (b0 + j) * AW_BLOCK + lane * 4;
+    const uint32_t left = at < n ? n - at : 0;
+    p[j] = aw_load4(t.p + at, left);
+    g[j] = aw_load4(static_cast<const G*>(t.g) + at, left);
+    if (BITS == 8) {
+      mc[j] = aw_load4(static_cast<const uint8_t*>(t.m) + at, left);
+      vc[j] = aw_load4(static_cast<const uint8_t*>(t.v) + at, left);
+      const bool in = (b0 + j) * AW_BLOCK < n;
+      ms[j] = in ? t.ms[b0 + j] : 0.0f;
+      vs[j] = in ? t.vs[b0 + j] : 0.0f;
+    } else {
+      m[j] = aw_load4(static_cast<const float*>(t.m) + at, left);
+      v[j] = aw_load4(static_cast<const float*>(t.v) + at, left);
+    }
+  }
+
+  AdamwScalars s = a.s;
+  if (a.d_lr || a.d_step)      // while the loads are in flight
+    aw_scalars(s, a.d_lr ? (double)*a.d_lr : s.lr, a.beta1, a.beta2, a.d_step ? *a.d_step : a.step, a.seed);
+  const float keep = (float)(1.0 - s.lr * t.weight_decay);
+  const float b1 = (float)a.beta1, c1 = (float)(1.0 - a.beta1);
+  const float b2 = (float)a.beta2, c2 = (float)(1.0 - a.beta2);
+  const float eps = (float)a.eps;
+  const float gs = a.d_grad_scale ? *a.d_grad_scale : 1.0f;    // x * 1 is exact
+
+  float ms_out[AW_PER_WAVE], vs_out[AW_PER_WAVE];
+#pragma unroll
+  for (int j = 0; j < AW_PER_WAVE; ++j) {
+    if ((b0 + j) * AW_BLOCK >= n) break;                        // uniform over the wave
+    const uint32_t at = (b0 + j) * AW_BLOCK + lane * 4;
+    const uint32_t left = at < n ? n - at : 0;
+    if (BITS == 8) {
+      const f32x2_t m01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[j], false);
+      const f32x2_t m23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[j], true);
+      const f32x2_t r01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[j], false);
+      const f32x2_t r23 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[j], true);
+      m[j] = float4{m01.x * ms[j], m01.y * ms[j], m23.x * ms[j], m23.y * ms[j]};
+      const float4 r = {r01.x * vs[j], r01.y * vs[j], r23.x * vs[j], r23.y * vs[j]};
+      v[j] = float4{r.x * r.x, r.y * r.y, r.z * r.z, r.w * r.w};
+    }
+    const float pi[4] = {p[j].x, p[j].y, p[j].z, p[j].w}, gi[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+    const float mi[4] = {m[j].x, m[j].y, m[j].z, m[j].w}, vi[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+    float po[4], mo[4], vo[4], ro[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ge = gi[e] * gs;
+      mo[e] = mi[e] * b1 + ge * c1;
+      vo[e] = vi[e] * b2 + (ge * c2) * ge;
+      ro[e] = __builtin_sqrtf(vo[e]);
+      po[e] = pi[e] * keep - (mo[e] / (ro[e] * s.root + eps)) * s.size;
+    }
+    aw_store4(t.p + at, po, left);
+    if (t.p16) aw_store4(t.p16 + at, po, left);
+    if (BITS == 8) {
+      uint32_t mm = 0, rm = 0;                                  // non-negative floats order like their bits
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mm = umax(mm, __float_as_uint(mo[e]) & 0x7FFFFFFFu);
+        rm = umax(rm, __float_as_uint(ro[e]) & 0x7FFFFFFFu);
+      }
+      const AwScale sm = aw_block_scale(aw_wave_max(mm)), sv = aw_block_scale(aw_wave_max(rm));
+      ms_out[j] = sm.scale;
+      vs_out[j] = sv.scale;
+      uint32_t mw = 0, vw = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t h = aw_hash(s.key + at + e);
+        const float my = fminf(__builtin_fabsf(mo[e]) * sm.inv, 448.0f), vy = fminf(ro[e] * sv.inv, 448.0f);
+        uint32_t cm = aw_e4m3_stochastic(my, h & 0xFFFFu), cv = aw_e4m3_stochastic(vy, h >> 16);
+        cm |= mo[e] < 0.0f ? 0x80u : 0u;
+        if (vy > 0.0f) cv = umax(cv, 1u);    // a zero would let the next step divide by a far too small root
+        mw |= cm << (8 * e);
+        vw |= cv << (8 * e);
+      }
+      aw_store4(static_cast<uint8_t*>(t.m) + at, mw, left);
+      aw_store4(static_cast<uint8_t*>(t.v) + at, vw, left);
+    } else {
+      aw_store4(static_cast<float*>(t.m) + at, mo, left);
+      aw_store4(static_cast<float*>(t.v) + at, vo, left);
+    }
+  }
+  if (BITS == 8) {
+    // the wave's scales in one store each
+#pragma unroll
+    for (int j = 0; j < AW_PER_WAVE; ++j) {
+      if ((b0 + j) * AW_BLOCK < n && lane == (uint32_t)j) {
+        t.ms[b0 + j] = ms_out[j];
+        t.vs[b0 + j] = vs_out[j];
+      }
+    }
+  }
+}
+
+uint32_t adamw_chunks(int64_t n) { return (uint32_t)((n + AW_CHUNK - 1) / AW_CHUNK); }
+
+void adamw_host_scalars(AdamwScalars& s, double lr, double beta1, double beta2, int64_t step, uint32_t seed) {
+  aw_scalars(s, lr, beta1, beta2, step, seed);
+}
+
+hipError_t launch_adamw(const AdamwArgs& a, uint32_t grid, int bits, bool g_bf16, hipStream_t s) {
+  if (bits == 8) {
+    if (g_bf16)
+      k_adamw<8, uint16_t><<<grid, AW_WG, 0, s>>>(a);
+    else
+      k_adamw<8, float><<<grid, AW_WG, 0, s>>>(a);
+  } else {
+    if (g_bf16)
+      k_adamw<32, uint16_t><<<grid, AW_WG, 0, s>>>(a);
+    else
+      k_adamw<32, float><<<grid, AW_WG, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace qf
+
+namespace {
+bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) != 0; }
+}  // namespace
+
+extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const qf_adamw_hyper* h,
+                                   void* stream) {
+  if (n < 0 || (state_bits != 32 && state_bits != 8)) return QF_ERR_ARG;
+  if (!h || (n > 0 && !t)) return QF_ERR_NULL;
+  // written so that a NaN fails
+  if (!(h->beta1 >= 0.0 && h->beta1 < 1.0 && h->beta2 >= 0.0 && h->beta2 < 1.0 && h->eps >= 0.0)) return QF_ERR_ARG;
+  if (!h->d_step && h->step < 1) return QF_ERR_ARG;
+  if (!h->d_lr && !(h->lr >= 0.0 && h->lr <= 1e30)) return QF_ERR_ARG;
+  if (misaligned(h->d_lr, 4) || misaligned(h->d_step, 8) || misaligned(h->d_grad_scale, 4) || misaligned(h->d_skip, 4))
+    return QF_ERR_ALIGN;
+  for (int i = 0; i < n; ++i) {
+    const qf_adamw_tensor& d = t[i];
+    if (d.n < 0 || d.n >= (1ll << 31)) return QF_ERR_SHAPE;
+    if (d.g_bf16 != 0 && d.g_bf16 != 1) return QF_ERR_ARG;
+    if (!(d.weight_decay >= 0.0 && d.weight_decay <= 1e30)) return QF_ERR_ARG;
+    if (d.n == 0) continue;
+    if (!d.p || !d.g || !d.m || !d.v) return QF_ERR_NULL;
+    if (state_bits == 8 && (!d.m_scale || !d.v_scale)) return QF_ERR_NULL;
+    if (misaligned(d.p, 16) || misaligned(d.g, 16) || misaligned(d.m, 16) || misaligned(d.v, 16) ||
+        misaligned(d.p16, 16) || misaligned(d.m_scale, 4) || misaligned(d.v_scale, 4))
+      return QF_ERR_ALIGN;
+  }
+  qf::AdamwArgs a;
+  memset(&a, 0, sizeof(a));
+  a.beta1 = h->beta1;
+  a.beta2 = h->beta2;
+  a.eps = h->eps;
+  a.step = h->step;
+  a.seed = h->seed;
+  a.d_lr = h->d_lr;
+  a.d_step = h->d_step;
+  a.d_grad_scale = h->d_grad_scale;
+  a.skip = h->d_skip;
+  qf::adamw_host_scalars(a.s, h->lr, h->beta1, h->beta2, h->step, h->seed);
+  for (int bf = 0; bf < 2; ++bf) {          // one run of launches per gradient type
+    int k = 0;
+    uint32_t grid = 0;
+    for (int i = 0; i <= n; ++i) {
+      if (i < n && t[i].n > 0 && t[i].g_bf16 == bf) {
+        qf::AdamwTensor& o = a.t[k];
+        o.p = t[i].p;
+        o.g = t[i].g;
+        o.m = t[i].m;
+        o.v = t[i].v;
+        o.ms = t[i].m_scale;
+        o.vs = t[i].v_scale;
+        o.p16 = t[i].p16;
+        o.n = (uint32_t)t[i].n;
+        o.weight_decay = t[i].weight_decay;
+        a.begin[k++] = grid;
+        grid += qf::adamw_chunks(t[i].n);
+      }
+      if (k == qf::AW_TENSORS || (i == n && k > 0)) {
+        for (int j = k; j < qf::AW_TENSORS; ++j) a.begin[j] = 0xFFFFFFFFu;   // no workgroup reaches these
+        const hipError_t e = qf::launch_adamw(a, grid, state_bits, bf == 1, (hipStream_t)stream);
+        if (e != hipSuccess) return qf::status_of(e);
+        k = 0;
+        grid = 0;
+      }
+    }
+  }
+  return QF_OK;
+}

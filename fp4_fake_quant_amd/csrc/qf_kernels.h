@@ -125,6 +125,42 @@ hipError_t launch_lora_merge(const LoraArgs& a, int grid, hipStream_t s);
 hipError_t launch_lora_merge_qdq(const LoraArgs& a, int grid, hipStream_t s);
 hipError_t launch_lora_grads(const LoraArgs& a, int grid, int accumulate, hipStream_t s);
 
+// ----------------------------------------------------------------- AdamW ---
+constexpr int AW_TENSORS = 48;      // tensors per launch: the descriptors stay below 4 KiB of kernel arguments
+
+struct AdamwTensor {
+  float* p;
+  const void* g;          // fp32 or bf16
+  void* m;                // fp32, or E4M3 codes with a scale per block in ms
+  void* v;                // fp32, or E4M3 codes of sqrt(v) with a scale per block in vs
+  float* ms;
+  float* vs;
+  uint16_t* p16;          // bf16 copy of p (null: none)
+  double weight_decay;
+  uint32_t n;
+};
+
+// What follows from the learning rate and the step number.
+struct AdamwScalars {
+  double lr;
+  float size;             // lr / (1 - beta1^step)
+  float root;             // 1 / sqrt(1 - beta2^step)
+  uint32_t key;           // of the stochastic rounding's hash
+};
+
+struct AdamwArgs {
+  AdamwTensor t[AW_TENSORS];
+  uint32_t begin[AW_TENSORS];   // first workgroup of each tensor; 0xFFFFFFFF past the last
+  double beta1, beta2, eps;
+  int64_t step;
+  uint32_t seed;
+  AdamwScalars s;               // used unless d_lr or d_step is given
+  const float* d_lr;
+  const int64_t* d_step;
+  const float* d_grad_scale;
+  const uint32_t* skip;
+};
+
 // Workgroups of the amax pass for a launch with `tiles` tiles of 256 * L_AMAX chunks.
 inline int amax_grid(int tiles) { return tiles < AMAX_GRID ? tiles : AMAX_GRID; }
 hipError_t launch_nvfp4_amax(const QArgs& a, hipStream_t s);

@@ -392,6 +392,68 @@ qf_status qf_lora_experts_merge_qdq_pack_nvfp4(const qf_lora_experts* e, int n, 
 qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int accumulate, void* ws, size_t ws_bytes,
                                         void* stream);
 
+/* -------------------------------------------------------------- AdamW ---- */
+/* One AdamW step over any number of tensors: the update of the continuous latent weights
+ * ("Method", "Framework overview") or of the adapters from the gradients that
+ * qf_ste_backward*, qf_linear_backward_mxfp4 and the adapter-gradient calls write.  The
+ * optional bf16 copy is what the next tensor-scale / QDQ / merge call reads.
+ *
+ * Per tensor, n elements (n < 2^31; 0 is skipped), every array contiguous:
+ *   p    fp32 weights, updated in place;  p16  bf16 copy of the new p, or NULL
+ *   g    gradient, fp32, or bf16 when g_bf16 is 1 (read only)
+ *   m, v moments, updated in place.  state_bits 32: fp32.  state_bits 8: E4M3 bytes of m
+ *        and of sqrt(v), element i in block i / QF_ADAMW_BLOCK with the fp32 scales
+ *        m_scale, v_scale [ceil(n / QF_ADAMW_BLOCK)]: m = code * m_scale,
+ *        v = (code * v_scale)^2.  All-zero bytes and scales start a run.
+ * Hyperparameters: step counts from 1.  d_lr (device float) and d_step (device int64)
+ * replace lr and step when not NULL, so that a captured step follows them on every replay
+ * (a device step below 1 counts as 1).  d_grad_scale (device float, or NULL) multiplies
+ * every gradient first (clipping, loss scale).  d_skip (device uint32, or NULL): nothing is
+ * written when it is not 0 when the kernel runs (e.g. a non-finite flag).  seed: of the
+ * stochastic rounding below (8-bit states only).
+ *
+ * Arithmetic, one fp32 rounding per operation, factors rounded once from 64 bits:
+ *   g = g * *d_grad_scale;  m' = m*b1 + g*(1-b1);  v' = v*b2 + (g*(1-b2))*g;
+ *   p' = p*(1 - lr*weight_decay) - (m' / (sqrt(v') * (1/sqrt(1-b2^t)) + eps)) * (lr/(1-b1^t));
+ *   p16 = bf16(p') (RNE).
+ * 8-bit states of a block, with x = m' or sqrt(v') and a = max |x| over its elements:
+ *   scale = a * fl(1/448), or 0 (and all codes 0) when a < 2^-100;  y = min(|x| * fl(1/scale), 448);
+ *   code: y rounded stochastically onto E4M3: with u = 16 random bits, below 2^-6
+ *   floor(fl(512 y + u 2^-16)), else the fp32 bits of y plus u * 16, truncated to 3 mantissa
+ *   bits.  sqrt(v') > 0 never gets code 0 (it would leave the next step's divisor near
+ *   eps).  m's sign is the code's top bit.  u = the low (m) or high (v) half of
+ *   H((key + i) mod 2^32) for element i of its tensor, key = H(seed ^ H(step mod 2^32)), with
+ *   H(x): x ^= x>>16; x *= 0x7FEB352D; x ^= x>>15; x *= 0x846CA68B; x ^= x>>16 (mod 2^32).
+ *   Same inputs, step and seed, same bits, however the tensors are grouped into calls.
+ * All arrays 16-byte aligned, scales and device scalars 4-byte (d_step 8-byte) aligned
+ * (QF_ERR_ALIGN).  QF_ERR_ARG: n < 0, state_bits not 8 or 32, g_bf16 not 0 or 1, a beta outside
+ * [0, 1), negative or NaN lr / eps / weight_decay, step < 1 without d_step.  QF_ERR_SHAPE: a
+ * size outside [0, 2^31).  A tensor may appear once per call; arrays must not overlap.
+ * Launches: one per 48 tensors (and per gradient type), no workspace. */
+#define QF_ADAMW_BLOCK 256
+typedef struct qf_adamw_tensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  uint16_t* p16;
+  int64_t n;
+  double weight_decay;
+  int32_t g_bf16;
+} qf_adamw_tensor;
+typedef struct qf_adamw_hyper {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* d_lr;
+  const int64_t* d_step;
+  const float* d_grad_scale;
+  const uint32_t* d_skip;
+  uint32_t seed;
+} qf_adamw_hyper;
+qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const qf_adamw_hyper* h, void* stream);
+
 /* ------------------------------------------------------------ dequant ---- */
 /* Packed engine layout -> BF16, the inverse direction of the pack calls ("Method":
  * weights leave training in the engine's own format; "Supported formats" table for

@@ -28,10 +28,11 @@ mxfp4       block-32 QDQ with a shared power-of-two scale, pack/unpack
 q4k         256-element super-blocks of eight 32-element sub-blocks, pack/unpack
 ste         straight-through estimator backward
 lora        LoRA merge (W + B.A) and adapter gradients (float64)
+adamw       AdamW step, fp32 states and stochastically rounded E4M3 block states
 gemm        float64 reference for Y = QDQ(X) . QDQ(W)^T and its error bound
 
 Parity status of each function is listed in the module docstrings.  Functions
 with no independent pin say "parity unpinned".
 """
 
-from . import primitives, nvfp4, mxfp4, q4k, ste, lora, gemm  # noqa: F401
+from . import primitives, nvfp4, mxfp4, q4k, ste, lora, gemm, adamw  # noqa: F401
