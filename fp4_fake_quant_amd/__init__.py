@@ -515,8 +515,8 @@ def qf_lora_adapter_grads(G, A, B, dA=None, dB=None, accumulate=False, ws=None):
     return dA, dB
 
 
-# --------------------------------------------------------------- AdamW ----
-ADAMW_BLOCK = 256
+# ---------------------------------------------------------------- rows ----
+ROW_TILE, ROW_MAX_IDS = 32, 1024
 
 
 def _same_gpu(*tensors):
@@ -539,6 +539,100 @@ def _on(dev):
     if dev is None or dev.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(dev)
+
+
+def _ids(t, name):
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    return t
+
+
+class RowPlan:
+    """Rows grouped by id (qf_row_plan): offsets [n_ids + 1], order [n] and tiles [t, 2], int32
+    on the device, for n rows with ids in [0, n_ids)."""
+
+    def __init__(self, n, n_ids, device):
+        self.n, self.n_ids, self.device = n, n_ids, device
+        t = lib().qf_row_plan_tiles(n, n_ids)
+        self.offsets = torch.empty(n_ids + 1, dtype=torch.int32, device=device)
+        self.order = torch.empty(n, dtype=torch.int32, device=device)
+        self.tiles = torch.empty((t, 2), dtype=torch.int32, device=device)
+
+
+def qf_row_plan(ids, n_ids, plan=None, ws=None):
+    """The RowPlan of ids (int32 device tensor, any shape; row i is element i in memory order):
+    rows with an id outside [0, n_ids) are in no group.  plan: one of the same n and n_ids to
+    write into."""
+    dev, n, n_ids = _same_gpu(_ids(ids, "ids"), ws), ids.numel(), int(n_ids)
+    if plan is None:
+        if not 1 <= n_ids <= ROW_MAX_IDS:
+            raise ValueError(f"n_ids is 1..{ROW_MAX_IDS}")
+        plan = RowPlan(n, n_ids, dev)
+    elif plan.n != n or plan.n_ids != n_ids or plan.device != dev:
+        raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} ids on {plan.device}")
+    need = lib().qf_row_plan_workspace(n, n_ids)
+    with _on(dev):
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().qf_row_plan(_p(ids), n, n_ids, _p(plan.offsets), _p(plan.order), _p(plan.tiles), _p(ws),
+                                 ws.numel() * ws.element_size() if ws is not None else 0, _stream()), "qf_row_plan")
+    return plan
+
+
+# ------------------------------------- adapters of many requests at once ----
+def qf_lora_apply_workspace(rows, K, r, n_adapters, planned=False):
+    return lib().qf_lora_apply_workspace(int(rows), int(K), int(r), int(n_adapters), int(bool(planned)))
+
+
+def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
+    plan = where if isinstance(where, RowPlan) else None
+    dev = _same_gpu(X, A, B, Y, scale, ws, *((plan.order,) if plan else (where,)))
+    xrows, K, ldx = _mat(_bf16(X, "X"), "X")
+    rows, N, ldy = _mat(_bf16(Y, "Y"), "Y")
+    for t, what in ((A, "A"), (B, "B")):
+        if _bf16(t, what).dim() != 3 or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous 3-D tensor [adapters, ...]")
+    E, r = A.shape[0], A.shape[1]
+    if A.shape[2] != K or tuple(B.shape) != (E, N, r):
+        raise ValueError(f"adapter shapes {tuple(A.shape)}, {tuple(B.shape)} do not fit X {tuple(X.shape)}, Y {tuple(Y.shape)}")
+    rows_per_x = int(rows_per_x)
+    if rows_per_x < 1 or xrows != (rows + rows_per_x - 1) // rows_per_x:
+        raise ValueError(f"X has {xrows} rows for {rows} rows of Y and rows_per_x={rows_per_x}")
+    if scale is not None and (scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() != E):
+        raise ValueError("scale must be a contiguous float32 tensor with a value per adapter")
+    if plan is not None and (plan.n != rows or plan.n_ids > E):
+        raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} adapters")
+    if plan is None and _ids(where, "ids").numel() != rows:
+        raise ValueError("ids must hold an id per row of Y")
+    with _on(dev):
+        if ws is None:
+            ws = torch.empty(max(lib().qf_lora_apply_workspace(rows, K, r, E, int(plan is not None)), 1),
+                             dtype=torch.uint8, device=dev)
+        tail = (_p(Y), ldy, rows, N, K, r, _p(ws), ws.numel() * ws.element_size(), _stream())
+        head = (_p(X), ldx, rows_per_x, _p(A), _p(B), _p(scale), E)
+        if plan is None:
+            st = lib().qf_lora_apply(*head, _p(where), *tail)
+        else:
+            st = lib().qf_lora_apply_planned(*head, _p(plan.offsets), _p(plan.order), _p(plan.tiles), plan.n_ids, *tail)
+        _check(st, name)
+    return Y
+
+
+def qf_lora_apply(X, A, B, ids, Y, scale=None, rows_per_x=1, ws=None):
+    """Y[i] += scale[e] * B[e] (A[e] X[i // rows_per_x]), e = ids[i] (none outside [0, E)), in
+    place: X [rows / rows_per_x, K], A [E, r, K], B [E, N, r], Y [rows, N] bf16, ids int32."""
+    return _lora_apply("qf_lora_apply", X, A, B, ids, Y, scale, rows_per_x, ws)
+
+
+def qf_lora_apply_planned(X, A, B, plan, Y, scale=None, rows_per_x=1, ws=None):
+    """qf_lora_apply with the RowPlan of the rows' ids, which serves every projection of a batch."""
+    if not isinstance(plan, RowPlan):
+        raise TypeError("plan must be a RowPlan")
+    return _lora_apply("qf_lora_apply_planned", X, A, B, plan, Y, scale, rows_per_x, ws)
+
+
+# --------------------------------------------------------------- AdamW ----
+ADAMW_BLOCK = 256
 
 
 def _flat(t, name, dtype, n):

@@ -137,6 +137,15 @@ SIGNATURES = {
                                               c_void_p]),
     "qf_linear_forward_mxfp4": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_i64, c_i64, c_i64, c_i64,
                                         ctypes.c_uint, c_void_p, c_i64, c_void_p, c_i64, c_void_p]),
+    "qf_row_plan_tiles": (c_i64, [c_i64, c_int]),
+    "qf_row_plan_workspace": (c_size_t, [c_i64, c_int]),
+    "qf_row_plan": (c_int, [c_void_p, c_i64, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qf_lora_apply_workspace": (c_size_t, [c_i64, c_i64, c_int, c_int, c_int]),
+    "qf_lora_apply": (c_int, [c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_i64,
+                              c_i64, c_i64, c_i64, c_int, c_void_p, c_size_t, c_void_p]),
+    "qf_lora_apply_planned": (c_int, [c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
+                                      c_void_p, c_int, c_void_p, c_i64, c_i64, c_i64, c_i64, c_int, c_void_p, c_size_t,
+                                      c_void_p]),
     "qf_adamw_step": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
     "qf_noalloc_scratch_bytes": (c_size_t, []),
     "qf_nvfp4_tensor_scale_grouped_noalloc": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p]),

@@ -161,6 +161,44 @@ struct AdamwArgs {
   const uint32_t* skip;
 };
 
+// -------------------------------------------------------------- row plan ---
+constexpr int RP_ONE = 4096;          // rows that one workgroup plans alone (one launch)
+constexpr int RP_MAX_WG = 64;         // workgroups of larger plans (each sums all of their counts)
+constexpr int RP_MIN_PER_WG = 2048;   // rows per workgroup of larger plans, at least
+
+struct RowPlanArgs {
+  const int32_t* ids;
+  int64_t n, per;          // rows, and rows per workgroup
+  int32_t n_ids;
+  int32_t* offsets;        // [n_ids + 1]
+  int32_t* order;          // [n]
+  int32_t* tiles;          // [n_tiles][2]
+  int64_t n_tiles;
+  uint32_t* hist;          // workspace [workgroups][n_ids]
+};
+hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
+
+// ------------------------------------------------- adapters beside a product ---
+constexpr int LORA_APPLY_ROW_FORM = 64;     // rows up to which a call without a plan goes row by row
+constexpr int LORA_APPLY_MAX_SPLITS = 8;    // K parts
+
+struct LoraApplyArgs {
+  const uint16_t* X;
+  const uint16_t* A;        // [n_adapters][r][K]
+  const uint16_t* B;        // [n_adapters][N][r]
+  const float* scale;       // [n_adapters] (null: 1)
+  uint16_t* Y;
+  int64_t ldx, ldy;
+  const int32_t* ids;       // rows form
+  const int32_t* offsets;   // tiles form: the row plan
+  const int32_t* order;
+  const int32_t* tiles;
+  float* S;                 // workspace [splits][rows][r]; by row (rows form) or position (tiles form)
+  int32_t rows, rows_per_x, K, N, r, n_adapters, n_ids, splits, n_part;
+};
+int lora_apply_splits(bool tiles, int64_t units, int K, int r);
+hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipStream_t s);
+
 // Workgroups of the amax pass for a launch with `tiles` tiles of 256 * L_AMAX chunks.
 inline int amax_grid(int tiles) { return tiles < AMAX_GRID ? tiles : AMAX_GRID; }
 hipError_t launch_nvfp4_amax(const QArgs& a, hipStream_t s);

@@ -392,6 +392,61 @@ qf_status qf_lora_experts_merge_qdq_pack_nvfp4(const qf_lora_experts* e, int n, 
 qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int accumulate, void* ws, size_t ws_bytes,
                                         void* stream);
 
+/* --------------------------------------------------------------- rows ---- */
+/* Row plan: groups rows by an id, keeping their order inside a group.  ids: device
+ * int32[n], row i's id in [0, n_ids); any other value (e.g. -1: a request without an
+ * adapter, a padded row, an expert slot that routing left empty) belongs to no group.
+ *   offsets  device int32[n_ids + 1]: group e is order[offsets[e] .. offsets[e + 1]);
+ *   order    device int32[n]: row numbers, ascending inside a group; -1 behind the last;
+ *   tiles    device int32[qf_row_plan_tiles(n, n_ids)][2], 8-byte aligned: {group, first
+ *            position in order} of every run of up to QF_ROW_TILE rows of one group, groups
+ *            ascending; {-1, 0} behind the last.
+ * A plan serves every call over the same rows (all projections of all layers).  0 <= n <
+ * QF_ROW_MAX_ROWS (QF_ERR_SHAPE), 1 <= n_ids <= QF_ROW_MAX_IDS (QF_ERR_ARG).  n == 0 writes
+ * zero offsets.  ws: qf_row_plan_workspace bytes (0 for small plans).  One or two launches;
+ * outputs do not depend on scheduling. */
+#define QF_ROW_TILE 32
+#define QF_ROW_MAX_IDS 1024
+#define QF_ROW_MAX_ROWS (1 << 30)
+int64_t qf_row_plan_tiles(int64_t n, int n_ids);          /* 0 for invalid arguments */
+size_t qf_row_plan_workspace(int64_t n, int n_ids);
+qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* -------------------------------------- adapters of many requests at once ---- */
+/* Y[i] += scale[e] * B_e (A_e X[i / rows_per_x]) for every row i of Y, e the adapter of row
+ * i: the unmerged adapters beside a projection that all rows share (a rollout batch whose
+ * requests use different adapters over one packed weight; Y is that product's output, e.g.
+ * of qf_gemm_mxfp4_packed).  A bf16 [n_adapters][r][K] and B bf16 [n_adapters][N][r] are the
+ * stacked adapters of the qf_lora_experts_* calls, d_scale a device float[n_adapters] (NULL:
+ * all 1).  Rows without an adapter keep their bits.
+ *   qf_lora_apply          ids device int32[rows]; an id outside [0, n_adapters) has none.
+ *   qf_lora_apply_planned  a qf_row_plan of the rows (n_ids <= n_adapters groups; its order,
+ *                          offsets and tiles for exactly `rows` rows), for callers that apply
+ *                          adapters at several projections of one batch.
+ * rows_per_x: consecutive rows of Y that share a row of X (1, or the routed experts per token
+ * when row t * k + j stands for expert j of token t); X has ceil(rows / rows_per_x) rows.
+ * S = A_e x is accumulated in fp32; Y's row is added in fp32 and rounded once:
+ *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) ((gamma_{K+12} + gamma_{2r+34} + 2^-17) P + gamma_{2r+34} |y0|),
+ *   P = |scale| sum_k |B| sum |A| |x|, gamma_n = n 2^-24 / (1 - n 2^-24).
+ * The order of the sums is fixed for given sizes: same inputs, same bits.
+ * Limits: r in 1..QF_LORA_APPLY_MAX_R, n_adapters in 1..QF_ROW_MAX_IDS, rows_per_x >= 1
+ * (QF_ERR_ARG); K a positive multiple of 8 and N >= 1, both below 2^22, rows in [0, 2^24),
+ * ldx >= K, ldy >= N (QF_ERR_SHAPE).  X and A 16-byte aligned, ldx a multiple of 8, B and Y
+ * 2-byte (QF_ERR_ALIGN); fastest with r a multiple of 8, B and Y 16-byte aligned and ldy a
+ * multiple of 8.  ws: qf_lora_apply_workspace bytes, 16-byte aligned, not shared by calls
+ * that may overlap.  No array may overlap Y.  Two launches, up to four without a plan. */
+#define QF_LORA_APPLY_MAX_R 128
+#define QF_LORA_APPLY_MAX_ROWS (1 << 24)
+size_t qf_lora_apply_workspace(int64_t rows, int64_t K, int r, int n_adapters, int planned);
+qf_status qf_lora_apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16_t* A, const uint16_t* B,
+                        const float* d_scale, int n_adapters, const int32_t* ids, uint16_t* Y, int64_t ldy,
+                        int64_t rows, int64_t N, int64_t K, int r, void* ws, size_t ws_bytes, void* stream);
+qf_status qf_lora_apply_planned(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16_t* A,
+                                const uint16_t* B, const float* d_scale, int n_adapters, const int32_t* offsets,
+                                const int32_t* order, const int32_t* tiles, int n_ids, uint16_t* Y, int64_t ldy,
+                                int64_t rows, int64_t N, int64_t K, int r, void* ws, size_t ws_bytes, void* stream);
+
 /* -------------------------------------------------------------- AdamW ---- */
 /* One AdamW step over any number of tensors: the update of the continuous latent weights
  * ("Method", "Framework overview") or of the adapters from the gradients that

@@ -1,0 +1,193 @@
+"""qf_row_plan and qf_lora_apply on the GPU against the oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp4_fake_quant_amd as fq
+from oracle import primitives as prim
+from oracle import rows
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+
+def ids_of(n, n_ids, seed, none=0.1, runs=False):
+    rng = np.random.default_rng(seed)
+    ids = np.sort(rng.integers(0, n_ids, n)) if runs else rng.integers(0, n_ids, n)
+    ids = np.where(rng.random(n) < none, rng.choice([-1, -7, n_ids, 2 ** 31 - 1], n), ids)
+    return ids.astype(np.int32)
+
+
+def check_plan(ids, n_ids):
+    p = fq.qf_row_plan(torch.from_numpy(ids).cuda(), n_ids)
+    for got, want, name in zip((p.offsets, p.order, p.tiles), rows.plan(ids, n_ids), ("offsets", "order", "tiles")):
+        assert np.array_equal(got.cpu().numpy(), want), f"{name}, n={ids.size}, n_ids={n_ids}"
+    return p
+
+
+@pytest.mark.parametrize("n", [0, 1, 31, 64, 65, 511, 513, 4096, 4097, 6000, 131072, 140001])
+@pytest.mark.parametrize("n_ids", [1, 2, 5, 128, 1000, 1024])
+def test_plan(n, n_ids):
+    check_plan(ids_of(n, n_ids, n + n_ids, runs=n % 2 == 1), n_ids)
+
+
+@pytest.mark.parametrize("n", [70, 9000])
+def test_plan_one_group_and_none(n):
+    check_plan(np.full(n, 3, np.int32), 5)
+    check_plan(np.full(n, -1, np.int32), 5)
+    a = np.full(n, -1, np.int32)
+    a[-1] = 4
+    check_plan(a, 5)
+
+
+def bf(rng, shape, scale=1.0):
+    return prim.f32_to_bf16((rng.standard_normal(shape) * scale).astype(np.float32))
+
+
+def case(T, K, N, r, E, seed, none=0.1, per=1, ldx=None, ldy=None, runs=False):
+    rng = np.random.default_rng(seed)
+    c = dict(X=bf(rng, (-(-T // per), K)), A=bf(rng, (E, r, K), K ** -0.5), B=bf(rng, (E, N, r), 0.2), Y=bf(rng, (T, N)),
+             scale=(rng.random(E) + 0.5).astype(np.float32), ids=ids_of(T, E, seed + 1, none, runs), per=per)
+    ldx, ldy = ldx or K, ldy or N
+    d = dict(A=dev(c["A"]), B=dev(c["B"]), scale=torch.from_numpy(c["scale"]).cuda(), ids=torch.from_numpy(c["ids"]).cuda())
+    d["X"] = torch.full((c["X"].shape[0], ldx), float("nan"), dtype=torch.bfloat16, device="cuda")[:, :K]
+    d["X"].copy_(dev(c["X"]))
+    d["Yfull"] = torch.full((T, ldy), 7.0, dtype=torch.bfloat16, device="cuda")
+    d["Y"] = d["Yfull"][:, :N]
+    d["Y"].copy_(dev(c["Y"]))
+    return c, d
+
+
+def check_apply(c, d, planned, scaled=True):
+    K, N, r = c["X"].shape[1], c["Y"].shape[1], c["A"].shape[1]
+    f = prim.bf16_to_f32
+    scale = c["scale"] if scaled else None
+    y, P, y0 = rows.apply(f(c["X"]), f(c["A"]), f(c["B"]), c["ids"], f(c["Y"]), scale, c["per"])
+    d["Y"].copy_(dev(c["Y"]))
+    kw = dict(scale=d["scale"] if scaled else None, rows_per_x=c["per"])
+    if planned:
+        plan = fq.qf_row_plan(d["ids"], c["A"].shape[0])
+        fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], plan, d["Y"], **kw)
+    else:
+        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], **kw)
+    got = host(d["Y"])
+    err = np.abs(f(got).astype(np.float64) - y)
+    bound = rows.apply_bound(y, P, y0, K, r)
+    assert np.all(err <= bound), f"worst {np.max(err / np.maximum(bound, 1e-300))} of the bound"
+    none = (c["ids"] < 0) | (c["ids"] >= c["A"].shape[0])
+    assert np.array_equal(got[none], c["Y"][none])
+    if d["Yfull"].shape[1] > N:
+        assert bool((d["Yfull"][:, N:] == 7.0).all())
+    return got
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("T,K,N,r,E", [
+    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (65, 2056, 300, 16, 9),
+    (33, 256, 64, 32, 1), (100, 520, 130, 33, 2), (97, 128, 257, 64, 5), (200, 200, 72, 128, 3), (130, 64, 40, 100, 40),
+    (300, 96, 2000, 8, 1000), (1000, 1024, 96, 4, 7)])
+def test_apply(T, K, N, r, E, planned):
+    c, d = case(T, K, N, r, E, T + r)
+    got = check_apply(c, d, planned)
+    assert np.array_equal(check_apply(c, d, planned), got)                 # the same bits again
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("T", [40, 700])
+def test_apply_strides_runs_no_scale(T, planned):
+    c, d = case(T, 320, 136, 16, 6, 5, ldx=336, ldy=144, runs=True)
+    check_apply(c, d, planned, scaled=False)
+    c, d = case(T, 320, 133, 16, 6, 6, ldx=328, ldy=135)                   # Y rows of 2-byte alignment
+    check_apply(c, d, planned)
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("T", [48, 1200])
+def test_apply_token_expert_pairs(T, planned):
+    """Rows t * k + j of Y share X's row t."""
+    c, d = case(T, 256, 192, 16, 32, 8, per=8)
+    check_apply(c, d, planned)
+    c, d = case(T + 3, 256, 192, 16, 32, 9, per=8)                         # a last row of X with fewer
+    check_apply(c, d, planned)
+
+
+@pytest.mark.parametrize("planned", [False, True])
+def test_apply_all_and_none(planned):
+    for T in (20, 300):
+        c, d = case(T, 128, 96, 16, 4, 10, none=1.1)
+        check_apply(c, d, planned)
+        c, d = case(T, 128, 96, 16, 4, 11, none=0.0)
+        c["ids"][:] = 2
+        d["ids"].fill_(2)
+        check_apply(c, d, planned)
+
+
+def test_rows_without_adapter_are_not_read():
+    """NaN in the X rows of requests without an adapter reaches nothing."""
+    for T in (30, 500):
+        c, d = case(T, 128, 96, 16, 4, 12, none=0.5)
+        none = torch.from_numpy((c["ids"] < 0) | (c["ids"] >= 4)).cuda()
+        d["X"][none] = float("nan")
+        check_apply(c, d, False)
+        check_apply(c, d, True)
+
+
+def test_forms_agree_with_a_prefix():
+    """A plan of fewer ids than adapters, and an empty batch."""
+    c, d = case(200, 128, 96, 16, 6, 13, none=0.0)
+    c["ids"] %= 4
+    d["ids"] %= 4
+    plan = fq.qf_row_plan(d["ids"], 4)
+    fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], plan, d["Y"], scale=d["scale"])
+    got = host(d["Y"])
+    assert np.array_equal(got, check_apply(c, d, True))
+    e = torch.empty((0, 96), dtype=torch.bfloat16, device="cuda")
+    fq.qf_lora_apply(torch.empty((0, 128), dtype=torch.bfloat16, device="cuda"), d["A"], d["B"],
+                     torch.empty(0, dtype=torch.int32, device="cuda"), e)
+
+
+@pytest.mark.parametrize("T", [24, 5000])
+def test_graph_replays(T):
+    """Plan and adapters captured once; ids, X and Y change between replays."""
+    E = 5
+    _, d = case(T, 256, 160, 16, E, 14)
+    ws = torch.empty(fq.qf_lora_apply_workspace(T, 256, 16, E), dtype=torch.uint8, device="cuda")
+
+    def step():
+        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], scale=d["scale"], ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (21, 22, 23):
+        c, n = case(T, 256, 160, 16, E, seed, runs=seed == 22)
+        for k in ("X", "ids", "Y", "A", "B", "scale"):
+            d[k].copy_(n[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        got = host(d["Y"])
+        assert np.array_equal(got, check_apply(c, n, False))
+
+
+def test_binding_checks():
+    _, d = case(10, 64, 40, 8, 4, 1)
+    with pytest.raises(ValueError):
+        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"][:9], d["Y"])
+    with pytest.raises(ValueError):
+        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], rows_per_x=2)
+    with pytest.raises(ValueError):
+        fq.qf_lora_apply(d["X"], d["A"][:3], d["B"], d["ids"], d["Y"])
+    with pytest.raises(ValueError):
+        fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], fq.qf_row_plan(d["ids"], 5), d["Y"])
+    with pytest.raises(TypeError):
+        fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], d["ids"], d["Y"])
+    with pytest.raises(ValueError):
+        fq.qf_row_plan(d["ids"], 1025)
+    with pytest.raises(fq.QFError):
+        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
