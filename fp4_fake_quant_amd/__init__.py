@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from ._lib import AdamwHyper, AdamwTensor, GgufTensor, LoraDesc, LoraExpertsDesc, StTensor, TensorDesc, lib
+from ._lib import AdamwHyper, AdamwTensor, GgufTensor, LoraDesc, LoraExpertsDesc, RouteDesc, StTensor, TensorDesc, lib
 
 QF_OK = 0
 QF_QDQ_A, QF_QDQ_W, QF_FP4_CORES, QF_MX_NOCLIP = 1, 2, 4, 8
@@ -515,8 +515,11 @@ def qf_lora_adapter_grads(G, A, B, dA=None, dB=None, accumulate=False, ws=None):
     return dA, dB
 
 
-# ---------------------------------------------------------------- rows ----
-ROW_TILE, ROW_MAX_IDS = 32, 1024
+# ------------------------------------------------------------- routing ----
+QF_ROUTE_SOFTMAX, QF_ROUTE_SIGMOID = 0, 1
+QF_ROUTE_GROUP_MAX, QF_ROUTE_GROUP_TOP2 = 0, 1
+_SCORING = {"softmax": QF_ROUTE_SOFTMAX, "sigmoid": QF_ROUTE_SIGMOID, 0: 0, 1: 1}
+_GROUP_RULE = {"max": QF_ROUTE_GROUP_MAX, "top2": QF_ROUTE_GROUP_TOP2, 0: 0, 1: 1}
 
 
 def _same_gpu(*tensors):
@@ -539,6 +542,69 @@ def _on(dev):
     if dev is None or dev.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(dev)
+
+
+def _route_desc(logits, k, scoring, renorm, scale):
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be float32 or bfloat16")
+    if scoring not in _SCORING:
+        raise ValueError("scoring is 'softmax' or 'sigmoid'")
+    T, E, ld = _mat(logits, "logits")
+    d = RouteDesc()
+    d.logits, d.tokens, d.ld, d.experts, d.k = logits.data_ptr(), T, ld, E, int(k)
+    d.logits_bf16, d.scoring, d.renorm = int(logits.dtype == torch.bfloat16), _SCORING[scoring], int(bool(renorm))
+    d.scale, d.n_group, d.topk_group = float(scale), 1, 1
+    return d, T, E
+
+
+def _dense(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    return t
+
+
+def qf_moe_route(logits, k, scoring="softmax", bias=None, n_group=1, topk_group=1, group_rule="max", renorm=True,
+                 scale=1.0, indices=None, weights=None):
+    """(indices int32 [T, k], weights float32 [T, k]) of the k experts of every row of logits
+    [T, E] (float32 or bfloat16): scoring "softmax" or "sigmoid", chosen by score + bias (float32
+    [E]) within the topk_group best of n_group groups (ranked by "max" or "top2"), weights =
+    scores (over their sum when renorm) * scale."""
+    d, T, E = _route_desc(logits, k, scoring, renorm, scale)
+    if group_rule not in _GROUP_RULE:
+        raise ValueError("group_rule is 'max' or 'top2'")
+    dev = _same_gpu(logits, bias, indices, weights)
+    if bias is not None:
+        d.bias = _dense(bias, "bias", torch.float32, (E,)).data_ptr()
+    d.n_group, d.topk_group, d.group_rule = int(n_group), int(topk_group), _GROUP_RULE[group_rule]
+    with _on(dev):
+        if indices is None:
+            indices = torch.empty((T, max(d.k, 0)), dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty((T, max(d.k, 0)), dtype=torch.float32, device=dev)
+        _dense(indices, "indices", torch.int32, (T, d.k))
+        _dense(weights, "weights", torch.float32, (T, d.k))
+        _check(lib().qf_moe_route(ctypes.byref(d), _p(indices), _p(weights), _stream()), "qf_moe_route")
+    return indices, weights
+
+
+def qf_moe_route_backward(logits, indices, d_weights, scoring="softmax", renorm=True, scale=1.0, d_logits=None):
+    """d_logits [T, E] (logits' type) from d_weights float32 [T, k] for the forward's indices."""
+    d, T, E = _route_desc(logits, indices.shape[1] if indices.dim() == 2 else 0, scoring, renorm, scale)
+    dev = _same_gpu(logits, indices, d_weights, d_logits)
+    _dense(indices, "indices", torch.int32, (T, d.k))
+    _dense(d_weights, "d_weights", torch.float32, (T, d.k))
+    with _on(dev):
+        if d_logits is None:
+            d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        if d_logits.dtype != logits.dtype or tuple(d_logits.shape) != (T, E):
+            raise ValueError("d_logits must have the logits' shape and type")
+        _check(lib().qf_moe_route_backward(ctypes.byref(d), _p(indices), _p(d_weights), _p(d_logits),
+                                           _mat(d_logits, "d_logits")[2], _stream()), "qf_moe_route_backward")
+    return d_logits
+
+
+# ---------------------------------------------------------------- rows ----
+ROW_TILE, ROW_MAX_IDS = 32, 1024
 
 
 def _ids(t, name):

@@ -58,6 +58,14 @@ class GgufTensor(ctypes.Structure):
                 ("type", ctypes.c_uint32), ("data", c_void_p), ("nbytes", ctypes.c_uint64)]
 
 
+class RouteDesc(ctypes.Structure):
+    """Mirror of qf_route_desc in include/qf.h."""
+    _fields_ = [("logits", c_void_p), ("tokens", c_i64), ("ld", c_i64), ("bias", c_void_p),
+                ("scale", ctypes.c_float), ("logits_bf16", ctypes.c_int32), ("experts", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("scoring", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_rule", ctypes.c_int32)]
+
+
 class AdamwTensor(ctypes.Structure):
     """Mirror of qf_adamw_tensor in include/qf.h."""
     _fields_ = [("p", c_void_p), ("g", c_void_p), ("m", c_void_p), ("v", c_void_p),
@@ -137,6 +145,8 @@ SIGNATURES = {
                                               c_void_p]),
     "qf_linear_forward_mxfp4": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_i64, c_i64, c_i64, c_i64,
                                         ctypes.c_uint, c_void_p, c_i64, c_void_p, c_i64, c_void_p]),
+    "qf_moe_route": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p]),
+    "qf_moe_route_backward": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_i64, c_void_p]),
     "qf_row_plan_tiles": (c_i64, [c_i64, c_int]),
     "qf_row_plan_workspace": (c_size_t, [c_i64, c_int]),
     "qf_row_plan": (c_int, [c_void_p, c_i64, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),

@@ -199,6 +199,22 @@ struct LoraApplyArgs {
 int lora_apply_splits(bool tiles, int64_t units, int K, int r);
 hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipStream_t s);
 
+// ----------------------------------------------------------------- routing ---
+struct RouteArgs {
+  const void* logits;       // fp32 or bf16 [T, ld]
+  int64_t ld, T;
+  const float* bias;
+  int32_t* indices;         // [T, k]
+  float* weights;           // [T, k]
+  const float* dweights;    // backward
+  void* dlogits;
+  int64_t ldd;
+  float scale;
+  int32_t E, k, scoring, renorm, n_group, topk_group, group_top2;
+};
+hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s);
+hipError_t launch_route_backward(const RouteArgs& a, bool bf16, hipStream_t s);
+
 // Workgroups of the amax pass for a launch with `tiles` tiles of 256 * L_AMAX chunks.
 inline int amax_grid(int tiles) { return tiles < AMAX_GRID ? tiles : AMAX_GRID; }
 hipError_t launch_nvfp4_amax(const QArgs& a, hipStream_t s);

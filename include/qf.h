@@ -392,6 +392,57 @@ qf_status qf_lora_experts_merge_qdq_pack_nvfp4(const qf_lora_experts* e, int n, 
 qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int accumulate, void* ws, size_t ws_bytes,
                                         void* stream);
 
+/* ------------------------------------------------------------ routing ---- */
+/* Routing of tokens to the experts that the stacked-experts calls merge and quantize:
+ * scores of a token's router logits, the k experts it goes to, and their weights.
+ *   logits   fp32, or bf16 when logits_bf16 is 1, [tokens, ld]
+ *   scores   s = softmax(x) over the row, or s_e = 1 / (1 + exp(-x_e))
+ *   bias     device float[experts] or NULL: chosen by s + bias (load balance); the weights
+ *            do not see it.  Minus infinity takes an expert out.
+ *   groups   the experts form n_group equal runs; only those of the topk_group best groups
+ *            can be chosen.  A group ranks by its largest s + bias (QF_ROUTE_GROUP_MAX), or by
+ *            the sum of its two largest (QF_ROUTE_GROUP_TOP2; of one, that one).
+ *            n_group = topk_group = 1: no groups.
+ *   indices  int32 [tokens, k], best first;  ties (of experts and of groups) to the lower index
+ *   weights  fp32 [tokens, k]: s[index] * scale, divided by the chosen scores' sum first when
+ *            renorm is 1 (0 where that sum is 0)
+ * A logit of minus infinity masks its expert: never chosen, score 0.  A row with fewer than k
+ * experts left fills up with index -1 and weight 0 (a fully masked row is all of them, and
+ * qf_row_plan leaves those out).  A row with a NaN or plus infinity (in a logit, or a bias)
+ * gets index -1 and weight NaN throughout.
+ * Choice: exact with respect to the logits when bias is NULL and groups rank by their
+ * largest (scores increase with logits); else by s + bias in 64 bits, each function within
+ * a few units of rounding of the exact one.  Weights: fp32, relative error at most
+ * (2 D + 60) 2^-24, D the largest distance of a counted logit to the largest (softmax; sigmoid: 0).
+ * Limits: experts in 1..QF_ROUTE_MAX_EXPERTS, tokens in [0, 2^30), ld >= experts
+ * (QF_ERR_SHAPE); k in 1..QF_ROUTE_MAX_K and at most the experts of topk_group groups, n_group
+ * in 1..QF_ROUTE_MAX_GROUPS dividing experts, topk_group in 1..n_group, known constants,
+ * flags 0 or 1, scale finite (QF_ERR_ARG).  Arrays aligned to their element (QF_ERR_ALIGN);
+ * fastest with experts and ld multiples of 4 and logits 16-byte aligned.  One launch. */
+#define QF_ROUTE_SOFTMAX 0
+#define QF_ROUTE_SIGMOID 1
+#define QF_ROUTE_GROUP_MAX 0
+#define QF_ROUTE_GROUP_TOP2 1
+#define QF_ROUTE_MAX_EXPERTS 1024
+#define QF_ROUTE_MAX_K 32
+#define QF_ROUTE_MAX_GROUPS 64
+typedef struct qf_route_desc {
+  const void* logits;
+  int64_t tokens, ld;
+  const float* bias;
+  float scale;
+  int32_t logits_bf16, experts, k, scoring, renorm, n_group, topk_group, group_rule;
+} qf_route_desc;
+qf_status qf_moe_route(const qf_route_desc* d, int32_t* indices, float* weights, void* stream);
+/* Gradient of those weights: d_logits [tokens, ldd] (the logits' type) = sum_j d_weights[t, j]
+ * * d weights[t, j] / d logits[t, :], for the indices that the forward gave (a constant; an
+ * index outside [0, experts) contributes nothing, a row of them gets zeros).  Every element
+ * of the rows is written.  fp32 arithmetic, one rounding to bf16; softmax without renorm has a
+ * gradient in every logit, the other forms in the chosen ones only.  bias and the group
+ * fields are not read.  Limits as above, ldd >= experts. */
+qf_status qf_moe_route_backward(const qf_route_desc* d, const int32_t* indices, const float* d_weights, void* d_logits,
+                                int64_t ldd, void* stream);
+
 /* --------------------------------------------------------------- rows ---- */
 /* Row plan: groups rows by an id, keeping their order inside a group.  ids: device
  * int32[n], row i's id in [0, n_ids); any other value (e.g. -1: a request without an

@@ -29,6 +29,7 @@ q4k         256-element super-blocks of eight 32-element sub-blocks, pack/unpack
 ste         straight-through estimator backward
 lora        LoRA merge (W + B.A) and adapter gradients (float64)
 adamw       AdamW step, fp32 states and stochastically rounded E4M3 block states
+route       routing of tokens to experts and its gradient (float64)
 rows        row plan (grouping by id) and per-request adapters (float64)
 gemm        float64 reference for Y = QDQ(X) . QDQ(W)^T and its error bound
 
@@ -36,4 +37,4 @@ Parity status of each function is listed in the module docstrings.  Functions
 with no independent pin say "parity unpinned".
 """
 
-from . import primitives, nvfp4, mxfp4, q4k, ste, lora, gemm, adamw, rows  # noqa: F401
+from . import primitives, nvfp4, mxfp4, q4k, ste, lora, gemm, adamw, rows, route  # noqa: F401
