@@ -9,7 +9,6 @@ given are allocated with torch (device memory is torch's job here); every
 computation runs in the library's HIP kernels.
 """
 
-import contextlib
 import ctypes
 
 import torch
@@ -39,7 +38,7 @@ def _check(status, where):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _p(t):
@@ -523,25 +522,35 @@ _GROUP_RULE = {"max": QF_ROUTE_GROUP_MAX, "top2": QF_ROUTE_GROUP_TOP2, 0: 0, 1: 
 
 
 def _same_gpu(*tensors):
-    """The one GPU that holds every given tensor (None entries are skipped)."""
-    dev = None
+    """The index of the one GPU that holds every given tensor (None entries are skipped)."""
+    dev = -1
     for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise TypeError("tensors must live on the GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors live on {dev} and {t.device}")
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if i < 0 or dev >= 0:
+                    raise (TypeError("tensors must live on the GPU") if i < 0 else
+                           ValueError(f"tensors live on GPUs {dev} and {i}"))
+                dev = i
+            elif i < 0:
+                raise TypeError("tensors must live on the GPU")
     return dev
 
 
-def _on(dev):
-    """Makes dev the current device for a call (its current stream is then the call's)."""
-    if dev is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+def _call(dev, name, *args):
+    """Calls an entry point with GPU dev current and dev's current stream as its last argument."""
+    f = getattr(lib(), name)
+    if dev < 0 or dev == torch.cuda.current_device():
+        st = f(*args, _stream())
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream())
+    if st != QF_OK:
+        raise QFError(st, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _route_desc(logits, k, scoring, renorm, scale):
@@ -575,15 +584,17 @@ def qf_moe_route(logits, k, scoring="softmax", bias=None, n_group=1, topk_group=
     dev = _same_gpu(logits, bias, indices, weights)
     if bias is not None:
         d.bias = _dense(bias, "bias", torch.float32, (E,)).data_ptr()
-    d.n_group, d.topk_group, d.group_rule = int(n_group), int(topk_group), _GROUP_RULE[group_rule]
-    with _on(dev):
-        if indices is None:
-            indices = torch.empty((T, max(d.k, 0)), dtype=torch.int32, device=dev)
-        if weights is None:
-            weights = torch.empty((T, max(d.k, 0)), dtype=torch.float32, device=dev)
-        _dense(indices, "indices", torch.int32, (T, d.k))
-        _dense(weights, "weights", torch.float32, (T, d.k))
-        _check(lib().qf_moe_route(ctypes.byref(d), _p(indices), _p(weights), _stream()), "qf_moe_route")
+    d.n_group, d.topk_group, d.group_rule = n_group, topk_group, _GROUP_RULE[group_rule]
+    shape = (T, max(d.k, 0))
+    if indices is None:
+        indices = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    else:
+        _dense(indices, "indices", torch.int32, shape)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    else:
+        _dense(weights, "weights", torch.float32, shape)
+    _call(dev, "qf_moe_route", ctypes.byref(d), indices.data_ptr(), weights.data_ptr())
     return indices, weights
 
 
@@ -593,13 +604,13 @@ def qf_moe_route_backward(logits, indices, d_weights, scoring="softmax", renorm=
     dev = _same_gpu(logits, indices, d_weights, d_logits)
     _dense(indices, "indices", torch.int32, (T, d.k))
     _dense(d_weights, "d_weights", torch.float32, (T, d.k))
-    with _on(dev):
-        if d_logits is None:
-            d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    if d_logits is None:
+        d_logits, ldd = torch.empty((T, E), dtype=logits.dtype, device=logits.device), E
+    else:
         if d_logits.dtype != logits.dtype or tuple(d_logits.shape) != (T, E):
             raise ValueError("d_logits must have the logits' shape and type")
-        _check(lib().qf_moe_route_backward(ctypes.byref(d), _p(indices), _p(d_weights), _p(d_logits),
-                                           _mat(d_logits, "d_logits")[2], _stream()), "qf_moe_route_backward")
+        ldd = _mat(d_logits, "d_logits")[2]
+    _call(dev, "qf_moe_route_backward", ctypes.byref(d), indices.data_ptr(), d_weights.data_ptr(), d_logits.data_ptr(), ldd)
     return d_logits
 
 
@@ -618,7 +629,7 @@ class RowPlan:
     on the device, for n rows with ids in [0, n_ids)."""
 
     def __init__(self, n, n_ids, device):
-        self.n, self.n_ids, self.device = n, n_ids, device
+        self.n, self.n_ids = n, n_ids
         t = lib().qf_row_plan_tiles(n, n_ids)
         self.offsets = torch.empty(n_ids + 1, dtype=torch.int32, device=device)
         self.order = torch.empty(n, dtype=torch.int32, device=device)
@@ -633,15 +644,14 @@ def qf_row_plan(ids, n_ids, plan=None, ws=None):
     if plan is None:
         if not 1 <= n_ids <= ROW_MAX_IDS:
             raise ValueError(f"n_ids is 1..{ROW_MAX_IDS}")
-        plan = RowPlan(n, n_ids, dev)
-    elif plan.n != n or plan.n_ids != n_ids or plan.device != dev:
-        raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} ids on {plan.device}")
+        plan = RowPlan(n, n_ids, ids.device)
+    elif plan.n != n or plan.n_ids != n_ids or plan.offsets.get_device() != dev:
+        raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} ids on {plan.offsets.device}")
     need = lib().qf_row_plan_workspace(n, n_ids)
-    with _on(dev):
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        _check(lib().qf_row_plan(_p(ids), n, n_ids, _p(plan.offsets), _p(plan.order), _p(plan.tiles), _p(ws),
-                                 ws.numel() * ws.element_size() if ws is not None else 0, _stream()), "qf_row_plan")
+    if ws is None and need:
+        ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    _call(dev, "qf_row_plan", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
+          plan.tiles.data_ptr(), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
     return plan
 
 
@@ -670,17 +680,15 @@ def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
         raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} adapters")
     if plan is None and _ids(where, "ids").numel() != rows:
         raise ValueError("ids must hold an id per row of Y")
-    with _on(dev):
-        if ws is None:
-            ws = torch.empty(max(lib().qf_lora_apply_workspace(rows, K, r, E, int(plan is not None)), 1),
-                             dtype=torch.uint8, device=dev)
-        tail = (_p(Y), ldy, rows, N, K, r, _p(ws), ws.numel() * ws.element_size(), _stream())
-        head = (_p(X), ldx, rows_per_x, _p(A), _p(B), _p(scale), E)
-        if plan is None:
-            st = lib().qf_lora_apply(*head, _p(where), *tail)
-        else:
-            st = lib().qf_lora_apply_planned(*head, _p(plan.offsets), _p(plan.order), _p(plan.tiles), plan.n_ids, *tail)
-        _check(st, name)
+    if ws is None:
+        ws = torch.empty(max(lib().qf_lora_apply_workspace(rows, K, r, E, int(plan is not None)), 1), dtype=torch.uint8,
+                         device=X.device)
+    head = (X.data_ptr(), ldx, rows_per_x, A.data_ptr(), B.data_ptr(), _ptr(scale), E)
+    tail = (Y.data_ptr(), ldy, rows, N, K, r, ws.data_ptr(), ws.numel() * ws.element_size())
+    if plan is None:
+        _call(dev, name, *head, where.data_ptr(), *tail)
+    else:
+        _call(dev, name, *head, plan.offsets.data_ptr(), plan.order.data_ptr(), plan.tiles.data_ptr(), plan.n_ids, *tail)
     return Y
 
 
@@ -766,18 +774,15 @@ def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_l
     reads them on every replay); d_grad_scale (float32 [1]) multiplies the gradients; nothing
     is written where d_skip (int32 or uint32 [1]) is not 0.  seed: of the 8-bit states'
     stochastic rounding."""
-    dev = _same_gpu(d_lr, d_step, d_grad_scale, d_skip)
-    if dev is not None and batch.device is not None and dev != batch.device:
-        raise ValueError(f"device scalars live on {dev}, the tensors on {batch.device}")
     for t, name, kinds in ((d_lr, "d_lr", (torch.float32,)), (d_step, "d_step", (torch.int64,)),
                            (d_grad_scale, "d_grad_scale", (torch.float32,)),
                            (d_skip, "d_skip", (torch.int32, torch.uint32))):
-        if t is not None and (t.dtype not in kinds or t.numel() != 1):
-            raise TypeError(f"{name} must be one {kinds[0]} on the device")
-    h = AdamwHyper(float(lr), float(beta1), float(beta2), float(eps), int(step), _p(d_lr), _p(d_step),
-                   _p(d_grad_scale), _p(d_skip), int(seed) & 0xFFFFFFFF)
-    with _on(batch.device):
-        _check(lib().qf_adamw_step(batch.ref, batch.n, batch.state_bits, ctypes.byref(h), _stream()), "qf_adamw_step")
+        if t is not None and (t.dtype not in kinds or t.numel() != 1 or t.get_device() < 0 or
+                              batch.device >= 0 and t.get_device() != batch.device):
+            raise TypeError(f"{name} must be one {kinds[0]} on the tensors' device")
+    h = AdamwHyper(lr, beta1, beta2, eps, step, _ptr(d_lr), _ptr(d_step), _ptr(d_grad_scale), _ptr(d_skip),
+                   seed & 0xFFFFFFFF)
+    _call(batch.device, "qf_adamw_step", batch.ref, batch.n, batch.state_bits, ctypes.byref(h))
 
 
 # ------------------------------------------------------------- dequant ----

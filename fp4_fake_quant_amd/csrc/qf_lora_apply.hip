@@ -7,7 +7,7 @@
 //   rows   few rows: a workgroup per row (and part of K or of N), vector FMAs; the adapters'
 //          bytes are the work, and a decode step's rows rarely share an adapter.
 //   tiles  otherwise: the row plan's tiles of up to 32 rows of one adapter, on the bf16 matrix
-//          cores (32x32x16).  X is read once; the second step accumulates onto Y in fp32 and
+//          cores (16x16x32).  X is read once; the second step accumulates onto Y in fp32 and
 //          rounds once.  S enters the matrix cores as the sum of two bf16 (hi + lo, relative
 //          error below 2^-16), so its rounding stays far under Y's own.
 // Both are bounded by memory: X and Y pass once, 4 r flops per X element and per Y element.
@@ -22,10 +22,11 @@
 namespace qf {
 
 typedef __bf16 la_bf16x8 __attribute__((ext_vector_type(8)));
-typedef float la_f32x16 __attribute__((ext_vector_type(16)));
+typedef float la_f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int LA_WG = 256, LA_WAVES = LA_WG / 64;
-constexpr int LA_KSTEP = 64;                       // K per wave and step: 128 bytes of every row
+constexpr int LA_KSTEP = 128;                      // K per wave and step, at most
+constexpr int LA_NSTEP = 64;                       // N per wave and step: 128 bytes of every row
 constexpr int LA_ROW_RANKS = 16;                   // adapter rows per workgroup of the rows form
 constexpr int LA_ROW_K = LA_WG * 8;                // K per pass of a rows-form workgroup
 
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_row_down(LoraApplyArgs a) {
     for (int j = 0; j < LA_ROW_RANKS; ++j) part[threadIdx.x >> 6][j] = acc[j];
   __syncthreads();
   if ((int)threadIdx.x < nr)
-    a.S[((int64_t)split * a.rows + row) * a.r + r0 + threadIdx.x] =
+    a.S[((int64_t)split * a.rows + row) * a.rpad + r0 + threadIdx.x] =
         (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
 }
 
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_row_up(LoraApplyArgs a) {
   if ((int)threadIdx.x < QF_LORA_APPLY_MAX_R) {
     float v = 0.0f;
     if ((int)threadIdx.x < a.r)
-      for (int p = 0; p < a.splits; ++p) v += a.S[((int64_t)p * a.rows + row) * a.r + threadIdx.x];
+      for (int p = 0; p < a.splits; ++p) v += a.S[((int64_t)p * a.rows + row) * a.rpad + threadIdx.x];
     s[threadIdx.x] = v * scale;                    // zero past r
   }
   __syncthreads();
@@ -129,159 +130,237 @@ __global__ __launch_bounds__(LA_WG) void k_lora_row_up(LoraApplyArgs a) {
 }
 
 // --------------------------------------------------------------- tiles form ----
-// One tile's adapter, rows and positions; a plan that does not fit the call gives no tile.
+// One tile's adapter, positions, and the rows of this lane's two 16-row blocks (-1: none).  A plan
+// that does not fit the call gives no tile or no row.  The loads of a tile depend on each other
+// (tile, then order and offsets, then X or Y), so they are issued as early as they can be.
 struct LaTile {
-  int e, first, count;
+  int e, first, count, row[2];
 };
-__device__ __forceinline__ bool la_tile(const LoraApplyArgs& a, int t, LaTile& o) {
+__device__ __forceinline__ bool la_tile(const LoraApplyArgs& a, int t, int i, LaTile& o) {
   const int2 w = reinterpret_cast<const int2*>(a.tiles)[t];
-  if ((uint32_t)w.x >= (uint32_t)a.n_ids || w.y < 0) return false;
+  if ((uint32_t)w.x >= (uint32_t)a.n_ids || (uint32_t)w.y >= (uint32_t)a.rows) return false;
   o.e = w.x;
   o.first = w.y;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) o.row[b] = a.order[std::min(w.y + 16 * b + i, a.rows - 1)];
   o.count = std::min(std::min(a.offsets[w.x + 1], a.rows) - w.y, (int)QF_ROW_TILE);
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+    if (16 * b + i >= o.count || (uint32_t)o.row[b] >= (uint32_t)a.rows) o.row[b] = -1;
   return o.count > 0;
 }
-__device__ __forceinline__ int la_row(const LoraApplyArgs& a, const LaTile& t, int i) {
-  if (i >= t.count) return -1;
-  const int row = a.order[t.first + i];
-  return (uint32_t)row < (uint32_t)a.rows ? row : -1;
-}
 
-// S of one tile and K part: 32 rows x 32 NB adapter rows.  Lane (i = lane & 31, h = lane >> 5)
-// holds 8 bf16 of X row i and of adapter row i per matrix instruction; a 64-wide K step takes
-// the 64 bytes h * 64 .. of both, 16 at a time (the order of K inside a step is free).
+// S of one tile and K part: 32 rows x 16 NB adapter rows, two 16-row blocks of the 16x16x32
+// matrix instruction.  Lane (i = lane & 15, g = lane >> 4) holds 8 bf16 of X row i and of adapter
+// row i: the four lanes of a row read 64 contiguous bytes per load, two loads a 128-byte line.
+// Steps of 32 J columns, the next step's loads in flight during this one's products; the waves
+// take steps in turn and join their parts in LDS as (0 + 2) + (1 + 3).  Lanes without a row read
+// row 0 (their results are not stored); adapter rows past r are stored as zero.
 template <int NB>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
-  __shared__ float buf[QF_ROW_TILE][NB * 32 + 1];
+  constexpr int J = NB <= 2 ? LA_KSTEP / 32 : 2, STEP = 32 * J;
+  __shared__ la_f32x4 part[2][2 * NB][64];
+  const int split = blockIdx.y, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   LaTile t;
-  if (!la_tile(a, blockIdx.x, t)) return;
-  const int split = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
-  const int row = la_row(a, t, i);
-  const uint16_t* x = a.X + (int64_t)((row < 0 ? 0 : row) / a.rows_per_x) * a.ldx;
-  const uint16_t* A = a.A + ((int64_t)t.e * a.r + i) * a.K;
-  la_f32x16 acc[NB];
+  if (!la_tile(a, blockIdx.x, i, t)) return;
+  const uint16_t* x[2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < 2; ++b) x[b] = a.X + (int64_t)(std::max(t.row[b], 0) / a.rows_per_x) * a.ldx + g * 8;
+  const uint16_t* A[NB];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[b][j] = 0.0f;
-  for (int k0 = (split * LA_WAVES + wave) * LA_KSTEP; k0 < a.K; k0 += a.splits * LA_WAVES * LA_KSTEP) {
-    uint4 xv[4], av[NB][4];
+  for (int n = 0; n < NB; ++n)
+    A[n] = a.A + ((int64_t)t.e * a.r + std::min(n * 16 + i, a.r - 1)) * a.K + g * 8;
+  la_f32x4 acc[2][NB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + h * 32 + j * 8;
-      xv[j] = uint4{0, 0, 0, 0};
-      if (row >= 0 && k < a.K) xv[j] = *reinterpret_cast<const uint4*>(x + k);
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        av[b][j] = uint4{0, 0, 0, 0};
-        if (b * 32 + i < a.r && k < a.K) av[b][j] = *reinterpret_cast<const uint4*>(A + (int64_t)b * 32 * a.K + k);
+    for (int n = 0; n < NB; ++n) acc[b][n] = la_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  uint4 xv[J][2], av[J][NB];
+  auto load = [&](int k0) {
+    if (k0 + STEP <= a.K) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) xv[j][b] = *reinterpret_cast<const uint4*>(x[b] + k0 + j * 32);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) av[j][n] = *reinterpret_cast<const uint4*>(A[n] + k0 + j * 32);
+      }
+    } else {
+      const uint4 zero = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const bool in = k0 + j * 32 + g * 8 < a.K;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) xv[j][b] = in ? *reinterpret_cast<const uint4*>(x[b] + k0 + j * 32) : zero;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) av[j][n] = in ? *reinterpret_cast<const uint4*>(A[n] + k0 + j * 32) : zero;
       }
     }
+  };
+  const int stride = a.splits * LA_WAVES * STEP;
+  int k0 = (split * LA_WAVES + wave) * STEP;
+  if (k0 < a.K) load(k0);
+  while (k0 < a.K) {
+    uint4 xc[J][2], ac[J][NB];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < J; ++j) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        acc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(la_bf16x8, xv[j]),
-                                                         __builtin_bit_cast(la_bf16x8, av[b][j]), acc[b], 0, 0, 0);
-  }
-  // the waves' parts, added in order; register j of a lane is row 8 (j / 4) + 4 h + j % 4, column i
-  for (int w = 0; w < LA_WAVES; ++w) {
-    if (wave == w) {
+      for (int b = 0; b < 2; ++b) xc[j][b] = xv[j][b];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float* c = &buf[8 * (j >> 2) + 4 * h + (j & 3)][b * 32 + i];
-          *c = w == 0 ? acc[b][j] : *c + acc[b][j];
-        }
+      for (int n = 0; n < NB; ++n) ac[j][n] = av[j][n];
     }
+    k0 += stride;
+    if (k0 < a.K) load(k0);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          acc[b][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf16x8, xc[j][b]),
+                                                              __builtin_bit_cast(la_bf16x8, ac[j][n]), acc[b][n], 0, 0, 0);
+  }
+#pragma unroll
+  for (int from = 2; from > 0; from >>= 1) {
+    if (wave >= from && wave < 2 * from)
+#pragma unroll
+      for (int c = 0; c < 2 * NB; ++c) part[wave - from][c][lane] = acc[c / NB][c % NB];
+    __syncthreads();
+    if (wave < from)
+#pragma unroll
+      for (int c = 0; c < 2 * NB; ++c) acc[c / NB][c % NB] += part[wave][c][lane];
     __syncthreads();
   }
-  for (int c = threadIdx.x; c < t.count * a.r; c += LA_WG)
-    a.S[((int64_t)split * a.rows + t.first + c / a.r) * a.r + c % a.r] = buf[c / a.r][c % a.r];
+  if (wave != 0) return;
+  // register j of a lane: row 4 g + j of the block, adapter row i
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = 16 * b + 4 * g + j;
+      if (at < t.count)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          if (n * 16 < a.r)
+            a.S[((int64_t)split * a.rows + t.first + at) * a.rpad + n * 16 + i] = n * 16 + i < a.r ? acc[b][n][j] : 0.0f;
+    }
 }
 
 // Y of one tile and N part.  The matrix instruction's rows are outputs n and its columns the
-// tile's rows; its row m stands for n = n0 + 16 (m / 8) + 8 ((m / 4) % 2) + 4 half + m % 4 of a
-// 64-wide step, so that a lane ends up with 8 consecutive n of its row in two instructions'
-// registers: 16-byte accesses of Y.
+// tile's rows (two blocks of 16).  Row m of instruction `half` stands for n = n0 + 8 (m / 4) +
+// 4 half + m % 4 of a 32-wide step, so that a lane's two results are 8 consecutive n of its row
+// and the four lanes of a row access 64 contiguous bytes of Y at a time.  The instruction's 32
+// products are 16 adapter rows twice: S's high part in the first 16, its low part in the others,
+// B the same in both.  The next step's Y is loaded during this one's products.
 template <int RB, bool VEC_B, bool VEC_Y>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
+  constexpr int Q = LA_NSTEP / 32;
+  const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   LaTile t;
-  if (!la_tile(a, blockIdx.x, t)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 31, h = lane >> 5;
-  const int row = la_row(a, t, i);
+  if (!la_tile(a, blockIdx.x, i, t)) return;
+  const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part), step = LA_WAVES * LA_NSTEP;
+  int n0 = blockIdx.y * a.n_part + wave * LA_NSTEP;
+  uint16_t* y[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) y[b] = a.Y + (int64_t)std::max(t.row[b], 0) * a.ldy;
+  uint4 yv[Q][2];
+  auto load_y = [&](int at) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int n = at + 32 * q + 8 * g;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (VEC_Y && n + 8 <= a.N) {
+          yv[q][b] = *reinterpret_cast<const uint4*>(y[b] + n);
+          continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (n + j < a.N) w[j >> 1] |= (uint32_t)y[b][n + j] << (16 * (j & 1));
+        yv[q][b] = uint4{w[0], w[1], w[2], w[3]};
+      }
+    }
+  };
+  if (n0 < end) load_y(n0);
+
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
-  uint4 hi[RB], lo[RB];
+  uint4 sv[2][RB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    float v[8];
+  for (int b = 0; b < 2; ++b) {
+    const float* s = a.S + (int64_t)(t.first + std::min(16 * b + i, t.count - 1)) * a.rpad + (g & 1) * 8;
+    float v[RB][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int k = b * 16 + h * 8 + j;
-      v[j] = 0.0f;
-      if (i < t.count && k < a.r)
-        for (int p = 0; p < a.splits; ++p) v[j] += a.S[((int64_t)p * a.rows + t.first + i) * a.r + k];
-      v[j] *= scale;
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+    for (int p = 0; p < a.splits; ++p, s += (int64_t)a.rows * a.rpad)
+#pragma unroll
+      for (int k = 0; k < RB; ++k)
+        if (k * 16 < a.r) {
+          const float4 u = reinterpret_cast<const float4*>(s + k * 16)[0], w = reinterpret_cast<const float4*>(s + k * 16)[1];
+          v[k][0] += u.x; v[k][1] += u.y; v[k][2] += u.z; v[k][3] += u.w;
+          v[k][4] += w.x; v[k][5] += w.y; v[k][6] += w.z; v[k][7] += w.w;
+        }
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v0 = v[k][2 * j] * scale, v1 = v[k][2 * j + 1] * scale;
+        const uint32_t hi = pack_bf16x2(v0, v1);
+        w[j] = g < 2 ? hi : pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
+      }
+      sv[b][k] = uint4{w[0], w[1], w[2], w[3]};
     }
-    uint32_t wh[4], wl[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      wh[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-      wl[j] = pack_bf16x2(v[2 * j] - bf16_lo(wh[j]), v[2 * j + 1] - bf16_hi(wh[j]));
-    }
-    hi[b] = uint4{wh[0], wh[1], wh[2], wh[3]};
-    lo[b] = uint4{wl[0], wl[1], wl[2], wl[3]};
   }
   const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
-  uint16_t* y = a.Y + (int64_t)(row < 0 ? 0 : row) * a.ldy;
-  const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part);
-  for (int n0 = blockIdx.y * a.n_part + wave * 64; n0 < end; n0 += LA_WAVES * 64) {
-    la_f32x16 acc[2];
+  while (n0 < end) {
+    const int at = n0;
+    uint4 yc[Q][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 16 * q + 8 * h;
-      uint32_t w[4] = {0, 0, 0, 0};
-      if (row >= 0) {
-        if (VEC_Y && n + 8 <= a.N) {
-          const uint4 u = *reinterpret_cast<const uint4*>(y + n);
-          w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-        } else {
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (n + j < a.N) w[j >> 1] |= (uint32_t)y[n + j] << (16 * (j & 1));
+      for (int b = 0; b < 2; ++b) yc[q][b] = yv[q][b];
+    n0 += step;
+    if (n0 < end) load_y(n0);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int n = at + 32 * q + 8 * g;
+      la_f32x4 acc[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        acc[b][0] = la_f32x4{bf16_lo(yc[q][b].x), bf16_hi(yc[q][b].x), bf16_lo(yc[q][b].y), bf16_hi(yc[q][b].y)};
+        acc[b][1] = la_f32x4{bf16_lo(yc[q][b].z), bf16_hi(yc[q][b].z), bf16_lo(yc[q][b].w), bf16_hi(yc[q][b].w)};
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int m = at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3);
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+          uint4 bv = {0, 0, 0, 0};
+          if (m < a.N) bv = la_rank8<VEC_B>(B + (int64_t)m * a.r, k * 16 + (g & 1) * 8, a.r);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            acc[b][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf16x8, bv),
+                                                                   __builtin_bit_cast(la_bf16x8, sv[b][k]), acc[b][half], 0, 0, 0);
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j >> 2][4 * q + (j & 3)] = j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int n = n0 + 16 * (i >> 3) + 8 * ((i >> 2) & 1) + 4 * half + (i & 3);
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        uint4 bv = {0, 0, 0, 0};
-        if (n < a.N) bv = la_rank8<VEC_B>(B + (int64_t)n * a.r, b * 16 + h * 8, a.r);
-        acc[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(la_bf16x8, bv),
-                                                            __builtin_bit_cast(la_bf16x8, hi[b]), acc[half], 0, 0, 0);
-        acc[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(la_bf16x8, bv),
-                                                            __builtin_bit_cast(la_bf16x8, lo[b]), acc[half], 0, 0, 0);
-      }
-    }
-    if (row >= 0) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + 16 * q + 8 * h;
+      for (int b = 0; b < 2; ++b) {
+        if (t.row[b] < 0) continue;
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = pack_bf16x2(acc[j >> 1][4 * q + 2 * (j & 1)], acc[j >> 1][4 * q + 2 * (j & 1) + 1]);
+        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[b][j >> 1][2 * (j & 1)], acc[b][j >> 1][2 * (j & 1) + 1]);
         if (VEC_Y && n + 8 <= a.N) {
-          *reinterpret_cast<uint4*>(y + n) = uint4{w[0], w[1], w[2], w[3]};
+          *reinterpret_cast<uint4*>(y[b] + n) = uint4{w[0], w[1], w[2], w[3]};
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (n + j < a.N) y[n + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            if (n + j < a.N) y[b][n + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
         }
       }
     }
@@ -305,7 +384,7 @@ int lora_apply_splits(bool tiles, int64_t units, int K, int r) {
   const int per = tiles ? LA_WAVES * LA_KSTEP : LA_ROW_K;
   const int most = std::min((K + per - 1) / per, LORA_APPLY_MAX_SPLITS);
   int s = 1;
-  while (s * 2 <= most && wgs * s < 512) s *= 2;
+  while (s * 2 <= most && wgs * s < (tiles ? 1024 : 512)) s *= 2;
   return s;
 }
 
@@ -323,16 +402,17 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
     return hipGetLastError();
   }
   const dim3 g1((unsigned)n_tiles, (unsigned)a.splits);
-  if (a.r <= 32) k_lora_tile_down<1><<<g1, LA_WG, 0, s>>>(a);
-  else if (a.r <= 64) k_lora_tile_down<2><<<g1, LA_WG, 0, s>>>(a);
-  else k_lora_tile_down<4><<<g1, LA_WG, 0, s>>>(a);
+  if (a.r <= 16) k_lora_tile_down<1><<<g1, LA_WG, 0, s>>>(a);
+  else if (a.r <= 32) k_lora_tile_down<2><<<g1, LA_WG, 0, s>>>(a);
+  else if (a.r <= 64) k_lora_tile_down<4><<<g1, LA_WG, 0, s>>>(a);
+  else k_lora_tile_down<8><<<g1, LA_WG, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // N parts: whole passes of the four waves, about 1024 outputs, fewer for few tiles
-  int parts = (a.N + 1023) / 1024;
-  const int most = (a.N + LA_WAVES * 64 - 1) / (LA_WAVES * 64);
-  while (parts * 2 <= most && n_tiles * parts < 1024) parts *= 2;
-  a.n_part = ((a.N + parts - 1) / parts + LA_WAVES * 64 - 1) / (LA_WAVES * 64) * (LA_WAVES * 64);
+  // N parts: whole passes of the four waves; enough workgroups to fill the chip about once, no
+  // more (each pays for its tile's rows and S before its first product)
+  const int most = (a.N + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP);
+  const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1536 / n_tiles));
+  a.n_part = ((a.N + parts - 1) / parts + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP) * (LA_WAVES * LA_NSTEP);
   const dim3 g2((unsigned)n_tiles, (unsigned)((a.N + a.n_part - 1) / a.n_part));
   if (a.r <= 16) launch_up<1>(a, g2, vb, vy, s);
   else if (a.r <= 32) launch_up<2>(a, g2, vb, vy, s);
@@ -364,7 +444,7 @@ Space space_of(int64_t rows, int64_t K, int r, int n_adapters, bool planned) {
   const bool tiles = planned || !row_form(rows);
   const int64_t n_tiles = qf_row_plan_tiles(rows, n_adapters);
   const int splits = qf::lora_apply_splits(tiles, tiles ? n_tiles : rows, (int)K, r);
-  int64_t at = up256(rows * r * 4 * splits);
+  int64_t at = up256(rows * qf::lora_apply_rpad(r) * 4 * splits);
   if (tiles && !planned) {
     o.offsets = at;
     at += up256((int64_t)(n_adapters + 1) * 4);
@@ -430,6 +510,7 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
   a.K = (int)K;
   a.N = (int)N;
   a.r = r;
+  a.rpad = qf::lora_apply_rpad(r);
   a.n_adapters = n_adapters;
   a.n_ids = n_ids;
   const int64_t n_tiles = tiled ? qf_row_plan_tiles(rows, n_ids) : 0;
