@@ -61,6 +61,21 @@ __device__ __forceinline__ uint4 la_rank8(const uint16_t* row, int k, int r) {
   return uint4{w[0], w[1], w[2], w[3]};
 }
 
+// Lanes i and i ^ 8 of a 16-lane row exchange: lanes below 8 give v1 and get the other's v0.
+// Two registers that hold the 64-byte halves of a lane's own row become halves of two rows such
+// that one access of the wave covers whole 128-byte lines of 8 rows; applied again, it goes back.
+__device__ __forceinline__ void la_swap8(uint4& v0, uint4& v1, bool low) {
+  uint32_t a[4] = {v0.x, v0.y, v0.z, v0.w}, b[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t give = low ? b[j] : a[j];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
+    if (low) b[j] = got; else a[j] = got;
+  }
+  v0 = uint4{a[0], a[1], a[2], a[3]};
+  v1 = uint4{b[0], b[1], b[2], b[3]};
+}
+
 // ---------------------------------------------------------------- rows form ----
 __global__ __launch_bounds__(LA_WG) void k_lora_row_down(LoraApplyArgs a) {
   __shared__ float part[LA_WAVES][LA_ROW_RANKS];
@@ -250,40 +265,50 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
 
 // Y of one tile and N part.  The matrix instruction's rows are outputs n and its columns the
 // tile's rows (two blocks of 16).  Row m of instruction `half` stands for n = n0 + 8 (m / 4) +
-// 4 half + m % 4 of a 32-wide step, so that a lane's two results are 8 consecutive n of its row
-// and the four lanes of a row access 64 contiguous bytes of Y at a time.  The instruction's 32
-// products are 16 adapter rows twice: S's high part in the first 16, its low part in the others,
-// B the same in both.  The next step's Y is loaded during this one's products.
+// 4 half + m % 4 of a 32-wide step q, so that a lane's two results are 8 consecutive n of its row
+// and the four lanes of a row hold 64 contiguous bytes; the steps q = 0, 1 are the halves of a
+// 128-byte line, exchanged between lanes so that Y is accessed in whole lines.  The
+// instruction's 32 products are 16 adapter rows twice: S's high part in the first 16, its low part
+// in the others, B the same in both.  The next step's Y is loaded during this one's products.
 template <int RB, bool VEC_B, bool VEC_Y>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
-  constexpr int Q = LA_NSTEP / 32;
+  static_assert(LA_NSTEP == 64, "a step of the wave is one 128-byte line of every row");
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+  const bool low = i < 8;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   LaTile t;
   if (!la_tile(a, blockIdx.x, i, t)) return;
   const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part), step = LA_WAVES * LA_NSTEP;
   int n0 = blockIdx.y * a.n_part + wave * LA_NSTEP;
-  uint16_t* y[2];
+  // accesses v = 0, 1 of block b: rows (i & 7) + 8 v of the block, half i / 8 of the line
+  int row[2][2];
+  uint16_t* y[2][2];
+  const int off = 32 * (i >> 3) + 8 * g;
 #pragma unroll
-  for (int b = 0; b < 2; ++b) y[b] = a.Y + (int64_t)std::max(t.row[b], 0) * a.ldy;
-  uint4 yv[Q][2];
+  for (int b = 0; b < 2; ++b) {
+    const int other = __builtin_amdgcn_mov_dpp(t.row[b], 0x128, 0xF, 0xF, true);   // the row of lane i ^ 8
+    row[b][0] = low ? t.row[b] : other;
+    row[b][1] = low ? other : t.row[b];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) y[b][v] = a.Y + (int64_t)std::max(row[b][v], 0) * a.ldy + off;
+  }
+  uint4 yv[2][2];
   auto load_y = [&](int at) {
+    const int n = at + off;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int n = at + 32 * q + 8 * g;
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t w[4] = {0, 0, 0, 0};
+      for (int v = 0; v < 2; ++v) {
         if (VEC_Y && n + 8 <= a.N) {
-          yv[q][b] = *reinterpret_cast<const uint4*>(y[b] + n);
+          yv[b][v] = *reinterpret_cast<const uint4*>(y[b][v] + at);
           continue;
         }
+        uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (n + j < a.N) w[j >> 1] |= (uint32_t)y[b][n + j] << (16 * (j & 1));
-        yv[q][b] = uint4{w[0], w[1], w[2], w[3]};
+          if (n + j < a.N) w[j >> 1] |= (uint32_t)y[b][v][at + j] << (16 * (j & 1));
+        yv[b][v] = uint4{w[0], w[1], w[2], w[3]};
       }
-    }
   };
   if (n0 < end) load_y(n0);
 
@@ -320,21 +345,22 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
   while (n0 < end) {
     const int at = n0;
-    uint4 yc[Q][2];
+    uint4 yc[2][2];
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) yc[q][b] = yv[q][b];
+      for (int v = 0; v < 2; ++v) yc[b][v] = yv[b][v];
     n0 += step;
     if (n0 < end) load_y(n0);
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int n = at + 32 * q + 8 * g;
+    for (int b = 0; b < 2; ++b) la_swap8(yc[b][0], yc[b][1], low);    // now this lane's row, steps q = 0, 1
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
       la_f32x4 acc[2][2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        acc[b][0] = la_f32x4{bf16_lo(yc[q][b].x), bf16_hi(yc[q][b].x), bf16_lo(yc[q][b].y), bf16_hi(yc[q][b].y)};
-        acc[b][1] = la_f32x4{bf16_lo(yc[q][b].z), bf16_hi(yc[q][b].z), bf16_lo(yc[q][b].w), bf16_hi(yc[q][b].w)};
+        acc[b][0] = la_f32x4{bf16_lo(yc[b][q].x), bf16_hi(yc[b][q].x), bf16_lo(yc[b][q].y), bf16_hi(yc[b][q].y)};
+        acc[b][1] = la_f32x4{bf16_lo(yc[b][q].z), bf16_hi(yc[b][q].z), bf16_lo(yc[b][q].w), bf16_hi(yc[b][q].w)};
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -350,20 +376,27 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
         }
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (t.row[b] < 0) continue;
-        uint32_t w[4];
+      for (int b = 0; b < 2; ++b)
+        yc[b][q] = uint4{pack_bf16x2(acc[b][0][0], acc[b][0][1]), pack_bf16x2(acc[b][0][2], acc[b][0][3]),
+                         pack_bf16x2(acc[b][1][0], acc[b][1][1]), pack_bf16x2(acc[b][1][2], acc[b][1][3])};
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(acc[b][j >> 1][2 * (j & 1)], acc[b][j >> 1][2 * (j & 1) + 1]);
+    for (int b = 0; b < 2; ++b) la_swap8(yc[b][0], yc[b][1], low);
+    const int n = at + off;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        if (row[b][v] < 0) continue;
         if (VEC_Y && n + 8 <= a.N) {
-          *reinterpret_cast<uint4*>(y[b] + n) = uint4{w[0], w[1], w[2], w[3]};
+          *reinterpret_cast<uint4*>(y[b][v] + at) = yc[b][v];
         } else {
+          const uint32_t w[4] = {yc[b][v].x, yc[b][v].y, yc[b][v].z, yc[b][v].w};
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (n + j < a.N) y[b][n + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            if (n + j < a.N) y[b][v][at + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
         }
       }
-    }
   }
 }
 
