@@ -162,9 +162,9 @@ struct AdamwArgs {
 };
 
 // -------------------------------------------------------------- row plan ---
-constexpr int RP_ONE = 4096;          // rows that one workgroup plans alone (one launch)
-constexpr int RP_MAX_WG = 64;         // workgroups of larger plans (each sums all of their counts)
-constexpr int RP_MIN_PER_WG = 2048;   // rows per workgroup of larger plans, at least
+constexpr int RP_ONE_LAUNCH = 16384;  // rows up to which every workgroup counts all of them itself
+constexpr int RP_MAX_WG = 128;        // workgroups of a plan, at most
+constexpr int RP_MIN_PER_WG = 2048;   // rows per workgroup, at least
 
 struct RowPlanArgs {
   const int32_t* ids;
@@ -174,7 +174,7 @@ struct RowPlanArgs {
   int32_t* order;          // [n]
   int32_t* tiles;          // [n_tiles][2]
   int64_t n_tiles;
-  uint32_t* hist;          // workspace [workgroups][n_ids]
+  uint32_t* hist;          // workspace [workgroups][n_ids rounded up to even] (null: one launch)
 };
 hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
 

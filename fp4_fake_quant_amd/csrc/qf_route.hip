@@ -1,13 +1,23 @@
 // Routing of tokens to experts: scores, selection, weights, and their gradient.
 //
 // A row (token) is held by L lanes of one wave, V consecutive logits each, so that an index
-// order is a lane order.  Selection repeats k times: the lane's best (lowest index on ties),
-// the row's best over its L lanes (cross-lane max), the lowest lane that holds it.
+// order is a lane order, and one wave works on 64 / L rows.
 //
 // What is compared decides the chosen experts, and a tie decided by rounding would choose
 // differently from one implementation to the next.  Without a bias (and with groups ranked by
 // their best expert) both scorings are increasing in the logit, so the logits themselves are
-// compared: exact.  Otherwise scores plus bias are compared in 64 bits.
+// compared: exact.  Otherwise scores plus bias are compared as if in 64 bits.
+//
+// Both are done twice at most.  The fast pass orders 31-bit integer keys: the leading bits of
+// the fp32 value, and below them the place in the lane, so that the largest key below the
+// last choice takes one subtraction and half a maximum per logit and nothing has to be
+// removed.  It knows when it cannot tell: two neighbours in the order whose values are closer
+// than the key's truncation and the fp32 score's error bound.  Only then does the wave select
+// again, on the fp32 logits themselves or on 64-bit scores.  bf16 logits fit a key with their
+// index and need no second pass.  The selection is bounded by vector instructions (k + 1 rounds
+// of about 40), the rest by memory.
+#include <type_traits>
+
 #include "qf_device.h"
 #include "qf_kernels.h"
 
@@ -73,53 +83,174 @@ __device__ __forceinline__ void rt_load(const uint16_t* row, int e0, int E, floa
   }
 }
 
-template <typename K> __device__ __forceinline__ K rt_exp(K x);
-template <> __device__ __forceinline__ float rt_exp<float>(float x) { return expf(x); }
-template <> __device__ __forceinline__ double rt_exp<double>(double x) { return exp(x); }
-
-// Keeps only the experts of the best groups: the others' keys become minus infinity.
+// LDS of a wave's group ranking.
 template <int L, int V, typename K>
-__device__ __forceinline__ void rt_groups(const RouteArgs& a, int sub, int lane, K (&key)[V], K* keys, K* score, uint8_t* keep) {
+struct RtGroups {
+  K keys[RT_WAVE / L * L * V];
+  K score[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
+  uint8_t keep[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
+};
+
+template <typename K>
+__device__ __forceinline__ void rt_top2(K& m1, K& m2, K v) {
+  m2 = v > m1 ? m1 : (v > m2 ? v : m2);
+  m1 = v > m1 ? v : m1;
+}
+
+// Keeps only the experts of the best groups: the others' keys become minus infinity.  False
+// where a kept and a dropped group differ by no more than margin.
+template <int L, int V, typename K>
+__device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane, K (&key)[V], RtGroups<L, V, K>& s, K margin) {
   const int size = a.E / a.n_group;
+  const K none = -(K)RT_INF;
+  K* keys = s.keys + sub * (L * V);
+  K* score = s.score + sub * QF_ROUTE_MAX_GROUPS;
+  uint8_t* keep = s.keep + sub * QF_ROUTE_MAX_GROUPS;
+  // a group is a power of two of whole lanes: its two best by exchange
+  const int lanes = size / V;
+  const bool whole = size % V == 0 && (lanes & (lanes - 1)) == 0;
+  if (whole) {
+    K m1 = none, m2 = none;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (lane * V + i < a.E) keys[sub * (L * V) + lane * V + i] = key[i];
-  __syncthreads();
-  for (int g = lane; g < a.n_group; g += L) {
-    K m1 = -(K)RT_INF, m2 = -(K)RT_INF;
-    for (int i = 0; i < size; ++i) {
-      const K v = keys[sub * (L * V) + g * size + i];
-      m2 = v > m1 ? m1 : (v > m2 ? v : m2);
-      m1 = v > m1 ? v : m1;
+    for (int i = 0; i < V; ++i) rt_top2(m1, m2, key[i]);
+    for (int d = 1; d < lanes; d <<= 1) {
+      const K o1 = __shfl_xor(m1, d), o2 = __shfl_xor(m2, d);
+      m2 = m1 > o1 ? (m2 > o1 ? m2 : o1) : (m1 > o2 ? m1 : o2);
+      m1 = m1 > o1 ? m1 : o1;
     }
-    score[sub * QF_ROUTE_MAX_GROUPS + g] = a.group_top2 && m2 > -(K)RT_INF ? m1 + m2 : m1;
+    if (lane % lanes == 0 && lane * V < a.E) score[lane / lanes] = a.group_top2 && m2 > none ? m1 + m2 : m1;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane * V + i < a.E) keys[lane * V + i] = key[i];
+    __syncthreads();
+    for (int g = lane; g < a.n_group; g += L) {
+      K m1 = none, m2 = none;
+      for (int i = 0; i < size; ++i) rt_top2(m1, m2, keys[g * size + i]);
+      score[g] = a.group_top2 && m2 > none ? m1 + m2 : m1;
+    }
   }
   __syncthreads();
+  K worst = (K)RT_INF, best = none;            // of the kept, of the dropped
   for (int g = lane; g < a.n_group; g += L) {
-    const K mine = score[sub * QF_ROUTE_MAX_GROUPS + g];
+    const K mine = score[g];
     int rank = 0;
     for (int o = 0; o < a.n_group; ++o) {
-      const K v = score[sub * QF_ROUTE_MAX_GROUPS + o];
+      const K v = score[o];
       rank += v > mine || (v == mine && o < g);
     }
-    keep[sub * QF_ROUTE_MAX_GROUPS + g] = rank < a.topk_group;
+    const bool in = rank < a.topk_group;
+    keep[g] = in;
+    if (in) worst = mine < worst ? mine : worst;
+    else best = mine > best ? mine : best;
   }
   __syncthreads();
+  worst = -rt_row_max<L>(-worst);
+  best = rt_row_max<L>(best);
+  if (whole) {
+    const bool in = lane * V < a.E && keep[lane / lanes];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    if (e < a.E && !keep[sub * QF_ROUTE_MAX_GROUPS + e / size]) key[i] = -(K)RT_INF;
+    for (int i = 0; i < V; ++i) key[i] = in ? key[i] : none;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      if (e < a.E && !keep[e / size]) key[i] = none;
+    }
+  }
+  return !(best > none) || worst - best > margin;
+}
+
+// Selection by comparing keys of type K (ties to the lower index); minus infinity is never
+// chosen.
+template <int L, int V, typename K>
+__device__ __forceinline__ void rt_select(const RouteArgs& a, int lane, uint64_t seg, K (&key)[V], int32_t* chosen) {
+  for (int j = 0; j < a.k; ++j) {
+    K best = key[0];
+    int slot = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i) {
+      const bool up = key[i] > best;
+      best = up ? key[i] : best;
+      slot = up ? i : slot;
+    }
+    const K mx = rt_row_max<L>(best);
+    const uint64_t who = __ballot(best == mx) & seg;
+    if (who == 0) {                                          // NaN keys of a poisoned row
+      if (lane == 0) chosen[j] = -1;
+    } else if ((int)threadIdx.x == __ffsll((unsigned long long)who) - 1) {
+      chosen[j] = mx > -(K)RT_INF ? lane * V + slot : -1;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == slot) key[i] = -(K)RT_INF;
+    }
   }
 }
 
-// K: float compares logits, double compares scores plus bias.
-template <int L, int V, typename X, typename K, bool VEC, bool GROUPS>
+__device__ __forceinline__ uint32_t rt_order(float v) {      // increasing with v
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float rt_unorder(uint32_t u) {
+  return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+}
+template <int L>
+__device__ __forceinline__ uint32_t rt_row_umax(uint32_t v) {
+  v = umax(v, dpp_xor1(v));
+  v = umax(v, dpp_xor2(v));
+  v = umax(v, dpp_hmirror(v));
+  v = umax(v, dpp_mirror(v));
+  if (L > 16) v = umax(v, swz_xor16(v));
+  return v;
+}
+
+// Fast selection by keys below 2^31 (0: never chosen): each round takes the largest key below
+// the last one, which is the largest of key - last as an unsigned number (all keys above wrap
+// to small differences).  IDX low bits of a key are its place: in the lane, or in the row.
+// close(last, next): whether the values of two neighbours cannot be told apart.
+template <int L, int V, int IDX, bool IN_ROW, typename F>
+__device__ __forceinline__ bool rt_select_keys(const RouteArgs& a, int lane, const uint32_t (&key)[V], int32_t* chosen,
+                                               F close) {
+  uint32_t last = 0x80000000u;
+  bool sure = true;
+  const int rounds = IN_ROW ? a.k : a.k + 1;                // one more neighbour decides the last choice
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine = umax(mine, key[i] - last);
+    const uint32_t row = rt_row_umax<L>(mine);
+    const uint32_t next = row >= 0x80000000u ? last + row : 0;    // 0 also when nothing is below
+    if (!IN_ROW) {
+      if (j > 0 && next != 0) sure = sure && !close(last, next);
+      // a key that two lanes of a row have: more holders than rows
+      if (__popcll(__ballot(next != 0 && mine == row)) > __popcll(__ballot(next != 0 && lane == 0))) sure = false;
+    }
+    if (j < a.k) {
+      if (next == 0) {
+        if (lane == 0) chosen[j] = -1;
+      } else if (mine == row) {
+        chosen[j] = IN_ROW ? (1 << IDX) - 1 - (int)(next & ((1u << IDX) - 1u))
+                           : lane * V + V - 1 - (int)(next & ((1u << IDX) - 1u));
+      }
+    }
+    last = next;
+  }
+  return sure;
+}
+
+constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
+
+__device__ __forceinline__ float rt_fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+// SCORES: choose by scores plus bias, else by logits.
+template <int L, int V, typename X, bool SCORES, bool VEC, bool GROUPS>
 __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
   constexpr int ROWS = RT_WAVE / L;
-  constexpr bool SCORES = sizeof(K) == 8;
+  constexpr bool IN_ROW = !SCORES && sizeof(X) == 2;       // logit and index fit a key
+  using K2 = typename std::conditional<SCORES, double, float>::type;   // the second pass's keys
   __shared__ int32_t chosen[ROWS][QF_ROUTE_MAX_K];
-  __shared__ K keys[GROUPS ? ROWS * L * V : 1], gscore[GROUPS ? ROWS * QF_ROUTE_MAX_GROUPS : 1];
-  __shared__ uint8_t keep[GROUPS ? ROWS * QF_ROUTE_MAX_GROUPS : 1];
+  __shared__ typename std::conditional<GROUPS, RtGroups<L, V, K2>, char>::type gs2;
+  __shared__ typename std::conditional<GROUPS && SCORES, RtGroups<L, V, float>, char>::type gs1;
   const int lane = threadIdx.x % L, sub = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
   const bool live = t < a.T;
@@ -135,64 +266,98 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
     bad |= !(x[i] < RT_INF);
     top = fmaxf(top, x[i]);
   }
-  K key[V];
-  float total = 0.0f;              // softmax: the sum of exp(x - top), when the weights need it
+  float total = 0.0f;              // softmax: the sum of exp(x - top), when it is needed
   const bool softmax = a.scoring == QF_ROUTE_SOFTMAX;
+  float v[V];                      // what is compared
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = x[i];
   if (softmax && (SCORES || !a.renorm)) {
     top = rt_row_max<L>(top);
     if (top == -RT_INF) top = 0.0f;        // nothing but masked experts: every exp is 0
-  }
-  if (SCORES) {
-    K sum = 0;
+    float e[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = softmax ? rt_exp<K>((K)x[i] - (K)top) : (K)1 / ((K)1 + rt_exp<K>(-(K)x[i]));
-      sum += key[i];
+      e[i] = rt_fast_exp(x[i] - top);
+      total += e[i];
     }
-    if (softmax) {
-      sum = rt_row_sum<L>(sum);
-      total = (float)sum;
+    total = rt_row_sum<L>(total);
+    if (SCORES) {
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = e[i] * inv;
     }
+  } else if (SCORES) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + rt_fast_exp(-x[i]));
+  }
+  if (SCORES) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane * V + i;
-      if (softmax) key[i] = key[i] / sum;
-      if (a.bias && e < a.E) key[i] += (K)a.bias[e];
-      if (e >= a.E || x[i] == -RT_INF) key[i] = -(K)RT_INF;
-      bad |= !(key[i] < (K)RT_INF);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = x[i];
-    if (softmax && !a.renorm) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) total += expf(x[i] - top);
-      total = rt_row_sum<L>(total);
+      if (a.bias && e < a.E) v[i] += a.bias[e];
+      if (x[i] == -RT_INF) v[i] = -RT_INF;
+      bad |= !(v[i] < RT_INF);
     }
   }
-  const uint64_t seg = (L == 64 ? ~0ull : (1ull << L) - 1ull) << (sub * L);
+  const uint64_t seg = ((1ull << L) - 1ull) << (sub * L);
   bad = (__ballot(bad) & seg) != 0;
-  if (GROUPS) rt_groups<L, V, K>(a, sub, lane, key, keys, gscore, keep);
 
-  for (int j = 0; j < a.k; ++j) {
-    K best = key[0];
-    int slot = 0;
+  // The fp32 score's error: sigmoid, 5 units of 2^-24 (exp2 and its argument, sum, reciprocal,
+  // each weighed by s or s (1 - s)); softmax, 32 units of the largest score (the sum's
+  // roundings most of all); the bias adds half a unit of the key.  Twice that for a pair.
+  const float err = SCORES ? (softmax ? 0x1p-18f * (total > 0.0f ? 1.0f / total : 0.0f) : 0x1p-20f) : 0.0f;
+  bool sure = true;
+  if constexpr (GROUPS) {
+    if constexpr (SCORES) {
+      float big = 0.0f;
 #pragma unroll
-    for (int i = 1; i < V; ++i) {
-      const bool up = key[i] > best;
-      best = up ? key[i] : best;
-      slot = up ? i : slot;
+      for (int i = 0; i < V; ++i) big = fmaxf(big, v[i] > -RT_INF ? __builtin_fabsf(v[i]) : 0.0f);
+      sure = rt_groups<L, V, float>(a, sub, lane, v, gs1, 2.0f * err + 0x1p-21f * rt_row_max<L>(big));
+    } else {
+      rt_groups<L, V, float>(a, sub, lane, v, gs2, 0.0f);
     }
-    const K mx = rt_row_max<L>(best);
-    const uint64_t who = __ballot(best == mx) & seg;
-    const bool win = (int)threadIdx.x == __ffsll((unsigned long long)who) - 1;
-    if (win) {
-      chosen[sub][j] = mx > -(K)RT_INF ? lane * V + slot : -1;
+  }
+  uint32_t key[V];
+  constexpr int IDX = IN_ROW ? 10 : rt_log2(V);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i == slot) key[i] = -(K)RT_INF;
+  for (int i = 0; i < V; ++i) {
+    const uint32_t o = rt_order(v[i]);
+    key[i] = IN_ROW ? ((o >> 16) << IDX | (uint32_t)((1 << IDX) - 1 - (lane * V + i)))
+                    : ((o >> (IDX + 1)) << IDX | (uint32_t)(V - 1 - i));
+    if (!(v[i] > -RT_INF)) key[i] = 0;
+  }
+  sure = rt_select_keys<L, V, IDX, IN_ROW>(a, lane, key, chosen[sub], [&](uint32_t last, uint32_t next) {
+    if (!SCORES) return (last >> IDX) == (next >> IDX);
+    const float hi = rt_unorder((last >> IDX) << (IDX + 1)), lo = rt_unorder((next >> IDX) << (IDX + 1));
+    // truncation takes up to 2^(IDX + 1) units of 2^-23 of a value
+    return !(hi - lo > err + fmaxf(__builtin_fabsf(hi), __builtin_fabsf(lo)) * (0x1p-22f * (1 << IDX) + 0x1p-22f));
+  }) && sure;
+
+  if constexpr (!IN_ROW) {
+    if (__ballot(!sure && !bad && live) != 0) {
+      K2 key2[V];
+      if constexpr (SCORES) {
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          key2[i] = softmax ? exp((double)x[i] - (double)top) : 1.0 / (1.0 + exp(-(double)x[i]));
+          sum += key2[i];
+        }
+        if (softmax) sum = rt_row_sum<L>(sum);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = lane * V + i;
+          if (softmax) key2[i] = key2[i] / sum;
+          if (a.bias && e < a.E) key2[i] += (double)a.bias[e];
+          if (x[i] == -RT_INF) key2[i] = -(double)RT_INF;
+        }
+        if constexpr (GROUPS) rt_groups<L, V, K2>(a, sub, lane, key2, gs2, 0.0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key2[i] = v[i];          // the groups' choice was exact
+      }
+      rt_select<L, V, K2>(a, lane, seg, key2, chosen[sub]);
     }
-    if (who == 0 && lane == 0) chosen[sub][j] = -1;      // NaN keys of a poisoned row
   }
   __syncthreads();
 
@@ -306,25 +471,26 @@ __global__ __launch_bounds__(RT_WAVE) void k_route_backward(RouteArgs a) {
 }
 
 namespace {
-template <int L, int V, typename X, typename K>
+template <int L, int V, typename X, bool S>
 void route_go(const RouteArgs& a, bool vec, hipStream_t s) {
   constexpr int ROWS = RT_WAVE / L;
   const unsigned grid = (unsigned)((a.T + ROWS - 1) / ROWS);
   if (a.n_group > 1) {
-    if (vec) k_route<L, V, X, K, true, true><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, K, false, true><<<grid, RT_WAVE, 0, s>>>(a);
+    if (vec) k_route<L, V, X, S, true, true><<<grid, RT_WAVE, 0, s>>>(a);
+    else k_route<L, V, X, S, false, true><<<grid, RT_WAVE, 0, s>>>(a);
   } else {
-    if (vec) k_route<L, V, X, K, true, false><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, K, false, false><<<grid, RT_WAVE, 0, s>>>(a);
+    if (vec) k_route<L, V, X, S, true, false><<<grid, RT_WAVE, 0, s>>>(a);
+    else k_route<L, V, X, S, false, false><<<grid, RT_WAVE, 0, s>>>(a);
   }
 }
-template <typename X, typename K>
+// Few lanes with many logits each: a round's work over the lanes' logits is shared by more rows.
+template <typename X, bool S>
 void route_size(const RouteArgs& a, bool vec, hipStream_t s) {
-  if (a.E <= 64) route_go<16, 4, X, K>(a, vec, s);
-  else if (a.E <= 128) route_go<16, 8, X, K>(a, vec, s);
-  else if (a.E <= 256) route_go<16, 16, X, K>(a, vec, s);
-  else if (a.E <= 512) route_go<32, 16, X, K>(a, vec, s);
-  else route_go<32, 32, X, K>(a, vec, s);
+  if (a.E <= 64) route_go<16, 4, X, S>(a, vec, s);
+  else if (a.E <= 128) route_go<16, 8, X, S>(a, vec, s);
+  else if (a.E <= 256) route_go<16, 16, X, S>(a, vec, s);
+  else if (a.E <= 512) route_go<32, 16, X, S>(a, vec, s);
+  else route_go<32, 32, X, S>(a, vec, s);
 }
 }  // namespace
 
@@ -333,11 +499,11 @@ hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s) {
   const int64_t sz = bf16 ? 2 : 4;
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (4 * sz) == 0;
   if (bf16) {
-    if (scores) route_size<uint16_t, double>(a, vec, s);
-    else route_size<uint16_t, float>(a, vec, s);
+    if (scores) route_size<uint16_t, true>(a, vec, s);
+    else route_size<uint16_t, false>(a, vec, s);
   } else {
-    if (scores) route_size<float, double>(a, vec, s);
-    else route_size<float, float>(a, vec, s);
+    if (scores) route_size<float, true>(a, vec, s);
+    else route_size<float, false>(a, vec, s);
   }
   return hipGetLastError();
 }

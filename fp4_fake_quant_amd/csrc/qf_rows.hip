@@ -7,48 +7,80 @@
 // such lanes below it.  Nothing depends on the order of atomics (they only count), so the
 // result is the one stable order.
 //
-// Up to RP_ONE rows take one workgroup and one launch; more take a counting launch first,
-// whose per-workgroup counts every workgroup of the second launch sums for itself (at most
-// RP_MAX_WG rows of counts, read from L2).  Bounded by launch and LDS latency, not by bytes.
+// Up to RP_ONE_LAUNCH rows every workgroup counts all rows for itself (one launch; reading 4 n
+// bytes from L2 is shorter than a second launch); more take a counting launch first, whose
+// per-workgroup counts every workgroup of the second launch sums.  Bounded by launch, load and
+// LDS latency, not by bytes.
 #include "qf_kernels.h"
 
 namespace qf {
 
 constexpr int RP_WAVES = 8, RP_WG = RP_WAVES * 64;
 constexpr int RP_IDS = QF_ROW_MAX_IDS;
+constexpr int RP_HELD = 4;                 // ids per lane kept in registers between counting and placing
 static_assert(RP_IDS == 2 * RP_WG, "the prefix sum handles two ids per thread");
 
 // Rows per workgroup and workgroups of a plan of n rows.
 int row_plan_wgs(int64_t n, int64_t* rows_per_wg) {
-  int64_t per = RP_ONE;
-  if (n > RP_ONE) {
-    per = (n + RP_MAX_WG - 1) / RP_MAX_WG;
-    per = (per + RP_WG - 1) / RP_WG * RP_WG;
-    if (per < RP_MIN_PER_WG) per = RP_MIN_PER_WG;
-  }
+  int64_t per = (n + RP_MAX_WG - 1) / RP_MAX_WG;
+  per = (per + RP_WG - 1) / RP_WG * RP_WG;
+  if (per < RP_MIN_PER_WG) per = RP_MIN_PER_WG;
   *rows_per_wg = per;
   return n > 0 ? (int)((n + per - 1) / per) : 1;
 }
+// Row length of the counts: even, so that two ids load together.
+__host__ __device__ inline uint32_t rp_pitch(uint32_t n_ids) { return (n_ids + 1) & ~1u; }
 
-__device__ __forceinline__ void rp_count(const int32_t* ids, int64_t lo, int64_t hi, uint32_t n_ids, uint32_t* cnt) {
-  for (int64_t i = lo + (threadIdx.x & 63); i < hi; i += 64) {
-    const uint32_t id = (uint32_t)ids[i];
-    if (id < n_ids) atomicAdd(&cnt[id], 1u);
+// The lanes of the wave with a valid id, and whether they all have the same one.
+struct RpWave {
+  uint64_t in;
+  bool one;
+};
+__device__ __forceinline__ RpWave rp_wave(uint32_t id, uint32_t n_ids) {
+  RpWave o;
+  o.in = __ballot(id < n_ids);
+  const int lane = o.in ? __ffsll((unsigned long long)o.in) - 1 : 0;
+  const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)id, lane);
+  o.one = __ballot(id < n_ids && id != first) == 0;
+  return o;
+}
+
+// Counts one id per lane (called by whole waves); a wave with a single id adds once, where 64
+// additions to one word would queue up.
+__device__ __forceinline__ void rp_add(uint32_t* cnt, uint32_t id, uint32_t n_ids) {
+  const RpWave w = rp_wave(id, n_ids);
+  if (w.one) {
+    if (w.in && (threadIdx.x & 63) == (uint32_t)__ffsll((unsigned long long)w.in) - 1)
+      atomicAdd(&cnt[id], (uint32_t)__popcll(w.in));
+  } else if (id < n_ids) {
+    atomicAdd(&cnt[id], 1u);
+  }
+}
+
+// Counts rows [lo, hi) into cnt with the whole workgroup.
+__device__ __forceinline__ void rp_count_all(const int32_t* ids, int64_t lo, int64_t hi, uint32_t n_ids, uint32_t* cnt) {
+  for (int64_t i0 = lo; i0 < hi; i0 += 16 * RP_WG) {
+    uint32_t id[16];                         // sixteen loads in flight
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int64_t i = i0 + j * RP_WG + threadIdx.x;
+      id[j] = i < hi ? (uint32_t)ids[i] : 0xFFFFFFFFu;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (i0 + j * RP_WG < hi) rp_add(cnt, id[j], n_ids);
   }
 }
 
 __global__ __launch_bounds__(RP_WG) void k_row_hist(const int32_t* __restrict__ ids, int64_t n, int64_t per,
                                                     uint32_t n_ids, uint32_t* __restrict__ hist) {
   __shared__ uint32_t cnt[RP_IDS];
-  for (uint32_t i = threadIdx.x; i < n_ids; i += RP_WG) cnt[i] = 0;
+  for (uint32_t i = threadIdx.x; i < rp_pitch(n_ids); i += RP_WG) cnt[i] = 0;
   __syncthreads();
   const int64_t lo = (int64_t)blockIdx.x * per, hi = lo + per < n ? lo + per : n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += RP_WG) {
-    const uint32_t id = (uint32_t)ids[i];
-    if (id < n_ids) atomicAdd(&cnt[id], 1u);
-  }
+  rp_count_all(ids, lo, hi, n_ids, cnt);
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < n_ids; i += RP_WG) hist[(int64_t)blockIdx.x * n_ids + i] = cnt[i];
+  for (uint32_t i = threadIdx.x; i < rp_pitch(n_ids); i += RP_WG) hist[(int64_t)blockIdx.x * rp_pitch(n_ids) + i] = cnt[i];
 }
 
 // Exclusive prefix sums of two values per id, ids 2 * thread and 2 * thread + 1.
@@ -75,15 +107,65 @@ __device__ __forceinline__ uint2 rp_scan(uint32_t a, uint32_t b, uint2* wave_sum
 
 __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
   __shared__ uint32_t cnt[RP_WAVES][RP_IDS];       // counts, then the next position, per wave and id
+  __shared__ uint32_t all[RP_IDS], prior[RP_IDS];  // rows of an id: in all, in the workgroups before this one
   __shared__ uint32_t off[RP_IDS + 1], toff[RP_IDS + 1];
   __shared__ uint2 wave_sum[RP_WAVES];
   const uint32_t n_ids = (uint32_t)a.n_ids, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint32_t i = threadIdx.x; i < n_ids * RP_WAVES; i += RP_WG) cnt[i / n_ids][i % n_ids] = 0;
-  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < RP_IDS; i += RP_WG) {
+    all[i] = 0;
+    prior[i] = 0;
+#pragma unroll
+    for (int w = 0; w < RP_WAVES; ++w) cnt[w][i] = 0;
+  }
   const int64_t lo = (int64_t)blockIdx.x * a.per, hi = lo + a.per < a.n ? lo + a.per : a.n;
   const int64_t part = a.per / RP_WAVES, wlo = lo + wave * part;      // per is a multiple of 8 x 64
   const int64_t whi = wlo + part < hi ? wlo + part : hi;
-  rp_count(a.ids, wlo, whi, n_ids, cnt[wave]);
+  uint32_t held[RP_HELD];                                             // the wave's first rows
+#pragma unroll
+  for (int j = 0; j < RP_HELD; ++j) {
+    const int64_t i = wlo + j * 64 + lane;
+    held[j] = i < whi ? (uint32_t)a.ids[i] : 0xFFFFFFFFu;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < RP_HELD; ++j)
+    if (wlo + j * 64 < whi) rp_add(cnt[wave], held[j], n_ids);
+  for (int64_t i0 = wlo + RP_HELD * 64; i0 < whi; i0 += 64)
+    rp_add(cnt[wave], i0 + lane < whi ? (uint32_t)a.ids[i0 + lane] : 0xFFFFFFFFu, n_ids);
+  if (a.hist) {
+    // two ids per thread and, where there are fewer ids than that, several parts of the workgroups
+    uint32_t pairs = 1;
+    while (pairs * 2 < n_ids) pairs *= 2;
+    const uint32_t id = (threadIdx.x & (pairs - 1)) * 2, pitch = rp_pitch(n_ids);
+    if (id < n_ids) {
+      uint2 s = {0, 0}, p = {0, 0};
+      for (uint32_t b0 = threadIdx.x / pairs; b0 < gridDim.x; b0 += 16 * (RP_WG / pairs)) {
+        uint2 h[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t b = b0 + j * (RP_WG / pairs);
+          h[j] = b < gridDim.x ? *reinterpret_cast<const uint2*>(a.hist + (int64_t)b * pitch + id) : uint2{0, 0};
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const bool earlier = b0 + j * (RP_WG / pairs) < blockIdx.x;
+          s.x += h[j].x;
+          s.y += h[j].y;
+          p.x += earlier ? h[j].x : 0;
+          p.y += earlier ? h[j].y : 0;
+        }
+      }
+      atomicAdd(&all[id], s.x);
+      atomicAdd(&prior[id], p.x);
+      if (id + 1 < n_ids) {
+        atomicAdd(&all[id + 1], s.y);
+        atomicAdd(&prior[id + 1], p.y);
+      }
+    }
+  } else {
+    rp_count_all(a.ids, 0, lo, n_ids, prior);
+    rp_count_all(a.ids, hi, a.n, n_ids, all);          // the later ones; the rest is added below
+  }
   __syncthreads();
 
   uint32_t before[2] = {0, 0}, total[2] = {0, 0}, tiles[2];
@@ -91,15 +173,12 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
   for (int j = 0; j < 2; ++j) {
     const uint32_t id = threadIdx.x * 2 + j;
     if (id < n_ids) {
-      if (gridDim.x == 1) {
+      before[j] = prior[id];
+      total[j] = all[id];
+      if (!a.hist) {
+        total[j] += before[j];
+#pragma unroll
         for (int w = 0; w < RP_WAVES; ++w) total[j] += cnt[w][id];
-      } else {
-#pragma unroll 8
-        for (uint32_t b = 0; b < gridDim.x; ++b) {
-          const uint32_t h = a.hist[(int64_t)b * n_ids + id];
-          total[j] += h;
-          if (b < blockIdx.x) before[j] += h;
-        }
       }
     }
     tiles[j] = (total[j] + QF_ROW_TILE - 1) / QF_ROW_TILE;
@@ -117,6 +196,7 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
         toff[n_ids] = t + tiles[j];
       }
       uint32_t next = o + before[j];
+#pragma unroll
       for (int w = 0; w < RP_WAVES; ++w) {
         const uint32_t c = cnt[w][id];
         cnt[w][id] = next;
@@ -131,13 +211,23 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
   while ((1u << bits) < n_ids) ++bits;
   for (int64_t i0 = wlo; i0 < whi; i0 += 64) {
     const int64_t i = i0 + lane;
-    const uint32_t id = i < whi ? (uint32_t)a.ids[i] : 0xFFFFFFFFu;
-    const bool in = id < n_ids;
-    uint64_t peers = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __ballot((id >> b) & 1u);
-      peers &= ((id >> b) & 1u) ? set : ~set;
+    const int step = (int)((i0 - wlo) >> 6);
+    uint32_t id;
+    if (step < RP_HELD) {
+      id = held[0];
+#pragma unroll
+      for (int j = 1; j < RP_HELD; ++j) id = step == j ? held[j] : id;
+    } else {
+      id = i < whi ? (uint32_t)a.ids[i] : 0xFFFFFFFFu;
     }
+    const bool in = id < n_ids;
+    const RpWave w = rp_wave(id, n_ids);
+    uint64_t peers = w.in;
+    if (!w.one)
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((id >> b) & 1u);
+        peers &= ((id >> b) & 1u) ? set : ~set;
+      }
     const uint32_t rank = __popcll(peers & ((1ull << lane) - 1ull));
     uint32_t at = 0;
     if (in && rank == 0) at = atomicAdd(&cnt[wave][id], (uint32_t)__popcll(peers));
@@ -169,13 +259,21 @@ hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s) {
   int64_t per;
   const int wgs = row_plan_wgs(a.n, &per);
   a.per = per;
-  if (wgs > 1) {
+  if (a.n > RP_ONE_LAUNCH) {
     k_row_hist<<<wgs, RP_WG, 0, s>>>(a.ids, a.n, per, (uint32_t)a.n_ids, a.hist);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+  } else {
+    a.hist = nullptr;
   }
   k_row_plan<<<wgs, RP_WG, 0, s>>>(a);
   return hipGetLastError();
+}
+
+size_t row_plan_hist_bytes(int64_t n, int n_ids) {
+  if (n <= RP_ONE_LAUNCH) return 0;
+  int64_t per;
+  return (size_t)row_plan_wgs(n, &per) * rp_pitch((uint32_t)n_ids) * 4;
 }
 
 }  // namespace qf
@@ -189,9 +287,7 @@ int64_t qf_row_plan_tiles(int64_t n, int n_ids) {
 
 size_t qf_row_plan_workspace(int64_t n, int n_ids) {
   if (n < 0 || n >= QF_ROW_MAX_ROWS || n_ids < 1 || n_ids > QF_ROW_MAX_IDS) return 0;
-  int64_t per;
-  const int wgs = qf::row_plan_wgs(n, &per);
-  return wgs > 1 ? (size_t)wgs * n_ids * 4 : 0;
+  return qf::row_plan_hist_bytes(n, n_ids);
 }
 
 qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
@@ -199,9 +295,9 @@ qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets
   if (n < 0 || n >= QF_ROW_MAX_ROWS) return QF_ERR_SHAPE;
   if (n_ids < 1 || n_ids > QF_ROW_MAX_IDS) return QF_ERR_ARG;
   if (!offsets || (n > 0 && (!ids || !order || !tiles))) return QF_ERR_NULL;
-  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)order | (uintptr_t)ws) % 4 || (uintptr_t)tiles % 8)
-    return QF_ERR_ALIGN;
   const size_t need = qf_row_plan_workspace(n, n_ids);
+  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)order) % 4 || (uintptr_t)tiles % 8 || (need > 0 && (uintptr_t)ws % 8))
+    return QF_ERR_ALIGN;
   if (need > 0 && (!ws || ws_bytes < need)) return QF_ERR_WORKSPACE;
   qf::RowPlanArgs a;
   a.ids = ids;

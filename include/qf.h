@@ -454,7 +454,7 @@ qf_status qf_moe_route_backward(const qf_route_desc* d, const int32_t* indices, 
  *            ascending; {-1, 0} behind the last.
  * A plan serves every call over the same rows (all projections of all layers).  0 <= n <
  * QF_ROW_MAX_ROWS (QF_ERR_SHAPE), 1 <= n_ids <= QF_ROW_MAX_IDS (QF_ERR_ARG).  n == 0 writes
- * zero offsets.  ws: qf_row_plan_workspace bytes (0 for small plans).  One or two launches;
+ * zero offsets.  ws: qf_row_plan_workspace bytes (0 for small plans), 8-byte aligned.  One or two launches;
  * outputs do not depend on scheduling. */
 #define QF_ROW_TILE 32
 #define QF_ROW_MAX_IDS 1024

@@ -26,7 +26,7 @@ def check_plan(ids, n_ids):
     return p
 
 
-@pytest.mark.parametrize("n", [0, 1, 31, 64, 65, 511, 513, 4096, 4097, 6000, 131072, 140001])
+@pytest.mark.parametrize("n", [0, 1, 31, 64, 65, 511, 513, 2048, 2049, 6000, 32768, 32769, 131072, 300001])
 @pytest.mark.parametrize("n_ids", [1, 2, 5, 128, 1000, 1024])
 def test_plan(n, n_ids):
     check_plan(ids_of(n, n_ids, n + n_ids, runs=n % 2 == 1), n_ids)

@@ -64,6 +64,7 @@ def test_row_plan_refusals():
     need = L.qf_row_plan_workspace(100000, 8)
     assert need > 0 and L.qf_row_plan_workspace(4096, 8) == 0
     assert call(n=100000) == 4 and call(n=100000, ws=ws, wsb=need - 1) == 4
+    assert call(n=100000, ws=P(0x10000004), wsb=need) == 3
     assert L.qf_row_plan_workspace(5, 0) == 0 and L.qf_row_plan_tiles(-1, 4) == 0 and L.qf_row_plan_tiles(5, 1025) == 0
 
 
