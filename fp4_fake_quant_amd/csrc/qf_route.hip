@@ -83,10 +83,13 @@ __device__ __forceinline__ void rt_load(const uint16_t* row, int e0, int E, floa
   }
 }
 
+// Groups: none, each a power of two of whole lanes (WHOLE), or any.
+enum { RT_NO_GROUPS = 0, RT_WHOLE = 1, RT_ANY = 2 };
+
 // LDS of a wave's group ranking.
-template <int L, int V, typename K>
+template <int L, int V, int GROUPS, typename K>
 struct RtGroups {
-  K keys[RT_WAVE / L * L * V];
+  K keys[GROUPS == RT_ANY ? RT_WAVE / L * L * V : 1];
   K score[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
   uint8_t keep[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
 };
@@ -99,17 +102,16 @@ __device__ __forceinline__ void rt_top2(K& m1, K& m2, K v) {
 
 // Keeps only the experts of the best groups: the others' keys become minus infinity.  False
 // where a kept and a dropped group differ by no more than margin.
-template <int L, int V, typename K>
-__device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane, K (&key)[V], RtGroups<L, V, K>& s, K margin) {
+template <int L, int V, int GROUPS, typename K>
+__device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane, K (&key)[V], RtGroups<L, V, GROUPS, K>& s,
+                                          K margin) {
   const int size = a.E / a.n_group;
   const K none = -(K)RT_INF;
-  K* keys = s.keys + sub * (L * V);
+  K* keys = s.keys + (GROUPS == RT_ANY ? sub * (L * V) : 0);
   K* score = s.score + sub * QF_ROUTE_MAX_GROUPS;
   uint8_t* keep = s.keep + sub * QF_ROUTE_MAX_GROUPS;
-  // a group is a power of two of whole lanes: its two best by exchange
   const int lanes = size / V;
-  const bool whole = size % V == 0 && (lanes & (lanes - 1)) == 0;
-  if (whole) {
+  if (GROUPS == RT_WHOLE) {                    // a group's two best by exchange
     K m1 = none, m2 = none;
 #pragma unroll
     for (int i = 0; i < V; ++i) rt_top2(m1, m2, key[i]);
@@ -147,7 +149,7 @@ __device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane,
   __syncthreads();
   worst = -rt_row_max<L>(-worst);
   best = rt_row_max<L>(best);
-  if (whole) {
+  if (GROUPS == RT_WHOLE) {
     const bool in = lane * V < a.E && keep[lane / lanes];
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = in ? key[i] : none;
@@ -204,13 +206,13 @@ __device__ __forceinline__ uint32_t rt_row_umax(uint32_t v) {
   return v;
 }
 
-// Fast selection by keys below 2^31 (0: never chosen): each round takes the largest key below
+// Fast selection by keys below 2^31 (below `least`: never chosen): each round takes the largest key below
 // the last one, which is the largest of key - last as an unsigned number (all keys above wrap
 // to small differences).  IDX low bits of a key are its place: in the lane, or in the row.
 // close(last, next): whether the values of two neighbours cannot be told apart.
 template <int L, int V, int IDX, bool IN_ROW, typename F>
-__device__ __forceinline__ bool rt_select_keys(const RouteArgs& a, int lane, const uint32_t (&key)[V], int32_t* chosen,
-                                               F close) {
+__device__ __forceinline__ bool rt_select_keys(const RouteArgs& a, int lane, const uint32_t (&key)[V], uint32_t least,
+                                               int32_t* chosen, F close) {
   uint32_t last = 0x80000000u;
   bool sure = true;
   const int rounds = IN_ROW ? a.k : a.k + 1;                // one more neighbour decides the last choice
@@ -219,7 +221,8 @@ __device__ __forceinline__ bool rt_select_keys(const RouteArgs& a, int lane, con
 #pragma unroll
     for (int i = 0; i < V; ++i) mine = umax(mine, key[i] - last);
     const uint32_t row = rt_row_umax<L>(mine);
-    const uint32_t next = row >= 0x80000000u ? last + row : 0;    // 0 also when nothing is below
+    uint32_t next = row >= 0x80000000u ? last + row : 0;          // nothing is below: 0
+    next = next < least ? 0 : next;
     if (!IN_ROW) {
       if (j > 0 && next != 0) sure = sure && !close(last, next);
       // a key that two lanes of a row have: more holders than rows
@@ -243,14 +246,14 @@ constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
 __device__ __forceinline__ float rt_fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 // SCORES: choose by scores plus bias, else by logits.
-template <int L, int V, typename X, bool SCORES, bool VEC, bool GROUPS>
+template <int L, int V, typename X, bool SCORES, bool VEC, int GROUPS>
 __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
   constexpr int ROWS = RT_WAVE / L;
   constexpr bool IN_ROW = !SCORES && sizeof(X) == 2;       // logit and index fit a key
   using K2 = typename std::conditional<SCORES, double, float>::type;   // the second pass's keys
   __shared__ int32_t chosen[ROWS][QF_ROUTE_MAX_K];
-  __shared__ typename std::conditional<GROUPS, RtGroups<L, V, K2>, char>::type gs2;
-  __shared__ typename std::conditional<GROUPS && SCORES, RtGroups<L, V, float>, char>::type gs1;
+  __shared__ typename std::conditional<GROUPS != 0, RtGroups<L, V, GROUPS, K2>, char>::type gs2;
+  __shared__ typename std::conditional<GROUPS != 0 && SCORES, RtGroups<L, V, GROUPS, float>, char>::type gs1;
   const int lane = threadIdx.x % L, sub = threadIdx.x / L;
   const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
   const bool live = t < a.T;
@@ -290,13 +293,18 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = __builtin_amdgcn_rcpf(1.0f + rt_fast_exp(-x[i]));
   }
+  float bias[V];
   if (SCORES) {
+    if (a.bias) {
+      rt_load<V, VEC>(a.bias, lane * V, a.E, bias);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) bias[i] = 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (a.bias && e < a.E) v[i] += a.bias[e];
-      if (x[i] == -RT_INF) v[i] = -RT_INF;
-      bad |= !(v[i] < RT_INF);
+      bad |= !(bias[i] < RT_INF);
+      v[i] = x[i] > -RT_INF ? v[i] + bias[i] : -RT_INF;
     }
   }
   const uint64_t seg = ((1ull << L) - 1ull) << (sub * L);
@@ -307,28 +315,28 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
   // roundings most of all); the bias adds half a unit of the key.  Twice that for a pair.
   const float err = SCORES ? (softmax ? 0x1p-18f * (total > 0.0f ? 1.0f / total : 0.0f) : 0x1p-20f) : 0.0f;
   bool sure = true;
-  if constexpr (GROUPS) {
+  if constexpr (GROUPS != 0) {
     if constexpr (SCORES) {
       float big = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) big = fmaxf(big, v[i] > -RT_INF ? __builtin_fabsf(v[i]) : 0.0f);
-      sure = rt_groups<L, V, float>(a, sub, lane, v, gs1, 2.0f * err + 0x1p-21f * rt_row_max<L>(big));
+      sure = rt_groups<L, V, GROUPS, float>(a, sub, lane, v, gs1, 2.0f * err + 0x1p-21f * rt_row_max<L>(big));
     } else {
-      rt_groups<L, V, float>(a, sub, lane, v, gs2, 0.0f);
+      rt_groups<L, V, GROUPS, float>(a, sub, lane, v, gs2, 0.0f);
     }
   }
   uint32_t key[V];
   constexpr int IDX = IN_ROW ? 10 : rt_log2(V);
+  constexpr uint32_t LOW = (1u << IDX) - 1u;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const uint32_t o = rt_order(v[i]);
-    key[i] = IN_ROW ? ((o >> 16) << IDX | (uint32_t)((1 << IDX) - 1 - (lane * V + i)))
-                    : ((o >> (IDX + 1)) << IDX | (uint32_t)(V - 1 - i));
-    if (!(v[i] > -RT_INF)) key[i] = 0;
-  }
-  sure = rt_select_keys<L, V, IDX, IN_ROW>(a, lane, key, chosen[sub], [&](uint32_t last, uint32_t next) {
+  for (int i = 0; i < V; ++i)
+    key[i] = IN_ROW ? ((rt_order(v[i]) >> 16) << IDX | (LOW - (uint32_t)(lane * V + i)))
+                    : ((rt_order(v[i]) >> 1) & ~LOW) | (LOW - (uint32_t)i);
+  // the smallest finite value's key: minus infinity is the one before it in order
+  constexpr uint32_t least = IN_ROW ? (0x0080u << IDX) : (0x00800000u >> 1);
+  sure = rt_select_keys<L, V, IDX, IN_ROW>(a, lane, key, least, chosen[sub], [&](uint32_t last, uint32_t next) {
     if (!SCORES) return (last >> IDX) == (next >> IDX);
-    const float hi = rt_unorder((last >> IDX) << (IDX + 1)), lo = rt_unorder((next >> IDX) << (IDX + 1));
+    const float hi = rt_unorder((last & ~LOW) << 1), lo = rt_unorder((next & ~LOW) << 1);
     // truncation takes up to 2^(IDX + 1) units of 2^-23 of a value
     return !(hi - lo > err + fmaxf(__builtin_fabsf(hi), __builtin_fabsf(lo)) * (0x1p-22f * (1 << IDX) + 0x1p-22f));
   }) && sure;
@@ -346,12 +354,10 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
         if (softmax) sum = rt_row_sum<L>(sum);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int e = lane * V + i;
           if (softmax) key2[i] = key2[i] / sum;
-          if (a.bias && e < a.E) key2[i] += (double)a.bias[e];
-          if (x[i] == -RT_INF) key2[i] = -(double)RT_INF;
+          key2[i] = x[i] > -RT_INF ? key2[i] + (double)bias[i] : -(double)RT_INF;
         }
-        if constexpr (GROUPS) rt_groups<L, V, K2>(a, sub, lane, key2, gs2, 0.0);
+        if constexpr (GROUPS != 0) rt_groups<L, V, GROUPS, K2>(a, sub, lane, key2, gs2, 0.0);
       } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) key2[i] = v[i];          // the groups' choice was exact
@@ -475,12 +481,15 @@ template <int L, int V, typename X, bool S>
 void route_go(const RouteArgs& a, bool vec, hipStream_t s) {
   constexpr int ROWS = RT_WAVE / L;
   const unsigned grid = (unsigned)((a.T + ROWS - 1) / ROWS);
-  if (a.n_group > 1) {
-    if (vec) k_route<L, V, X, S, true, true><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, S, false, true><<<grid, RT_WAVE, 0, s>>>(a);
+  const int size = a.E / a.n_group, lanes = size / V;
+  if (a.n_group > 1 && vec && size % V == 0 && (lanes & (lanes - 1)) == 0) {
+    k_route<L, V, X, S, true, RT_WHOLE><<<grid, RT_WAVE, 0, s>>>(a);
+  } else if (a.n_group > 1) {
+    if (vec) k_route<L, V, X, S, true, RT_ANY><<<grid, RT_WAVE, 0, s>>>(a);
+    else k_route<L, V, X, S, false, RT_ANY><<<grid, RT_WAVE, 0, s>>>(a);
   } else {
-    if (vec) k_route<L, V, X, S, true, false><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, S, false, false><<<grid, RT_WAVE, 0, s>>>(a);
+    if (vec) k_route<L, V, X, S, true, RT_NO_GROUPS><<<grid, RT_WAVE, 0, s>>>(a);
+    else k_route<L, V, X, S, false, RT_NO_GROUPS><<<grid, RT_WAVE, 0, s>>>(a);
   }
 }
 // Few lanes with many logits each: a round's work over the lanes' logits is shared by more rows.
@@ -497,7 +506,8 @@ void route_size(const RouteArgs& a, bool vec, hipStream_t s) {
 hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s) {
   const bool scores = a.bias != nullptr || (a.n_group > 1 && a.group_top2);
   const int64_t sz = bf16 ? 2 : 4;
-  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (4 * sz) == 0;
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && (uintptr_t)a.logits % (4 * sz) == 0 &&
+                   (uintptr_t)a.bias % 16 == 0;
   if (bf16) {
     if (scores) route_size<uint16_t, true>(a, vec, s);
     else route_size<uint16_t, false>(a, vec, s);
