@@ -16,6 +16,7 @@
 // again, on the fp32 logits themselves or on 64-bit scores.  bf16 logits fit a key with their
 // index and need no second pass.  The selection is bounded by vector instructions (k + 1 rounds
 // of about 40), the rest by memory.
+#include <algorithm>
 #include <type_traits>
 
 #include "qf_device.h"
@@ -94,10 +95,13 @@ struct RtGroups {
   uint8_t keep[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
 };
 
-template <typename K>
-__device__ __forceinline__ void rt_top2(K& m1, K& m2, K v) {
+__device__ __forceinline__ void rt_top2(double& m1, double& m2, double v) {
   m2 = v > m1 ? m1 : (v > m2 ? v : m2);
   m1 = v > m1 ? v : m1;
+}
+__device__ __forceinline__ void rt_top2(float& m1, float& m2, float v) {
+  m2 = __builtin_amdgcn_fmed3f(m1, m2, v);
+  m1 = fmaxf(m1, v);
 }
 
 // Keeps only the experts of the best groups: the others' keys become minus infinity.  False
@@ -206,39 +210,36 @@ __device__ __forceinline__ uint32_t rt_row_umax(uint32_t v) {
   return v;
 }
 
-// Fast selection by keys below 2^31 (below `least`: never chosen): each round takes the largest key below
-// the last one, which is the largest of key - last as an unsigned number (all keys above wrap
-// to small differences).  IDX low bits of a key are its place: in the lane, or in the row.
-// close(last, next): whether the values of two neighbours cannot be told apart.
-template <int L, int V, int IDX, bool IN_ROW, typename F>
-__device__ __forceinline__ bool rt_select_keys(const RouteArgs& a, int lane, const uint32_t (&key)[V], uint32_t least,
-                                               int32_t* chosen, F close) {
+// Fast selection by keys below 2^31: each round takes the largest key below the last one,
+// which is the largest of key - last as an unsigned number (all keys above wrap to small
+// differences).  The j-th key ends up in lane j % L, register j / L, and unless places[] is null
+// the lane that holds it writes its index there.  Where nothing is left the keys are below
+// `least`, minus infinity's.  False if two lanes of a row hold an equal valid key (only one
+// counts then).
+template <int L, int V, int P>
+__device__ __forceinline__ bool rt_select_keys(int rounds, int lane, const uint32_t (&key)[V], uint32_t least, int top_index,
+                                               uint32_t low, int32_t* places, uint32_t (&held)[P]) {
   uint32_t last = 0x80000000u;
-  bool sure = true;
-  const int rounds = IN_ROW ? a.k : a.k + 1;                // one more neighbour decides the last choice
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t mine = 0;
+  int holders = 0, valid = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) mine = umax(mine, key[i] - last);
-    const uint32_t row = rt_row_umax<L>(mine);
-    uint32_t next = row >= 0x80000000u ? last + row : 0;          // nothing is below: 0
-    next = next < least ? 0 : next;
-    if (!IN_ROW) {
-      if (j > 0 && next != 0) sure = sure && !close(last, next);
-      // a key that two lanes of a row have: more holders than rows
-      if (__popcll(__ballot(next != 0 && mine == row)) > __popcll(__ballot(next != 0 && lane == 0))) sure = false;
-    }
-    if (j < a.k) {
-      if (next == 0) {
-        if (lane == 0) chosen[j] = -1;
-      } else if (mine == row) {
-        chosen[j] = IN_ROW ? (1 << IDX) - 1 - (int)(next & ((1u << IDX) - 1u))
-                           : lane * V + V - 1 - (int)(next & ((1u << IDX) - 1u));
+  for (int p = 0; p < P; ++p) {
+    held[p] = 0;
+    for (int i = 0; i < L && p * L + i < rounds; ++i) {
+      uint32_t mine = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine = umax(mine, key[v] - last);
+      const uint32_t row = rt_row_umax<L>(mine);
+      last = (last + row) & (uint32_t)((int32_t)row >> 31);      // 0 when nothing is below
+      held[p] = lane == i ? last : held[p];
+      const bool ok = last >= least;
+      if (places != nullptr && mine == row && ok) {
+        places[p * L + i] = top_index - (int)(last & low);
+        ++holders;
       }
+      valid += ok;
     }
-    last = next;
   }
-  return sure;
+  return places == nullptr || rt_row_sum<L>(holders) == valid;
 }
 
 constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
@@ -251,7 +252,7 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
   constexpr int ROWS = RT_WAVE / L;
   constexpr bool IN_ROW = !SCORES && sizeof(X) == 2;       // logit and index fit a key
   using K2 = typename std::conditional<SCORES, double, float>::type;   // the second pass's keys
-  __shared__ int32_t chosen[ROWS][QF_ROUTE_MAX_K];
+  __shared__ int32_t chosen[ROWS][QF_ROUTE_MAX_K + 1];
   __shared__ typename std::conditional<GROUPS != 0, RtGroups<L, V, GROUPS, K2>, char>::type gs2;
   __shared__ typename std::conditional<GROUPS != 0 && SCORES, RtGroups<L, V, GROUPS, float>, char>::type gs1;
   const int lane = threadIdx.x % L, sub = threadIdx.x / L;
@@ -261,20 +262,14 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
   float x[V];
   rt_load<V, VEC>(row, lane * V, live ? a.E : 0, x);
 
-  // a NaN or plus infinity poisons its row
-  bool bad = false;
-  float top = -RT_INF;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bad |= !(x[i] < RT_INF);
-    top = fmaxf(top, x[i]);
-  }
-  float total = 0.0f;              // softmax: the sum of exp(x - top), when it is needed
+  float top = -RT_INF, total = 0.0f;       // softmax: the sum of exp(x - top), when it is needed
   const bool softmax = a.scoring == QF_ROUTE_SOFTMAX;
   float v[V];                      // what is compared
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = x[i];
   if (softmax && (SCORES || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
     top = rt_row_max<L>(top);
     if (top == -RT_INF) top = 0.0f;        // nothing but masked experts: every exp is 0
     float e[V];
@@ -302,13 +297,20 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
       for (int i = 0; i < V; ++i) bias[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      bad |= !(bias[i] < RT_INF);
-      v[i] = x[i] > -RT_INF ? v[i] + bias[i] : -RT_INF;
-    }
+    for (int i = 0; i < V; ++i) v[i] = x[i] == -RT_INF ? -RT_INF : v[i] + bias[i];
+  }
+  // a NaN or plus infinity poisons its row: as integers, positive ones are the largest signed
+  // numbers, and negative NaN lies above minus infinity among the unsigned
+  int32_t most = INT32_MIN;
+  uint32_t mostu = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    most = std::max(most, (int32_t)__float_as_uint(v[i]));
+    if (SCORES) most = std::max(most, (int32_t)__float_as_uint(x[i]));
+    mostu = umax(mostu, __float_as_uint(v[i]));
   }
   const uint64_t seg = ((1ull << L) - 1ull) << (sub * L);
-  bad = (__ballot(bad) & seg) != 0;
+  const bool bad = (__ballot(most >= 0x7F800000 || mostu > 0xFF800000u) & seg) != 0;
 
   // The fp32 score's error: sigmoid, 5 units of 2^-24 (exp2 and its argument, sum, reciprocal,
   // each weighed by s or s (1 - s)); softmax, 32 units of the largest score (the sum's
@@ -334,12 +336,38 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
                     : ((rt_order(v[i]) >> 1) & ~LOW) | (LOW - (uint32_t)i);
   // the smallest finite value's key: minus infinity is the one before it in order
   constexpr uint32_t least = IN_ROW ? (0x0080u << IDX) : (0x00800000u >> 1);
-  sure = rt_select_keys<L, V, IDX, IN_ROW>(a, lane, key, least, chosen[sub], [&](uint32_t last, uint32_t next) {
-    if (!SCORES) return (last >> IDX) == (next >> IDX);
-    const float hi = rt_unorder((last & ~LOW) << 1), lo = rt_unorder((next & ~LOW) << 1);
-    // truncation takes up to 2^(IDX + 1) units of 2^-23 of a value
-    return !(hi - lo > err + fmaxf(__builtin_fabsf(hi), __builtin_fabsf(lo)) * (0x1p-22f * (1 << IDX) + 0x1p-22f));
-  }) && sure;
+  constexpr int P = (QF_ROUTE_MAX_K + 1 + L - 1) / L, PER = (QF_ROUTE_MAX_K + L - 1) / L;
+  uint32_t held[P];
+  // one round more than choices: the next key decides the last choice
+  const int rounds = IN_ROW ? a.k : a.k + 1;
+  sure = rt_select_keys<L, V, P>(rounds, lane, key, least, lane * V + V - 1, LOW, IN_ROW ? nullptr : chosen[sub], held) && sure;
+  int id[PER];
+  if constexpr (IN_ROW) {
+#pragma unroll
+    for (int p = 0; p < PER; ++p) id[p] = held[p] >= least ? (int)(LOW - (held[p] & LOW)) : -1;
+  } else {
+    // neighbours in the order, each pair in the first one's lane
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      uint32_t next = __shfl_down(held[p], 1, L);
+      if (p + 1 < P) {
+        const uint32_t wrap = __shfl(held[p + 1 < P ? p + 1 : p], 0, L);
+        next = lane == L - 1 ? wrap : next;
+      }
+      if (lane + p * L < a.k && next >= least) {
+        bool close = (held[p] & ~LOW) == (next & ~LOW);
+        if (SCORES) {
+          const float hi = rt_unorder((held[p] & ~LOW) << 1), lo = rt_unorder((next & ~LOW) << 1);
+          // truncation takes up to 2^(IDX + 1) units of 2^-23 of a value
+          close = !(hi - lo > err + fmaxf(__builtin_fabsf(hi), __builtin_fabsf(lo)) * (0x1p-22f * (1 << IDX) + 0x1p-22f));
+        }
+        sure = sure && !close;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < PER; ++p) id[p] = held[p] >= least && lane + p * L < a.k ? chosen[sub][lane + p * L] : -1;
+  }
 
   if constexpr (!IN_ROW) {
     if (__ballot(!sure && !bad && live) != 0) {
@@ -363,19 +391,19 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
         for (int i = 0; i < V; ++i) key2[i] = v[i];          // the groups' choice was exact
       }
       rt_select<L, V, K2>(a, lane, seg, key2, chosen[sub]);
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < PER; ++p) id[p] = lane + p * L < a.k ? chosen[sub][lane + p * L] : -1;
     }
   }
-  __syncthreads();
 
   // weights: lane j (and j + L) of a row has its j-th choice
-  constexpr int PER = (QF_ROUTE_MAX_K + L - 1) / L;
-  int id[PER];
   float u[PER], xs[PER];
   float first = -RT_INF;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int j = lane + p * L;
-    id[p] = live && !bad && j < a.k ? chosen[sub][j] : -1;
+    if (!live || bad || j >= a.k) id[p] = -1;
     xs[p] = id[p] >= 0 ? rt_logit(row, id[p]) : -RT_INF;
     first = fmaxf(first, xs[p]);
   }
