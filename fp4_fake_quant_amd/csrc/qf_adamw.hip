@@ -64,12 +64,25 @@ __device__ __forceinline__ uint32_t aw_wave_max(uint32_t v) {
   return umax((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 32));
 }
 
-// E4M3 magnitude code of y >= 0 (at most 448), rounded up with probability (distance to the
-// code below) / step: rnd holds 16 random bits, added below the kept mantissa bits.
+// E4M3 magnitude code of y in [0, 448 (1 + 2^-21)], rounded up with probability (distance to the
+// code below) / step: rnd holds 16 random bits, added below the kept mantissa bits.  512 y and
+// rnd / 65536 are exact, so the one rounding of the fused sum is the sum's; y just above 448 has
+// too few bits there for rnd to carry.
 __device__ __forceinline__ uint32_t aw_e4m3_stochastic(float y, uint32_t rnd) {
-  const uint32_t small = (uint32_t)(int)__builtin_floorf(y * 512.0f + (float)rnd * 0x1p-16f);
+  const uint32_t small = (uint32_t)__builtin_fmaf(y, 512.0f, (float)rnd * 0x1p-16f);   // truncates: floor
   const uint32_t large = ((__float_as_uint(y) + (rnd << 4)) >> 20) - 960u;
-  return umin(y < 0.015625f ? small : large, 0x7Eu);
+  return y < 0.015625f ? small : large;
+}
+
+// The correctly rounded square root of v >= 0 that is 0 or at least 2^-96 (below, the residuals
+// underflow): the hardware's, which is at most one unit off, and its two neighbours tested by
+// the sign of v - s s'.
+__device__ __forceinline__ float aw_sqrt(float v) {
+  float s = __builtin_amdgcn_sqrtf(v);
+  const float down = __uint_as_float(__float_as_uint(s) - 1u), up = __uint_as_float(__float_as_uint(s) + 1u);
+  const float rd = __builtin_fmaf(-down, s, v), ru = __builtin_fmaf(-up, s, v);
+  s = rd <= 0.0f ? down : s;
+  return ru > 0.0f ? up : s;
 }
 
 struct AwScale {
@@ -84,19 +97,21 @@ __device__ __forceinline__ AwScale aw_block_scale(uint32_t top_bits) {
   return o;
 }
 
-// Four consecutive elements of an array with n left from here (n >= 4 in all but a tensor's
-// last lanes); missing ones read as zero.
+// Four consecutive elements of an array; unless FULL only `left` of them exist (the others read
+// as zero and are not written).
+template <bool FULL>
 __device__ __forceinline__ float4 aw_load4(const float* p, uint32_t left) {
-  if (left >= 4) return *reinterpret_cast<const float4*>(p);
+  if (FULL || left >= 4) return *reinterpret_cast<const float4*>(p);
   float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   if (left > 0) o.x = p[0];
   if (left > 1) o.y = p[1];
   if (left > 2) o.z = p[2];
   return o;
 }
+template <bool FULL>
 __device__ __forceinline__ float4 aw_load4(const uint16_t* p, uint32_t left) {
   uint2 w = {0u, 0u};
-  if (left >= 4) {
+  if (FULL || left >= 4) {
     w = *reinterpret_cast<const uint2*>(p);
   } else {
     if (left > 0) w.x = p[0];
@@ -105,25 +120,28 @@ __device__ __forceinline__ float4 aw_load4(const uint16_t* p, uint32_t left) {
   }
   return {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
 }
+template <bool FULL>
 __device__ __forceinline__ uint32_t aw_load4(const uint8_t* p, uint32_t left) {
-  if (left >= 4) return *reinterpret_cast<const uint32_t*>(p);
+  if (FULL || left >= 4) return *reinterpret_cast<const uint32_t*>(p);
   uint32_t w = 0;
   if (left > 0) w = p[0];
   if (left > 1) w |= (uint32_t)p[1] << 8;
   if (left > 2) w |= (uint32_t)p[2] << 16;
   return w;
 }
+template <bool FULL>
 __device__ __forceinline__ void aw_store4(float* p, const float (&v)[4], uint32_t left) {
-  if (left >= 4) {
+  if (FULL || left >= 4) {
     *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
     return;
   }
   for (uint32_t i = 0; i < 3; ++i)
     if (i < left) p[i] = v[i];
 }
+template <bool FULL>
 __device__ __forceinline__ void aw_store4(uint16_t* p, const float (&v)[4], uint32_t left) {
   const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
-  if (left >= 4) {
+  if (FULL || left >= 4) {
     *reinterpret_cast<uint2*>(p) = uint2{lo, hi};
     return;
   }
@@ -131,8 +149,9 @@ __device__ __forceinline__ void aw_store4(uint16_t* p, const float (&v)[4], uint
   if (left > 1) p[1] = (uint16_t)(lo >> 16);
   if (left > 2) p[2] = (uint16_t)hi;
 }
+template <bool FULL>
 __device__ __forceinline__ void aw_store4(uint8_t* p, uint32_t w, uint32_t left) {
-  if (left >= 4) {
+  if (FULL || left >= 4) {
     *reinterpret_cast<uint32_t*>(p) = w;
     return;
   }
@@ -140,37 +159,38 @@ __device__ __forceinline__ void aw_store4(uint8_t* p, uint32_t w, uint32_t left)
     if (i < left) p[i] = (uint8_t)(w >> (8 * i));
 }
 
-template <int BITS, typename G>
-__global__ __launch_bounds__(AW_WG) void k_adamw(AdamwArgs a) {
-  if (a.skip && *a.skip) return;
-  const uint32_t wg = blockIdx.x;
-  int ti = -1;
-#pragma unroll
-  for (int i = 0; i < AW_TENSORS; ++i) ti += wg >= a.begin[i];
-  const AdamwTensor& t = a.t[ti];
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * AW_PER_WAVE;   // first block of the wave
-  const uint32_t n = t.n;
+// The wave's blocks b0 .. b0 + 3 of one tensor; FULL: all of their elements exist.
+template <int BITS, typename G, bool FULL, typename Args>
+__device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, uint32_t b0, uint32_t lane) {
+  // uniform bases: the lane's part of every address is a small offset
+  const uint64_t first = (uint64_t)b0 * AW_BLOCK;
+  float* const tp = t.p + first;
+  const G* const tg = static_cast<const G*>(t.g) + first;
+  uint16_t* const tp16 = t.p16 ? t.p16 + first : nullptr;
+  float* const tm = static_cast<float*>(t.m) + (BITS == 8 ? 0 : first);
+  float* const tv = static_cast<float*>(t.v) + (BITS == 8 ? 0 : first);
+  uint8_t* const tmc = static_cast<uint8_t*>(t.m) + (BITS == 8 ? first : 0);
+  uint8_t* const tvc = static_cast<uint8_t*>(t.v) + (BITS == 8 ? first : 0);
+  const uint32_t n = FULL ? AW_PER_WAVE * AW_BLOCK : (uint32_t)(t.n - first);
 
   float4 p[AW_PER_WAVE], g[AW_PER_WAVE], m[AW_PER_WAVE], v[AW_PER_WAVE];
   uint32_t mc[AW_PER_WAVE], vc[AW_PER_WAVE];
   float ms[AW_PER_WAVE], vs[AW_PER_WAVE];
 #pragma unroll
   for (int j = 0; j < AW_PER_WAVE; ++j) {
-    const uint32_t at = (b0 + j) * AW_BLOCK + lane * 4;
+    const uint32_t at = j * AW_BLOCK + lane * 4;
     const uint32_t left = at < n ? n - at : 0;
-    p[j] = aw_load4(t.p + at, left);
-    g[j] = aw_load4(static_cast<const G*>(t.g) + at, left);
+    p[j] = aw_load4<FULL>(tp + at, left);
+    g[j] = aw_load4<FULL>(tg + at, left);
     if (BITS == 8) {
-      mc[j] = aw_load4(static_cast<const uint8_t*>(t.m) + at, left);
-      vc[j] = aw_load4(static_cast<const uint8_t*>(t.v) + at, left);
-      const bool in = (b0 + j) * AW_BLOCK < n;
+      mc[j] = aw_load4<FULL>(tmc + at, left);
+      vc[j] = aw_load4<FULL>(tvc + at, left);
+      const bool in = FULL || j * AW_BLOCK < n;
       ms[j] = in ? t.ms[b0 + j] : 0.0f;
       vs[j] = in ? t.vs[b0 + j] : 0.0f;
     } else {
-      m[j] = aw_load4(static_cast<const float*>(t.m) + at, left);
-      v[j] = aw_load4(static_cast<const float*>(t.v) + at, left);
+      m[j] = aw_load4<FULL>(tm + at, left);
+      v[j] = aw_load4<FULL>(tv + at, left);
     }
   }
 
@@ -181,13 +201,12 @@ __global__ __launch_bounds__(AW_WG) void k_adamw(AdamwArgs a) {
   const float b1 = (float)a.beta1, c1 = (float)(1.0 - a.beta1);
   const float b2 = (float)a.beta2, c2 = (float)(1.0 - a.beta2);
   const float eps = (float)a.eps;
-  const float gs = a.d_grad_scale ? *a.d_grad_scale : 1.0f;    // x * 1 is exact
 
   float ms_out[AW_PER_WAVE], vs_out[AW_PER_WAVE];
 #pragma unroll
   for (int j = 0; j < AW_PER_WAVE; ++j) {
-    if ((b0 + j) * AW_BLOCK >= n) break;                        // uniform over the wave
-    const uint32_t at = (b0 + j) * AW_BLOCK + lane * 4;
+    if (!FULL && j * AW_BLOCK >= n) break;                      // uniform over the wave
+    const uint32_t at = j * AW_BLOCK + lane * 4;
     const uint32_t left = at < n ? n - at : 0;
     if (BITS == 8) {
       const f32x2_t m01 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[j], false);
@@ -198,57 +217,89 @@ __global__ __launch_bounds__(AW_WG) void k_adamw(AdamwArgs a) {
       const float4 r = {r01.x * vs[j], r01.y * vs[j], r23.x * vs[j], r23.y * vs[j]};
       v[j] = float4{r.x * r.x, r.y * r.y, r.z * r.z, r.w * r.w};
     }
-    const float pi[4] = {p[j].x, p[j].y, p[j].z, p[j].w}, gi[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+    const float pi[4] = {p[j].x, p[j].y, p[j].z, p[j].w};
     const float mi[4] = {m[j].x, m[j].y, m[j].z, m[j].w}, vi[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+    float gi[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+    if (a.d_grad_scale) {
+      const float gs = *a.d_grad_scale;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) gi[e] *= gs;
+    }
     float po[4], mo[4], vo[4], ro[4];
+    uint32_t tiny = 0xFFFFFFFFu;                                // least v > 0; zeros wrap to the top
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float ge = gi[e] * gs;
-      mo[e] = mi[e] * b1 + ge * c1;
-      vo[e] = vi[e] * b2 + (ge * c2) * ge;
-      ro[e] = __builtin_sqrtf(vo[e]);
-      po[e] = pi[e] * keep - (mo[e] / (ro[e] * s.root + eps)) * s.size;
+      mo[e] = mi[e] * b1 + gi[e] * c1;
+      vo[e] = vi[e] * b2 + (gi[e] * c2) * gi[e];
+      tiny = umin(tiny, __float_as_uint(vo[e]) - 1u);
     }
-    aw_store4(t.p + at, po, left);
-    if (t.p16) aw_store4(t.p16 + at, po, left);
+    if (__builtin_expect(__ballot(tiny < 0x0F800000u - 1u) != 0, 0)) {   // some v below 2^-96
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ro[e] = __builtin_sqrtf(vo[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ro[e] = aw_sqrt(vo[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) po[e] = pi[e] * keep - (mo[e] / (ro[e] * s.root + eps)) * s.size;
+    aw_store4<FULL>(tp + at, po, left);
+    if (tp16) aw_store4<FULL>(tp16 + at, po, left);
     if (BITS == 8) {
       uint32_t mm = 0, rm = 0;                                  // non-negative floats order like their bits
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         mm = umax(mm, __float_as_uint(mo[e]) & 0x7FFFFFFFu);
-        rm = umax(rm, __float_as_uint(ro[e]) & 0x7FFFFFFFu);
+        rm = umax(rm, __float_as_uint(ro[e]));
       }
       const AwScale sm = aw_block_scale(aw_wave_max(mm)), sv = aw_block_scale(aw_wave_max(rm));
       ms_out[j] = sm.scale;
       vs_out[j] = sv.scale;
       uint32_t mw = 0, vw = 0;
+      const uint32_t key = s.key + (uint32_t)first + at;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t h = aw_hash(s.key + at + e);
-        const float my = fminf(__builtin_fabsf(mo[e]) * sm.inv, 448.0f), vy = fminf(ro[e] * sv.inv, 448.0f);
-        uint32_t cm = aw_e4m3_stochastic(my, h & 0xFFFFu), cv = aw_e4m3_stochastic(vy, h >> 16);
-        cm |= mo[e] < 0.0f ? 0x80u : 0u;
-        if (vy > 0.0f) cv = umax(cv, 1u);    // a zero would let the next step divide by a far too small root
+        const uint32_t h = aw_hash(key + e);
+        const float my = __builtin_fabsf(mo[e]) * sm.inv, vy = ro[e] * sv.inv;
+        const uint32_t sign = (__float_as_uint(mo[e]) >> 24) & 0x80u;
+        const uint32_t cm = aw_e4m3_stochastic(my, h & 0xFFFFu) | sign;
+        // no zero for v > 0: it would let the next step divide by a far too small root
+        const uint32_t cv = umax(aw_e4m3_stochastic(vy, h >> 16), umin(__float_as_uint(vy), 1u));
         mw |= cm << (8 * e);
         vw |= cv << (8 * e);
       }
-      aw_store4(static_cast<uint8_t*>(t.m) + at, mw, left);
-      aw_store4(static_cast<uint8_t*>(t.v) + at, vw, left);
+      aw_store4<FULL>(tmc + at, mw, left);
+      aw_store4<FULL>(tvc + at, vw, left);
     } else {
-      aw_store4(static_cast<float*>(t.m) + at, mo, left);
-      aw_store4(static_cast<float*>(t.v) + at, vo, left);
+      aw_store4<FULL>(tm + at, mo, left);
+      aw_store4<FULL>(tv + at, vo, left);
     }
   }
   if (BITS == 8) {
-    // the wave's scales in one store each
 #pragma unroll
     for (int j = 0; j < AW_PER_WAVE; ++j) {
-      if ((b0 + j) * AW_BLOCK < n && lane == (uint32_t)j) {
+      if ((FULL || j * AW_BLOCK < n) && lane == (uint32_t)j) {
         t.ms[b0 + j] = ms_out[j];
         t.vs[b0 + j] = vs_out[j];
       }
     }
   }
+}
+
+template <int BITS, typename G, typename Args>
+__global__ __launch_bounds__(AW_WG) void k_adamw(Args a) {
+  if (a.skip && *a.skip) return;
+  const uint32_t wg = blockIdx.x;
+  int ti = -1;
+#pragma unroll
+  for (int i = 0; i < Args::TENSORS; ++i) ti += wg >= a.begin[i];
+  const AdamwTensor& t = a.t[ti];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * AW_PER_WAVE;   // first block of the wave
+  if ((uint64_t)(b0 + AW_PER_WAVE) * AW_BLOCK <= t.n)
+    aw_blocks<BITS, G, true>(a, t, b0, lane);
+  else if ((uint64_t)b0 * AW_BLOCK < t.n)
+    aw_blocks<BITS, G, false>(a, t, b0, lane);
 }
 
 uint32_t adamw_chunks(int64_t n) { return (uint32_t)((n + AW_CHUNK - 1) / AW_CHUNK); }
@@ -257,19 +308,30 @@ void adamw_host_scalars(AdamwScalars& s, double lr, double beta1, double beta2, 
   aw_scalars(s, lr, beta1, beta2, step, seed);
 }
 
-hipError_t launch_adamw(const AdamwArgs& a, uint32_t grid, int bits, bool g_bf16, hipStream_t s) {
+template <typename Args>
+static hipError_t launch(const Args& a, uint32_t grid, int bits, bool g_bf16, hipStream_t s) {
   if (bits == 8) {
     if (g_bf16)
-      k_adamw<8, uint16_t><<<grid, AW_WG, 0, s>>>(a);
+      k_adamw<8, uint16_t, Args><<<grid, AW_WG, 0, s>>>(a);
     else
-      k_adamw<8, float><<<grid, AW_WG, 0, s>>>(a);
+      k_adamw<8, float, Args><<<grid, AW_WG, 0, s>>>(a);
   } else {
     if (g_bf16)
-      k_adamw<32, uint16_t><<<grid, AW_WG, 0, s>>>(a);
+      k_adamw<32, uint16_t, Args><<<grid, AW_WG, 0, s>>>(a);
     else
-      k_adamw<32, float><<<grid, AW_WG, 0, s>>>(a);
+      k_adamw<32, float, Args><<<grid, AW_WG, 0, s>>>(a);
   }
   return hipGetLastError();
+}
+
+// The arguments of a launch travel with it: a few tensors take the short form.
+hipError_t launch_adamw(const AdamwArgs<AW_TENSORS>& a, int n, uint32_t grid, int bits, bool g_bf16, hipStream_t s) {
+  if (n > AW_FEW) return launch(a, grid, bits, g_bf16, s);
+  AdamwArgs<AW_FEW> f;
+  static_cast<AdamwCommon&>(f) = a;
+  memcpy(f.t, a.t, sizeof(f.t));
+  memcpy(f.begin, a.begin, sizeof(f.begin));
+  return launch(f, grid, bits, g_bf16, s);
 }
 
 }  // namespace qf
@@ -300,8 +362,7 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
         misaligned(d.p16, 16) || misaligned(d.m_scale, 4) || misaligned(d.v_scale, 4))
       return QF_ERR_ALIGN;
   }
-  qf::AdamwArgs a;
-  memset(&a, 0, sizeof(a));
+  qf::AdamwArgs<qf::AW_TENSORS> a;
   a.beta1 = h->beta1;
   a.beta2 = h->beta2;
   a.eps = h->eps;
@@ -332,7 +393,7 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
       }
       if (k == qf::AW_TENSORS || (i == n && k > 0)) {
         for (int j = k; j < qf::AW_TENSORS; ++j) a.begin[j] = 0xFFFFFFFFu;   // no workgroup reaches these
-        const hipError_t e = qf::launch_adamw(a, grid, state_bits, bf == 1, (hipStream_t)stream);
+        const hipError_t e = qf::launch_adamw(a, k, grid, state_bits, bf == 1, (hipStream_t)stream);
         if (e != hipSuccess) return qf::status_of(e);
         k = 0;
         grid = 0;

@@ -127,6 +127,7 @@ hipError_t launch_lora_grads(const LoraArgs& a, int grid, int accumulate, hipStr
 
 // ----------------------------------------------------------------- AdamW ---
 constexpr int AW_TENSORS = 48;      // tensors per launch: the descriptors stay below 4 KiB of kernel arguments
+constexpr int AW_FEW = 8;           // up to this many take a shorter argument block
 
 struct AdamwTensor {
   float* p;
@@ -148,9 +149,7 @@ struct AdamwScalars {
   uint32_t key;           // of the stochastic rounding's hash
 };
 
-struct AdamwArgs {
-  AdamwTensor t[AW_TENSORS];
-  uint32_t begin[AW_TENSORS];   // first workgroup of each tensor; 0xFFFFFFFF past the last
+struct AdamwCommon {
   double beta1, beta2, eps;
   int64_t step;
   uint32_t seed;
@@ -159,6 +158,12 @@ struct AdamwArgs {
   const int64_t* d_step;
   const float* d_grad_scale;
   const uint32_t* skip;
+};
+template <int N>
+struct AdamwArgs : AdamwCommon {
+  static constexpr int TENSORS = N;
+  uint32_t begin[N];            // first workgroup of each tensor; 0xFFFFFFFF past the last
+  AdamwTensor t[N];
 };
 
 // -------------------------------------------------------------- row plan ---

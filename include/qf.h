@@ -527,7 +527,7 @@ qf_status qf_lora_apply_planned(const uint16_t* X, int64_t ldx, int64_t rows_per
  *   code: y rounded stochastically onto E4M3: with u = 16 random bits, below 2^-6
  *   floor(fl(512 y + u 2^-16)), else the fp32 bits of y plus u * 16, truncated to 3 mantissa
  *   bits.  sqrt(v') > 0 never gets code 0 (it would leave the next step's divisor near
- *   eps).  m's sign is the code's top bit.  u = the low (m) or high (v) half of
+ *   eps).  m's sign bit is the code's top bit.  u = the low (m) or high (v) half of
  *   H((key + i) mod 2^32) for element i of its tensor, key = H(seed ^ H(step mod 2^32)), with
  *   H(x): x ^= x>>16; x *= 0x7FEB352D; x ^= x>>15; x *= 0x846CA68B; x ^= x>>16 (mod 2^32).
  *   Same inputs, step and seed, same bits, however the tensors are grouped into calls.

@@ -77,7 +77,7 @@ def encode(x, rnd, lift):
     code = np.where(y < F(2.0 ** -6), small, large)
     if lift:
         code = np.where((y > 0) & (code < 1), 1, code)
-    code = code + np.where(xp < 0, 128, 0)
+    code = code + np.where(np.signbit(xp), 128, 0)
     return code.reshape(-1)[:n].astype(np.uint8), scale
 
 
