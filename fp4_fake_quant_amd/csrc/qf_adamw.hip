@@ -10,7 +10,9 @@
 //
 // One wave owns whole 256-element blocks, 4 consecutive elements per lane: every fp32 load
 // and store instruction of a wave covers 1 KiB of contiguous memory, and a block's largest
-// magnitude is one cross-lane reduction.
+// magnitude is one cross-lane reduction.  Every byte passes once (30 per element with fp32
+// states, fp32 gradient and bf16 copy; 16 with 8-bit states and bf16 gradient), so all of it is
+// accessed with the non-temporal policy.  Measured on 218 M elements: see aw_per_wave.
 #include <algorithm>
 #include <string.h>
 
@@ -21,8 +23,12 @@ namespace qf {
 
 constexpr int AW_WG = 256;
 constexpr int AW_BLOCK = QF_ADAMW_BLOCK;           // elements per 8-bit block: 64 lanes x 4
-constexpr int AW_PER_WAVE = 4;                     // blocks in flight per wave
-constexpr int AW_CHUNK = AW_WG / 64 * AW_PER_WAVE * AW_BLOCK;
+// Blocks in flight per wave.  More give a wave more loads to wait for at once, fewer give small
+// tensors more waves.  Microseconds for 1 / 2 / 4 blocks: fp32 states, 1.1 M elements 7.8 / 8.0 /
+// 8.9 and 218 M 1120 / 1164 / 1113; 8-bit states, 22 M elements in 120 tensors 83 / 87 / 94 and
+// 218 M 637 / 606 / 605 (and without the non-temporal policy, 4 blocks: 1214, 687).
+constexpr int aw_per_wave(int bits) { return bits == 8 ? 2 : 1; }
+constexpr int aw_chunk(int bits) { return AW_WG / 64 * aw_per_wave(bits) * AW_BLOCK; }
 constexpr float AW_MIN_MAX = 7.888609052210118e-31f;   // 2^-100: smaller block maxima store zeros
 
 static_assert(AW_BLOCK == 256, "a wave of 64 lanes holds one block, 4 elements per lane");
@@ -97,11 +103,17 @@ __device__ __forceinline__ AwScale aw_block_scale(uint32_t top_bits) {
   return o;
 }
 
+typedef float aw_f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t aw_u32x2 __attribute__((ext_vector_type(2)));
+
 // Four consecutive elements of an array; unless FULL only `left` of them exist (the others read
 // as zero and are not written).
 template <bool FULL>
 __device__ __forceinline__ float4 aw_load4(const float* p, uint32_t left) {
-  if (FULL || left >= 4) return *reinterpret_cast<const float4*>(p);
+  if (FULL || left >= 4) {
+    const aw_f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const aw_f32x4*>(p));
+    return float4{q.x, q.y, q.z, q.w};
+  }
   float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   if (left > 0) o.x = p[0];
   if (left > 1) o.y = p[1];
@@ -110,9 +122,9 @@ __device__ __forceinline__ float4 aw_load4(const float* p, uint32_t left) {
 }
 template <bool FULL>
 __device__ __forceinline__ float4 aw_load4(const uint16_t* p, uint32_t left) {
-  uint2 w = {0u, 0u};
+  aw_u32x2 w = {0u, 0u};
   if (FULL || left >= 4) {
-    w = *reinterpret_cast<const uint2*>(p);
+    w = __builtin_nontemporal_load(reinterpret_cast<const aw_u32x2*>(p));
   } else {
     if (left > 0) w.x = p[0];
     if (left > 1) w.x |= (uint32_t)p[1] << 16;
@@ -122,7 +134,7 @@ __device__ __forceinline__ float4 aw_load4(const uint16_t* p, uint32_t left) {
 }
 template <bool FULL>
 __device__ __forceinline__ uint32_t aw_load4(const uint8_t* p, uint32_t left) {
-  if (FULL || left >= 4) return *reinterpret_cast<const uint32_t*>(p);
+  if (FULL || left >= 4) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   uint32_t w = 0;
   if (left > 0) w = p[0];
   if (left > 1) w |= (uint32_t)p[1] << 8;
@@ -132,7 +144,7 @@ __device__ __forceinline__ uint32_t aw_load4(const uint8_t* p, uint32_t left) {
 template <bool FULL>
 __device__ __forceinline__ void aw_store4(float* p, const float (&v)[4], uint32_t left) {
   if (FULL || left >= 4) {
-    *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
+    __builtin_nontemporal_store(aw_f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<aw_f32x4*>(p));
     return;
   }
   for (uint32_t i = 0; i < 3; ++i)
@@ -142,7 +154,7 @@ template <bool FULL>
 __device__ __forceinline__ void aw_store4(uint16_t* p, const float (&v)[4], uint32_t left) {
   const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
   if (FULL || left >= 4) {
-    *reinterpret_cast<uint2*>(p) = uint2{lo, hi};
+    __builtin_nontemporal_store(aw_u32x2{lo, hi}, reinterpret_cast<aw_u32x2*>(p));
     return;
   }
   if (left > 0) p[0] = (uint16_t)lo;
@@ -152,16 +164,17 @@ __device__ __forceinline__ void aw_store4(uint16_t* p, const float (&v)[4], uint
 template <bool FULL>
 __device__ __forceinline__ void aw_store4(uint8_t* p, uint32_t w, uint32_t left) {
   if (FULL || left >= 4) {
-    *reinterpret_cast<uint32_t*>(p) = w;
+    __builtin_nontemporal_store(w, reinterpret_cast<uint32_t*>(p));
     return;
   }
   for (uint32_t i = 0; i < 3; ++i)
     if (i < left) p[i] = (uint8_t)(w >> (8 * i));
 }
 
-// The wave's blocks b0 .. b0 + 3 of one tensor; FULL: all of their elements exist.
+// The wave's blocks from b0 of one tensor; FULL: all of their elements exist.
 template <int BITS, typename G, bool FULL, typename Args>
 __device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, uint32_t b0, uint32_t lane) {
+  constexpr int PER = aw_per_wave(BITS);
   // uniform bases: the lane's part of every address is a small offset
   const uint64_t first = (uint64_t)b0 * AW_BLOCK;
   float* const tp = t.p + first;
@@ -171,13 +184,13 @@ __device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, u
   float* const tv = static_cast<float*>(t.v) + (BITS == 8 ? 0 : first);
   uint8_t* const tmc = static_cast<uint8_t*>(t.m) + (BITS == 8 ? first : 0);
   uint8_t* const tvc = static_cast<uint8_t*>(t.v) + (BITS == 8 ? first : 0);
-  const uint32_t n = FULL ? AW_PER_WAVE * AW_BLOCK : (uint32_t)(t.n - first);
+  const uint32_t n = FULL ? PER * AW_BLOCK : (uint32_t)(t.n - first);
 
-  float4 p[AW_PER_WAVE], g[AW_PER_WAVE], m[AW_PER_WAVE], v[AW_PER_WAVE];
-  uint32_t mc[AW_PER_WAVE], vc[AW_PER_WAVE];
-  float ms[AW_PER_WAVE], vs[AW_PER_WAVE];
+  float4 p[PER], g[PER], m[PER], v[PER];
+  uint32_t mc[PER], vc[PER];
+  float ms[PER], vs[PER];
 #pragma unroll
-  for (int j = 0; j < AW_PER_WAVE; ++j) {
+  for (int j = 0; j < PER; ++j) {
     const uint32_t at = j * AW_BLOCK + lane * 4;
     const uint32_t left = at < n ? n - at : 0;
     p[j] = aw_load4<FULL>(tp + at, left);
@@ -202,9 +215,9 @@ __device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, u
   const float b2 = (float)a.beta2, c2 = (float)(1.0 - a.beta2);
   const float eps = (float)a.eps;
 
-  float ms_out[AW_PER_WAVE], vs_out[AW_PER_WAVE];
+  float ms_out[PER], vs_out[PER];
 #pragma unroll
-  for (int j = 0; j < AW_PER_WAVE; ++j) {
+  for (int j = 0; j < PER; ++j) {
     if (!FULL && j * AW_BLOCK >= n) break;                      // uniform over the wave
     const uint32_t at = j * AW_BLOCK + lane * 4;
     const uint32_t left = at < n ? n - at : 0;
@@ -276,7 +289,7 @@ __device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, u
   }
   if (BITS == 8) {
 #pragma unroll
-    for (int j = 0; j < AW_PER_WAVE; ++j) {
+    for (int j = 0; j < PER; ++j) {
       if ((FULL || j * AW_BLOCK < n) && lane == (uint32_t)j) {
         t.ms[b0 + j] = ms_out[j];
         t.vs[b0 + j] = vs_out[j];
@@ -295,14 +308,15 @@ __global__ __launch_bounds__(AW_WG) void k_adamw(Args a) {
   const AdamwTensor& t = a.t[ti];
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * AW_PER_WAVE;   // first block of the wave
-  if ((uint64_t)(b0 + AW_PER_WAVE) * AW_BLOCK <= t.n)
+  constexpr int PER = aw_per_wave(BITS);
+  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * PER;   // first block of the wave
+  if ((uint64_t)(b0 + PER) * AW_BLOCK <= t.n)
     aw_blocks<BITS, G, true>(a, t, b0, lane);
   else if ((uint64_t)b0 * AW_BLOCK < t.n)
     aw_blocks<BITS, G, false>(a, t, b0, lane);
 }
 
-uint32_t adamw_chunks(int64_t n) { return (uint32_t)((n + AW_CHUNK - 1) / AW_CHUNK); }
+uint32_t adamw_chunks(int64_t n, int bits) { return (uint32_t)((n + aw_chunk(bits) - 1) / aw_chunk(bits)); }
 
 void adamw_host_scalars(AdamwScalars& s, double lr, double beta1, double beta2, int64_t step, uint32_t seed) {
   aw_scalars(s, lr, beta1, beta2, step, seed);
@@ -389,7 +403,7 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
         o.n = (uint32_t)t[i].n;
         o.weight_decay = t[i].weight_decay;
         a.begin[k++] = grid;
-        grid += qf::adamw_chunks(t[i].n);
+        grid += qf::adamw_chunks(t[i].n, state_bits);
       }
       if (k == qf::AW_TENSORS || (i == n && k > 0)) {
         for (int j = k; j < qf::AW_TENSORS; ++j) a.begin[j] = 0xFFFFFFFFu;   // no workgroup reaches these
