@@ -145,6 +145,15 @@ __global__ __launch_bounds__(LA_WG) void k_lora_row_up(LoraApplyArgs a) {
 }
 
 // --------------------------------------------------------------- tiles form ----
+// The tile of a workgroup: workgroups go to the 8 XCDs in turn, tiles of one adapter follow each
+// other, so every block of 64 tiles is dealt out in runs of 8: an adapter's A and B then pass
+// through few of the XCDs' caches (all 8 would read 63 MB more for 24 adapters of 4096 x 16 and
+// 6144 x 16, next to 134 MB of X and 200 of Y).
+__device__ __forceinline__ int la_tile_of(unsigned wg, unsigned n) {
+  const unsigned base = wg & ~63u, r = wg & 63u;
+  return (int)(base + 64u <= n ? base + (r & 7u) * 8u + (r >> 3) : wg);
+}
+
 // One tile's adapter, positions, and the rows of this lane's two 16-row blocks (-1: none).  A plan
 // that does not fit the call gives no tile or no row.  The loads of a tile depend on each other
 // (tile, then order and offsets, then X or Y), so they are issued as early as they can be.
@@ -178,7 +187,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
   const int split = blockIdx.y, lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   LaTile t;
-  if (!la_tile(a, blockIdx.x, i, t)) return;
+  if (!la_tile(a, la_tile_of(blockIdx.x, gridDim.x), i, t)) return;
   const uint16_t* x[2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) x[b] = a.X + (int64_t)(std::max(t.row[b], 0) / a.rows_per_x) * a.ldx + g * 8;
@@ -277,9 +286,13 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   const bool low = i < 8;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   LaTile t;
-  if (!la_tile(a, blockIdx.x, i, t)) return;
+  if (!la_tile(a, la_tile_of(blockIdx.x, gridDim.x), i, t)) return;
   const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part), step = LA_WAVES * LA_NSTEP;
-  int n0 = blockIdx.y * a.n_part + wave * LA_NSTEP;
+  // Tiles start at different steps: rows are a multiple of 256 bytes apart as a rule, and all
+  // tiles at one column would share a few memory channels.
+  const int begin = blockIdx.y * a.n_part + wave * LA_NSTEP;
+  const int steps = begin < end ? (end - begin + step - 1) / step : 0;
+  int left = steps, n0 = begin + (steps > 0 ? (int)(blockIdx.x % (unsigned)steps) * step : 0);
   // accesses v = 0, 1 of block b: rows (i & 7) + 8 v of the block, half i / 8 of the line
   int row[2][2];
   uint16_t* y[2][2];
@@ -310,7 +323,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
         yv[b][v] = uint4{w[0], w[1], w[2], w[3]};
       }
   };
-  if (n0 < end) load_y(n0);
+  if (left > 0) load_y(n0);
 
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
   uint4 sv[2][RB];
@@ -343,15 +356,15 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
     }
   }
   const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
-  while (n0 < end) {
+  while (left > 0) {
     const int at = n0;
     uint4 yc[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 2; ++v) yc[b][v] = yv[b][v];
-    n0 += step;
-    if (n0 < end) load_y(n0);
+    n0 = n0 + step < end ? n0 + step : begin;
+    if (--left > 0) load_y(n0);
 #pragma unroll
     for (int b = 0; b < 2; ++b) la_swap8(yc[b][0], yc[b][1], low);    // now this lane's row, steps q = 0, 1
 #pragma unroll
