@@ -27,8 +27,6 @@ namespace qf {
 constexpr int RT_WAVE = 64;       // one wave per workgroup: rows share nothing
 constexpr float RT_INF = __builtin_inff();
 
-__device__ __forceinline__ float rt_max_xor(float v, int d) { return fmaxf(v, __shfl_xor(v, d)); }
-
 // Reductions over the L lanes of a row.
 template <int L>
 __device__ __forceinline__ float rt_row_max(float v) {
@@ -434,74 +432,126 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
 // Gradient of the weights with respect to the logits.  With p_j = u_j / sum u:
 //   renormalised, softmax:  dx[i_j] = c p_j (g_j - sum g p);   sigmoid: times (1 - u_j)
 //   plain, sigmoid: dx[i_j] = c g_j u_j (1 - u_j);  softmax: dx[e] = c s_e (g_e - sum g u)
-// A row's gradient is assembled in LDS and leaves in whole lines.
-template <typename X>
-__device__ __forceinline__ void rt_store(X* p, float v);
-template <> __device__ __forceinline__ void rt_store<float>(float* p, float v) { *p = v; }
-template <> __device__ __forceinline__ void rt_store<uint16_t>(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.0f); }
+// Lanes and logits are laid out as in the forward pass; the chosen ones (two per lane where k is
+// over L) meet the row in LDS, so that the gradient leaves as one dense, coalesced row.  Bounded
+// by the dense write (and the read, for plain softmax).
+template <int V, bool VEC>
+__device__ __forceinline__ void rt_store(float* row, int e0, int E, const float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    if (VEC) {
+      if (e0 + i < E) *reinterpret_cast<float4*>(row + e0 + i) = float4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e0 + i + j < E) row[e0 + i + j] = x[i + j];
+    }
+  }
+}
+template <int V, bool VEC>
+__device__ __forceinline__ void rt_store(uint16_t* row, int e0, int E, const float (&x)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const uint2 w = {pack_bf16x2(x[i], x[i + 1]), pack_bf16x2(x[i + 2], x[i + 3])};
+    if (VEC) {
+      if (e0 + i < E) *reinterpret_cast<uint2*>(row + e0 + i) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e0 + i + j < E) row[e0 + i + j] = (uint16_t)((j < 2 ? w.x : w.y) >> (16 * (j & 1)));
+    }
+  }
+}
 
-template <typename X>
-__global__ __launch_bounds__(RT_WAVE) void k_route_backward(RouteArgs a) {
-  __shared__ float d[QF_ROUTE_MAX_EXPERTS];
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
-  const X* row = static_cast<const X*>(a.logits) + t * a.ld;
-  X* out = static_cast<X*>(a.dlogits) + t * a.ldd;
-  const bool softmax = a.scoring == QF_ROUTE_SOFTMAX;
-  for (int e = lane; e < a.E; e += RT_WAVE) d[e] = 0.0f;
-  const int id0 = lane < a.k ? a.indices[t * a.k + lane] : -1;
-  const int id = (uint32_t)id0 < (uint32_t)a.E ? id0 : -1;
-  const bool any = __ballot(id >= 0) != 0;
-  const float g = id >= 0 ? a.dweights[t * a.k + lane] * a.scale : 0.0f;
-  const float x = id >= 0 ? rt_logit(row, id) : -RT_INF;
-  float dx = 0.0f;
-  if (a.renorm || !softmax) {
-    float u;
-    if (softmax) {
-      float top = rt_row_max<32>(x);
-      top = rt_max_xor(top, 32);
-      u = id >= 0 && top > -RT_INF ? expf(x - top) : 0.0f;
-    } else {
-      u = id >= 0 ? 1.0f / (1.0f + expf(-x)) : 0.0f;
-    }
+constexpr int RB_WAVES = 4;
+template <int L, int V, typename X, bool VEC>
+__global__ __launch_bounds__(RT_WAVE * RB_WAVES) void k_route_backward(RouteArgs a) {
+  constexpr int ROWS = RT_WAVE / L, PER = (QF_ROUTE_MAX_K + L - 1) / L;
+  __shared__ float4 d4[RB_WAVES * ROWS][L * V / 4];
+  const int lane = threadIdx.x % L, sub = threadIdx.x / L;
+  const int64_t t = (int64_t)blockIdx.x * (RB_WAVES * ROWS) + sub;
+  const bool live = t < a.T;
+  const X* row = static_cast<const X*>(a.logits) + (live ? t : 0) * a.ld;
+  float* d = reinterpret_cast<float*>(d4[sub]);
+  const bool softmax = a.scoring == QF_ROUTE_SOFTMAX, dense = softmax && !a.renorm;
+  int id[PER];
+  float g[PER], x[PER], u[PER];
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    const int j = lane + p * L;
+    id[p] = live && j < a.k ? a.indices[t * a.k + j] : -1;
+    g[p] = live && j < a.k ? a.dweights[t * a.k + j] : 0.0f;
+    if ((uint32_t)id[p] >= (uint32_t)a.E) id[p] = -1;
+  }
+  float v[V];
+  if (dense) rt_load<V, VEC>(row, lane * V, live ? a.E : 0, v);
+#pragma unroll
+  for (int i = 0; i < V; i += 4) d4[sub][(lane * V + i) / 4] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+  float top = -RT_INF;
+#pragma unroll
+  for (int p = 0; p < PER; ++p) {
+    x[p] = id[p] >= 0 && !dense ? rt_logit(row, id[p]) : -RT_INF;
+    g[p] = id[p] >= 0 ? g[p] * a.scale : 0.0f;
+    top = fmaxf(top, x[p]);
+  }
+  if (!dense) {
+    if (softmax) top = rt_row_max<L>(top);
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+      u[p] = id[p] < 0 ? 0.0f : !softmax ? 1.0f / (1.0f + expf(-x[p])) : top > -RT_INF ? expf(x[p] - top) : 0.0f;
     if (a.renorm) {
-      const float total = rt_row_sum<64>(u);
-      const float p = total > 0.0f ? u / total : 0.0f;
-      const float mean = rt_row_sum<64>(g * p);
-      dx = p * (g - mean);
-      if (!softmax) dx *= 1.0f - u;
+      float total = 0.0f, mean = 0.0f;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) total += u[p];
+      total = rt_row_sum<L>(total);
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) mean += g[p] * (u[p] * inv);
+      mean = rt_row_sum<L>(mean);
+#pragma unroll
+      for (int p = 0; p < PER; ++p) g[p] = u[p] * inv * (g[p] - mean) * (softmax ? 1.0f : 1.0f - u[p]);
     } else {
-      dx = g * u * (1.0f - u);
+#pragma unroll
+      for (int p = 0; p < PER; ++p) g[p] *= u[p] * (1.0f - u[p]);
     }
-  } else {
-    dx = g;                       // the score's gradient; the row's part follows
   }
   __syncthreads();
-  for (int j = 0; j < a.k; ++j)   // in order, so that an index given twice adds up
-    if (lane == j && id >= 0) d[id] += dx;
+  // an index given twice adds up: the choices one after another
+#pragma unroll
+  for (int p = 0; p < PER; ++p)
+    for (int j = 0; j < L && p * L + j < a.k; ++j)
+      if (lane == j && id[p] >= 0) d[id[p]] += g[p];
   __syncthreads();
-  if (softmax && !a.renorm && any) {
-    float top = -RT_INF;
-    for (int e = lane; e < a.E; e += RT_WAVE) top = fmaxf(top, rt_logit(row, e));
-    top = rt_row_max<32>(top);
-    top = rt_max_xor(top, 32);
-    if (top == -RT_INF) top = 0.0f;
-    float total = 0.0f, dot = 0.0f;
-    for (int e = lane; e < a.E; e += RT_WAVE) {
-      const float s = expf(rt_logit(row, e) - top);
-      total += s;
-      dot += s * d[e];
-    }
-    total = rt_row_sum<64>(total);
-    dot = rt_row_sum<64>(dot);
-    const float mean = total > 0.0f ? dot / total : 0.0f;
-    for (int e = lane; e < a.E; e += RT_WAVE) {
-      const float s = total > 0.0f ? expf(rt_logit(row, e) - top) / total : 0.0f;
-      rt_store(out + e, s * (d[e] - mean));
-    }
-    return;
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const float4 w = d4[sub][(lane * V + i) / 4];
+    o[i] = w.x; o[i + 1] = w.y; o[i + 2] = w.z; o[i + 3] = w.w;
   }
-  for (int e = lane; e < a.E; e += RT_WAVE) rt_store(out + e, d[e]);
+  if (dense) {
+    int any = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p) any |= id[p] >= 0;
+    any = rt_row_sum<L>(any);
+    float most = -RT_INF, total = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = fmaxf(most, v[i]);
+    most = rt_row_max<L>(most);
+    if (most == -RT_INF) most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = expf(v[i] - most);
+      total += v[i];
+      dot += v[i] * o[i];
+    }
+    total = rt_row_sum<L>(total);
+    dot = rt_row_sum<L>(dot);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;       // a NaN stays
+    const float mean = dot * inv;
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = any ? v[i] * inv * (o[i] - mean) : 0.0f;
+  }
+  if (live) rt_store<V, VEC>(static_cast<X*>(a.dlogits) + t * a.ldd, lane * V, a.E, o);
 }
 
 namespace {
@@ -546,9 +596,30 @@ hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s) {
   return hipGetLastError();
 }
 
+namespace {
+template <int L, int V, typename X>
+void route_back_go(const RouteArgs& a, bool vec, hipStream_t s) {
+  constexpr int ROWS = RT_WAVE / L * RB_WAVES;
+  const unsigned grid = (unsigned)((a.T + ROWS - 1) / ROWS);
+  if (vec) k_route_backward<L, V, X, true><<<grid, RT_WAVE * RB_WAVES, 0, s>>>(a);
+  else k_route_backward<L, V, X, false><<<grid, RT_WAVE * RB_WAVES, 0, s>>>(a);
+}
+template <typename X>
+void route_back_size(const RouteArgs& a, bool vec, hipStream_t s) {
+  if (a.E <= 64) route_back_go<16, 4, X>(a, vec, s);
+  else if (a.E <= 128) route_back_go<16, 8, X>(a, vec, s);
+  else if (a.E <= 256) route_back_go<16, 16, X>(a, vec, s);
+  else if (a.E <= 512) route_back_go<32, 16, X>(a, vec, s);
+  else route_back_go<32, 32, X>(a, vec, s);
+}
+}  // namespace
+
 hipError_t launch_route_backward(const RouteArgs& a, bool bf16, hipStream_t s) {
-  if (bf16) k_route_backward<uint16_t><<<(unsigned)a.T, RT_WAVE, 0, s>>>(a);
-  else k_route_backward<float><<<(unsigned)a.T, RT_WAVE, 0, s>>>(a);
+  const int64_t sz = bf16 ? 2 : 4;
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && a.ldd % 4 == 0 && (uintptr_t)a.logits % (4 * sz) == 0 &&
+                   (uintptr_t)a.dlogits % (4 * sz) == 0;
+  if (bf16) route_back_size<uint16_t>(a, vec, s);
+  else route_back_size<float>(a, vec, s);
   return hipGetLastError();
 }
 
