@@ -24,7 +24,8 @@
 
 namespace qf {
 
-constexpr int RT_WAVE = 64;       // one wave per workgroup: rows share nothing
+constexpr int RT_WAVE = 64;
+constexpr int RT_WAVES = 4;       // waves per workgroup (they share nothing: fewer workgroups to start)
 constexpr float RT_INF = __builtin_inff();
 
 // Reductions over the L lanes of a row.
@@ -82,15 +83,21 @@ __device__ __forceinline__ void rt_load(const uint16_t* row, int e0, int E, floa
   }
 }
 
+// Orders a wave's own LDS accesses: its lanes exchange through LDS, waves do not.
+__device__ __forceinline__ void rt_wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Groups: none, each a power of two of whole lanes (WHOLE), or any.
 enum { RT_NO_GROUPS = 0, RT_WHOLE = 1, RT_ANY = 2 };
 
-// LDS of a wave's group ranking.
+// LDS of the group ranking, per row.
 template <int L, int V, int GROUPS, typename K>
 struct RtGroups {
-  K keys[GROUPS == RT_ANY ? RT_WAVE / L * L * V : 1];
-  K score[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
-  uint8_t keep[RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
+  K keys[GROUPS == RT_ANY ? RT_WAVES * RT_WAVE * V : 1];
+  K score[RT_WAVES * RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
+  uint8_t keep[RT_WAVES * RT_WAVE / L * QF_ROUTE_MAX_GROUPS];
 };
 
 __device__ __forceinline__ void rt_top2(double& m1, double& m2, double v) {
@@ -127,14 +134,14 @@ __device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane,
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (lane * V + i < a.E) keys[lane * V + i] = key[i];
-    __syncthreads();
+    rt_wave_sync();
     for (int g = lane; g < a.n_group; g += L) {
       K m1 = none, m2 = none;
       for (int i = 0; i < size; ++i) rt_top2(m1, m2, keys[g * size + i]);
       score[g] = a.group_top2 && m2 > none ? m1 + m2 : m1;
     }
   }
-  __syncthreads();
+  rt_wave_sync();
   K worst = (K)RT_INF, best = none;            // of the kept, of the dropped
   for (int g = lane; g < a.n_group; g += L) {
     const K mine = score[g];
@@ -148,7 +155,7 @@ __device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane,
     if (in) worst = mine < worst ? mine : worst;
     else best = mine > best ? mine : best;
   }
-  __syncthreads();
+  rt_wave_sync();
   worst = -rt_row_max<L>(-worst);
   best = rt_row_max<L>(best);
   if (GROUPS == RT_WHOLE) {
@@ -182,7 +189,7 @@ __device__ __forceinline__ void rt_select(const RouteArgs& a, int lane, uint64_t
     const uint64_t who = __ballot(best == mx) & seg;
     if (who == 0) {                                          // NaN keys of a poisoned row
       if (lane == 0) chosen[j] = -1;
-    } else if ((int)threadIdx.x == __ffsll((unsigned long long)who) - 1) {
+    } else if ((int)(threadIdx.x & 63) == __ffsll((unsigned long long)who) - 1) {
       chosen[j] = mx > -(K)RT_INF ? lane * V + slot : -1;
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -246,8 +253,8 @@ __device__ __forceinline__ float rt_fast_exp(float x) { return __builtin_amdgcn_
 
 // SCORES: choose by scores plus bias, else by logits.
 template <int L, int V, typename X, bool SCORES, bool VEC, int GROUPS>
-__global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
-  constexpr int ROWS = RT_WAVE / L;
+__global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
+  constexpr int ROWS = RT_WAVE * RT_WAVES / L;
   constexpr bool IN_ROW = !SCORES && sizeof(X) == 2;       // logit and index fit a key
   using K2 = typename std::conditional<SCORES, double, float>::type;   // the second pass's keys
   __shared__ int32_t chosen[ROWS][QF_ROUTE_MAX_K + 1];
@@ -307,7 +314,7 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
     if (SCORES) most = std::max(most, (int32_t)__float_as_uint(x[i]));
     mostu = umax(mostu, __float_as_uint(v[i]));
   }
-  const uint64_t seg = ((1ull << L) - 1ull) << (sub * L);
+  const uint64_t seg = ((1ull << L) - 1ull) << ((threadIdx.x & 63) / L * L);
   const bool bad = (__ballot(most >= 0x7F800000 || mostu > 0xFF800000u) & seg) != 0;
 
   // The fp32 score's error: sigmoid, 5 units of 2^-24 (exp2 and its argument, sum, reciprocal,
@@ -362,7 +369,7 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
         sure = sure && !close;
       }
     }
-    __syncthreads();
+    rt_wave_sync();
 #pragma unroll
     for (int p = 0; p < PER; ++p) id[p] = held[p] >= least && lane + p * L < a.k ? chosen[sub][lane + p * L] : -1;
   }
@@ -389,7 +396,7 @@ __global__ __launch_bounds__(RT_WAVE) void k_route(RouteArgs a) {
         for (int i = 0; i < V; ++i) key2[i] = v[i];          // the groups' choice was exact
       }
       rt_select<L, V, K2>(a, lane, seg, key2, chosen[sub]);
-      __syncthreads();
+      rt_wave_sync();
 #pragma unroll
       for (int p = 0; p < PER; ++p) id[p] = lane + p * L < a.k ? chosen[sub][lane + p * L] : -1;
     }
@@ -463,13 +470,12 @@ __device__ __forceinline__ void rt_store(uint16_t* row, int e0, int E, const flo
   }
 }
 
-constexpr int RB_WAVES = 4;
 template <int L, int V, typename X, bool VEC>
-__global__ __launch_bounds__(RT_WAVE * RB_WAVES) void k_route_backward(RouteArgs a) {
+__global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs a) {
   constexpr int ROWS = RT_WAVE / L, PER = (QF_ROUTE_MAX_K + L - 1) / L;
-  __shared__ float4 d4[RB_WAVES * ROWS][L * V / 4];
+  __shared__ float4 d4[RT_WAVES * ROWS][L * V / 4];
   const int lane = threadIdx.x % L, sub = threadIdx.x / L;
-  const int64_t t = (int64_t)blockIdx.x * (RB_WAVES * ROWS) + sub;
+  const int64_t t = (int64_t)blockIdx.x * (RT_WAVES * ROWS) + sub;
   const bool live = t < a.T;
   const X* row = static_cast<const X*>(a.logits) + (live ? t : 0) * a.ld;
   float* d = reinterpret_cast<float*>(d4[sub]);
@@ -515,13 +521,13 @@ __global__ __launch_bounds__(RT_WAVE * RB_WAVES) void k_route_backward(RouteArgs
       for (int p = 0; p < PER; ++p) g[p] *= u[p] * (1.0f - u[p]);
     }
   }
-  __syncthreads();
+  rt_wave_sync();
   // an index given twice adds up: the choices one after another
 #pragma unroll
   for (int p = 0; p < PER; ++p)
     for (int j = 0; j < L && p * L + j < a.k; ++j)
       if (lane == j && id[p] >= 0) d[id[p]] += g[p];
-  __syncthreads();
+  rt_wave_sync();
   float o[V];
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
@@ -557,17 +563,17 @@ __global__ __launch_bounds__(RT_WAVE * RB_WAVES) void k_route_backward(RouteArgs
 namespace {
 template <int L, int V, typename X, bool S>
 void route_go(const RouteArgs& a, bool vec, hipStream_t s) {
-  constexpr int ROWS = RT_WAVE / L;
+  constexpr int ROWS = RT_WAVE * RT_WAVES / L;
   const unsigned grid = (unsigned)((a.T + ROWS - 1) / ROWS);
   const int size = a.E / a.n_group, lanes = size / V;
   if (a.n_group > 1 && vec && size % V == 0 && (lanes & (lanes - 1)) == 0) {
-    k_route<L, V, X, S, true, RT_WHOLE><<<grid, RT_WAVE, 0, s>>>(a);
+    k_route<L, V, X, S, true, RT_WHOLE><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
   } else if (a.n_group > 1) {
-    if (vec) k_route<L, V, X, S, true, RT_ANY><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, S, false, RT_ANY><<<grid, RT_WAVE, 0, s>>>(a);
+    if (vec) k_route<L, V, X, S, true, RT_ANY><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
+    else k_route<L, V, X, S, false, RT_ANY><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
   } else {
-    if (vec) k_route<L, V, X, S, true, RT_NO_GROUPS><<<grid, RT_WAVE, 0, s>>>(a);
-    else k_route<L, V, X, S, false, RT_NO_GROUPS><<<grid, RT_WAVE, 0, s>>>(a);
+    if (vec) k_route<L, V, X, S, true, RT_NO_GROUPS><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
+    else k_route<L, V, X, S, false, RT_NO_GROUPS><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
   }
 }
 // Few lanes with many logits each: a round's work over the lanes' logits is shared by more rows.
@@ -599,10 +605,10 @@ hipError_t launch_route(const RouteArgs& a, bool bf16, hipStream_t s) {
 namespace {
 template <int L, int V, typename X>
 void route_back_go(const RouteArgs& a, bool vec, hipStream_t s) {
-  constexpr int ROWS = RT_WAVE / L * RB_WAVES;
+  constexpr int ROWS = RT_WAVE / L * RT_WAVES;
   const unsigned grid = (unsigned)((a.T + ROWS - 1) / ROWS);
-  if (vec) k_route_backward<L, V, X, true><<<grid, RT_WAVE * RB_WAVES, 0, s>>>(a);
-  else k_route_backward<L, V, X, false><<<grid, RT_WAVE * RB_WAVES, 0, s>>>(a);
+  if (vec) k_route_backward<L, V, X, true><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
+  else k_route_backward<L, V, X, false><<<grid, RT_WAVE * RT_WAVES, 0, s>>>(a);
 }
 template <typename X>
 void route_back_size(const RouteArgs& a, bool vec, hipStream_t s) {
