@@ -47,9 +47,14 @@ def _p(t):
 
 def _mat(x, name):
     """rows, cols, row stride of a 2-D tensor with unit column stride."""
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    return x.shape[0], x.shape[1], x.stride(0) if x.shape[0] > 1 else max(x.shape[1], x.stride(0))
+    rows, cols = shape
+    ld, step = x.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    return rows, cols, ld if rows > 1 else max(cols, ld)
 
 
 def _bf16(x, name):
@@ -540,7 +545,9 @@ def _same_gpu(*tensors):
 def _call(dev, name, *args):
     """Calls an entry point with GPU dev current and dev's current stream as its last argument."""
     f = getattr(lib(), name)
-    if dev < 0 or dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    elif dev < 0:
         st = f(*args, _stream())
     else:
         with torch.cuda.device(dev):
@@ -558,12 +565,9 @@ def _route_desc(logits, k, scoring, renorm, scale):
         raise TypeError("logits must be float32 or bfloat16")
     if scoring not in _SCORING:
         raise ValueError("scoring is 'softmax' or 'sigmoid'")
-    T, E, ld = _mat(logits, "logits")
-    d = RouteDesc()
-    d.logits, d.tokens, d.ld, d.experts, d.k = logits.data_ptr(), T, ld, E, int(k)
-    d.logits_bf16, d.scoring, d.renorm = int(logits.dtype == torch.bfloat16), _SCORING[scoring], int(bool(renorm))
-    d.scale, d.n_group, d.topk_group = float(scale), 1, 1
-    return d, T, E
+    T, E, ld = _mat(logits, "logits")      # the fields in qf_route_desc's order
+    return RouteDesc(logits.data_ptr(), T, ld, None, scale, logits.dtype is torch.bfloat16, E, k, _SCORING[scoring],
+                     bool(renorm), 1, 1, 0), T, E
 
 
 def _dense(t, name, dtype, shape):
@@ -584,8 +588,11 @@ def qf_moe_route(logits, k, scoring="softmax", bias=None, n_group=1, topk_group=
     dev = _same_gpu(logits, bias, indices, weights)
     if bias is not None:
         d.bias = _dense(bias, "bias", torch.float32, (E,)).data_ptr()
-    d.n_group, d.topk_group, d.group_rule = n_group, topk_group, _GROUP_RULE[group_rule]
-    shape = (T, max(d.k, 0))
+    if n_group != 1:
+        d.n_group, d.topk_group, d.group_rule = n_group, topk_group, _GROUP_RULE[group_rule]
+    elif topk_group != 1:
+        d.topk_group = topk_group
+    shape = (T, max(k, 0))
     if indices is None:
         indices = torch.empty(shape, dtype=torch.int32, device=logits.device)
     else:
@@ -662,16 +669,15 @@ def qf_lora_apply_workspace(rows, K, r, n_adapters, planned=False):
 
 def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
     plan = where if isinstance(where, RowPlan) else None
-    dev = _same_gpu(X, A, B, Y, scale, ws, *((plan.order,) if plan else (where,)))
+    dev = _same_gpu(X, A, B, Y, scale, ws, where if plan is None else plan.order)
     xrows, K, ldx = _mat(_bf16(X, "X"), "X")
     rows, N, ldy = _mat(_bf16(Y, "Y"), "Y")
     for t, what in ((A, "A"), (B, "B")):
         if _bf16(t, what).dim() != 3 or not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous 3-D tensor [adapters, ...]")
-    E, r = A.shape[0], A.shape[1]
-    if A.shape[2] != K or tuple(B.shape) != (E, N, r):
+    E, r, AK = A.shape
+    if AK != K or B.shape != (E, N, r):
         raise ValueError(f"adapter shapes {tuple(A.shape)}, {tuple(B.shape)} do not fit X {tuple(X.shape)}, Y {tuple(Y.shape)}")
-    rows_per_x = int(rows_per_x)
     if rows_per_x < 1 or xrows != (rows + rows_per_x - 1) // rows_per_x:
         raise ValueError(f"X has {xrows} rows for {rows} rows of Y and rows_per_x={rows_per_x}")
     if scale is not None and (scale.dtype != torch.float32 or not scale.is_contiguous() or scale.numel() != E):
@@ -681,14 +687,18 @@ def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
     if plan is None and _ids(where, "ids").numel() != rows:
         raise ValueError("ids must hold an id per row of Y")
     if ws is None:
-        ws = torch.empty(max(lib().qf_lora_apply_workspace(rows, K, r, E, int(plan is not None)), 1), dtype=torch.uint8,
-                         device=X.device)
-    head = (X.data_ptr(), ldx, rows_per_x, A.data_ptr(), B.data_ptr(), _ptr(scale), E)
-    tail = (Y.data_ptr(), ldy, rows, N, K, r, ws.data_ptr(), ws.numel() * ws.element_size())
-    if plan is None:
-        _call(dev, name, *head, where.data_ptr(), *tail)
+        ws_bytes = lib().qf_lora_apply_workspace(rows, K, r, E, plan is not None)
+        if ws_bytes:
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=X.device)
     else:
-        _call(dev, name, *head, plan.offsets.data_ptr(), plan.order.data_ptr(), plan.tiles.data_ptr(), plan.n_ids, *tail)
+        ws_bytes = ws.numel() * ws.element_size()
+    if plan is None:
+        _call(dev, name, X.data_ptr(), ldx, rows_per_x, A.data_ptr(), B.data_ptr(), _ptr(scale), E, where.data_ptr(),
+              Y.data_ptr(), ldy, rows, N, K, r, _ptr(ws), ws_bytes)
+    else:
+        _call(dev, name, X.data_ptr(), ldx, rows_per_x, A.data_ptr(), B.data_ptr(), _ptr(scale), E,
+              plan.offsets.data_ptr(), plan.order.data_ptr(), plan.tiles.data_ptr(), plan.n_ids, Y.data_ptr(), ldy, rows, N,
+              K, r, _ptr(ws), ws_bytes)
     return Y
 
 

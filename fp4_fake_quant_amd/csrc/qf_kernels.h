@@ -198,11 +198,11 @@ struct LoraApplyArgs {
   const int32_t* offsets;   // tiles form: the row plan
   const int32_t* order;
   const int32_t* tiles;
-  float* S;                 // workspace [splits][rows][rpad]; by row (rows form) or position (tiles form)
+  float* S;                 // tiles form: workspace [splits][positions][rpad]
   int32_t rows, rows_per_x, K, N, r, rpad, n_adapters, n_ids, splits, n_part;
 };
 inline int lora_apply_rpad(int r) { return (r + 15) / 16 * 16; }   // S's row length
-int lora_apply_splits(bool tiles, int64_t units, int K, int r);
+int lora_apply_splits(int64_t tiles, int K);
 hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipStream_t s);
 
 // ----------------------------------------------------------------- routing ---

@@ -4,14 +4,14 @@
 // rollout batch holds rows of many adapters, and the shared (packed) weight stays as it is.
 //
 // Two steps, S = X A^T (fp32) and Y += (scale S) B^T, in one of two forms:
-//   rows   few rows: a workgroup per row (and part of K or of N), vector FMAs; the adapters'
+//   rows   few rows: one launch, a workgroup per row and part of N, vector FMAs; the adapters'
 //          bytes are the work, and a decode step's rows rarely share an adapter.
 //   tiles  otherwise: the row plan's tiles of up to 32 rows of one adapter, on the bf16 matrix
 //          cores (16x16x32).  X is read once; the second step accumulates onto Y in fp32 and
 //          rounds once.  S enters the matrix cores as the sum of two bf16 (hi + lo, relative
 //          error below 2^-16), so its rounding stays far under Y's own.
 // Both are bounded by memory: X and Y pass once, 4 r flops per X element and per Y element.
-// K is split over workgroups when there are few rows; the parts of S are summed in a fixed
+// K is split over workgroups when there are few tiles; the parts of S are summed in a fixed
 // order by the second step (no atomics: same inputs, same bits).
 #include <algorithm>
 #include <string.h>
@@ -27,8 +27,8 @@ typedef float la_f32x4 __attribute__((ext_vector_type(4)));
 constexpr int LA_WG = 256, LA_WAVES = LA_WG / 64;
 constexpr int LA_KSTEP = 128;                      // K per wave and step, at most
 constexpr int LA_NSTEP = 64;                       // N per wave and step: 128 bytes of every row
-constexpr int LA_ROW_RANKS = 16;                   // adapter rows per workgroup of the rows form
-constexpr int LA_ROW_K = LA_WG * 8;                // K per pass of a rows-form workgroup
+constexpr int LR_WG = 1024, LR_WAVES = LR_WG / 64; // the rows form
+constexpr int LR_RANKS = 8;                        // adapter rows per wave and pass there
 
 __device__ __forceinline__ float la_wave_sum(float v) {
   v += __uint_as_float(dpp_xor1(__float_as_uint(v)));
@@ -77,71 +77,93 @@ __device__ __forceinline__ void la_swap8(uint4& v0, uint4& v1, bool low) {
 }
 
 // ---------------------------------------------------------------- rows form ----
-__global__ __launch_bounds__(LA_WG) void k_lora_row_down(LoraApplyArgs a) {
-  __shared__ float part[LA_WAVES][LA_ROW_RANKS];
-  const int row = blockIdx.x, r0 = blockIdx.y * LA_ROW_RANKS, split = blockIdx.z;
+// A workgroup per row and part of N, both steps in one launch: every part computes the row's S
+// again (its adapter's A comes from L2 after the first), which is shorter than a second launch.
+// The waves split K (kw of them, each lane 8 columns at a time) and, where K has fewer than 16
+// waves' columns, the adapter rows; their sums meet in LDS in a fixed order.  The first outputs'
+// B rows and Y are loaded before S is there.
+template <bool VEC>
+__global__ __launch_bounds__(LR_WG) void k_lora_rows(LoraApplyArgs a) {
+  __shared__ float part[LR_WAVES * QF_LORA_APPLY_MAX_R];
+  __shared__ float s[QF_LORA_APPLY_MAX_R];
+  const int row = blockIdx.y, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int e = a.ids[row];
   if ((uint32_t)e >= (uint32_t)a.n_adapters) return;
   const uint16_t* x = a.X + (int64_t)(row / a.rows_per_x) * a.ldx;
-  const uint16_t* A = a.A + ((int64_t)e * a.r + r0) * a.K;
-  const int nr = a.r - r0 < LA_ROW_RANKS ? a.r - r0 : LA_ROW_RANKS;
-  float acc[LA_ROW_RANKS];
+  const uint16_t* A = a.A + (int64_t)e * a.r * a.K;
+  const uint16_t* B = a.B + (int64_t)e * a.N * a.r;
+  const int n1 = std::min(a.N, (int)(blockIdx.x + 1) * a.n_part);
+  int n = blockIdx.x * a.n_part + threadIdx.x;
+  uint4 b0 = {0, 0, 0, 0}, b1 = {0, 0, 0, 0};
+  uint32_t y0 = 0;
+  if (n < n1) {
+    y0 = a.Y[(int64_t)row * a.ldy + n];
+    b0 = la_rank8<VEC>(B + (int64_t)n * a.r, 0, a.r);
+    b1 = la_rank8<VEC>(B + (int64_t)n * a.r, 8, a.r);
+  }
+
+  int kw = 1;
+  while (kw < LR_WAVES && kw * 512 < a.K) kw *= 2;
+  const int groups = LR_WAVES / kw, per = (a.r + groups - 1) / groups;
+  const int kwave = wave & (kw - 1), r0 = wave / kw * per, r1 = std::min(a.r, r0 + per);
+  for (int rc = r0; rc < r1; rc += LR_RANKS) {
+    float acc[LR_RANKS];
 #pragma unroll
-  for (int j = 0; j < LA_ROW_RANKS; ++j) acc[j] = 0.0f;
-  for (int k = split * LA_ROW_K + threadIdx.x * 8; k < a.K; k += a.splits * LA_ROW_K) {
-    float xf[8];
-    la_unpack8(*reinterpret_cast<const uint4*>(x + k), xf);
-    uint4 w[LA_ROW_RANKS];
+    for (int j = 0; j < LR_RANKS; ++j) acc[j] = 0.0f;
+    for (int k = (kwave * 64 + lane) * 8; k < a.K; k += kw * 512) {
+      const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
+      uint4 w[LR_RANKS];
 #pragma unroll
-    for (int j = 0; j < LA_ROW_RANKS; ++j)
-      if (j < nr) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)j * a.K + k);
+      for (int j = 0; j < LR_RANKS; ++j) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)std::min(rc + j, r1 - 1) * a.K + k);
+      float xf[8];
+      la_unpack8(xv, xf);
 #pragma unroll
-    for (int j = 0; j < LA_ROW_RANKS; ++j) {
-      if (j < nr) {
+      for (int j = 0; j < LR_RANKS; ++j) {
         float f[8];
         la_unpack8(w[j], f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[j] = __builtin_fmaf(xf[i], f[i], acc[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < LR_RANKS; ++j) {
+      acc[j] = la_wave_sum(acc[j]);
+      if (lane == 0 && rc + j < r1) part[kwave * a.r + rc + j] = acc[j];
+    }
   }
-#pragma unroll
-  for (int j = 0; j < LA_ROW_RANKS; ++j) acc[j] = la_wave_sum(acc[j]);
-  if ((threadIdx.x & 63) == 0)
-#pragma unroll
-    for (int j = 0; j < LA_ROW_RANKS; ++j) part[threadIdx.x >> 6][j] = acc[j];
   __syncthreads();
-  if ((int)threadIdx.x < nr)
-    a.S[((int64_t)split * a.rows + row) * a.rpad + r0 + threadIdx.x] =
-        (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
-}
-
-template <bool VEC>
-__global__ __launch_bounds__(LA_WG) void k_lora_row_up(LoraApplyArgs a) {
-  __shared__ float s[QF_LORA_APPLY_MAX_R];
-  const int row = blockIdx.y;
-  const int e = a.ids[row];
-  if ((uint32_t)e >= (uint32_t)a.n_adapters) return;
-  const float scale = a.scale ? a.scale[e] : 1.0f;
   if ((int)threadIdx.x < QF_LORA_APPLY_MAX_R) {
     float v = 0.0f;
-    if ((int)threadIdx.x < a.r)
-      for (int p = 0; p < a.splits; ++p) v += a.S[((int64_t)p * a.rows + row) * a.rpad + threadIdx.x];
-    s[threadIdx.x] = v * scale;                    // zero past r
+    if ((int)threadIdx.x < a.r) {
+      for (int w = 0; w < kw; ++w) v += part[w * a.r + threadIdx.x];
+      v *= a.scale ? a.scale[e] : 1.0f;
+    }
+    s[threadIdx.x] = v;                            // zero past r
   }
   __syncthreads();
-  const int n = blockIdx.x * LA_WG + threadIdx.x;
-  if (n >= a.N) return;
-  const uint16_t* b = a.B + ((int64_t)e * a.N + n) * a.r;
-  uint16_t* y = a.Y + (int64_t)row * a.ldy + n;
-  float acc = __uint_as_float((uint32_t)*y << 16);
-  for (int k = 0; k < a.r; k += 8) {
+  while (n < n1) {
+    float acc = __uint_as_float(y0 << 16);
     float f[8];
-    la_unpack8(la_rank8<VEC>(b, k, a.r), f);
+    la_unpack8(b0, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[k + i], acc);
+    for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[i], acc);
+    la_unpack8(b1, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[8 + i], acc);
+    for (int k = 16; k < a.r; k += 8) {
+      la_unpack8(la_rank8<VEC>(B + (int64_t)n * a.r, k, a.r), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[k + i], acc);
+    }
+    a.Y[(int64_t)row * a.ldy + n] = (uint16_t)pack_bf16x2(acc, 0.0f);
+    n += LR_WG;
+    if (n < n1) {
+      y0 = a.Y[(int64_t)row * a.ldy + n];
+      b0 = la_rank8<VEC>(B + (int64_t)n * a.r, 0, a.r);
+      b1 = la_rank8<VEC>(B + (int64_t)n * a.r, 8, a.r);
+    }
   }
-  *y = (uint16_t)pack_bf16x2(acc, 0.0f);
 }
 
 // --------------------------------------------------------------- tiles form ----
@@ -423,14 +445,12 @@ void launch_up(const LoraApplyArgs& a, dim3 g, bool vb, bool vy, hipStream_t s) 
 }
 }  // namespace
 
-// K parts: enough workgroups to fill the chip when there are few rows or tiles, each wave
-// keeping at least one step.
-int lora_apply_splits(bool tiles, int64_t units, int K, int r) {
-  const int64_t wgs = tiles ? units : units * ((r + LA_ROW_RANKS - 1) / LA_ROW_RANKS);
-  const int per = tiles ? LA_WAVES * LA_KSTEP : LA_ROW_K;
-  const int most = std::min((K + per - 1) / per, LORA_APPLY_MAX_SPLITS);
+// K parts of the tiles form: enough workgroups to fill the chip when there are few tiles, each
+// wave keeping at least one step.
+int lora_apply_splits(int64_t tiles, int K) {
+  const int most = std::min((K + LA_WAVES * LA_KSTEP - 1) / (LA_WAVES * LA_KSTEP), LORA_APPLY_MAX_SPLITS);
   int s = 1;
-  while (s * 2 <= most && wgs * s < (tiles ? 1024 : 512)) s *= 2;
+  while (s * 2 <= most && tiles * s < 1024) s *= 2;
   return s;
 }
 
@@ -438,13 +458,13 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
   const bool vb = a.r % 8 == 0 && (uintptr_t)a.B % 16 == 0;
   const bool vy = a.ldy % 8 == 0 && (uintptr_t)a.Y % 16 == 0;
   if (!tiles) {
-    const dim3 g1((unsigned)a.rows, (unsigned)((a.r + LA_ROW_RANKS - 1) / LA_ROW_RANKS), (unsigned)a.splits);
-    k_lora_row_down<<<g1, LA_WG, 0, s>>>(a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const dim3 g2((unsigned)((a.N + LA_WG - 1) / LA_WG), (unsigned)a.rows);
-    if (vb) k_lora_row_up<true><<<g2, LA_WG, 0, s>>>(a);
-    else k_lora_row_up<false><<<g2, LA_WG, 0, s>>>(a);
+    // parts of N: about one workgroup per CU, each with at least one output per thread
+    const int most = (a.N + LR_WG - 1) / LR_WG;
+    const int parts = std::min(most, std::max(1, 256 / a.rows));
+    a.n_part = ((a.N + parts - 1) / parts + 63) / 64 * 64;
+    const dim3 g((unsigned)((a.N + a.n_part - 1) / a.n_part), (unsigned)a.rows);
+    if (vb) k_lora_rows<true><<<g, LR_WG, 0, s>>>(a);
+    else k_lora_rows<false><<<g, LR_WG, 0, s>>>(a);
     return hipGetLastError();
   }
   const dim3 g1((unsigned)n_tiles, (unsigned)a.splits);
@@ -452,7 +472,7 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
   else if (a.r <= 32) k_lora_tile_down<2><<<g1, LA_WG, 0, s>>>(a);
   else if (a.r <= 64) k_lora_tile_down<4><<<g1, LA_WG, 0, s>>>(a);
   else k_lora_tile_down<8><<<g1, LA_WG, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // N parts: whole passes of the four waves; enough workgroups to fill the chip about once, no
   // more (each pays for its tile's rows and S before its first product)
@@ -487,11 +507,10 @@ struct Space {
 Space space_of(int64_t rows, int64_t K, int r, int n_adapters, bool planned) {
   Space o;
   memset(&o, 0, sizeof(o));
-  const bool tiles = planned || !row_form(rows);
+  if (!planned && row_form(rows)) return o;
   const int64_t n_tiles = qf_row_plan_tiles(rows, n_adapters);
-  const int splits = qf::lora_apply_splits(tiles, tiles ? n_tiles : rows, (int)K, r);
-  int64_t at = up256(rows * qf::lora_apply_rpad(r) * 4 * splits);
-  if (tiles && !planned) {
+  int64_t at = up256(rows * qf::lora_apply_rpad(r) * 4 * qf::lora_apply_splits(n_tiles, (int)K));
+  if (!planned) {
     o.offsets = at;
     at += up256((int64_t)(n_adapters + 1) * 4);
     o.order = at;
@@ -522,8 +541,8 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
       bad(offsets, 4) || bad(order, 4) || bad(tiles, 8))
     return QF_ERR_ALIGN;
   const Space sp = space_of(rows, K, r, n_adapters, planned);
-  if (!ws || ws_bytes < (size_t)sp.total) return QF_ERR_WORKSPACE;
-  if (bad(ws, 16)) return QF_ERR_ALIGN;
+  if (sp.total > 0 && (!ws || ws_bytes < (size_t)sp.total)) return QF_ERR_WORKSPACE;
+  if (sp.total > 0 && bad(ws, 16)) return QF_ERR_ALIGN;
   const bool tiled = planned || !row_form(rows);
   char* base = (char*)ws;
   if (tiled && !planned) {
@@ -560,7 +579,7 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
   a.n_adapters = n_adapters;
   a.n_ids = n_ids;
   const int64_t n_tiles = tiled ? qf_row_plan_tiles(rows, n_ids) : 0;
-  a.splits = qf::lora_apply_splits(tiled, tiled ? qf_row_plan_tiles(rows, n_adapters) : rows, a.K, r);
+  a.splits = tiled ? qf::lora_apply_splits(qf_row_plan_tiles(rows, n_adapters), a.K) : 1;
   return qf::status_of(qf::launch_lora_apply(a, tiled, n_tiles, (hipStream_t)stream));
 }
 

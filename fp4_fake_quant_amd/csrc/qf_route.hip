@@ -38,10 +38,20 @@ __device__ __forceinline__ float rt_row_max(float v) {
   if (L > 16) v = fmaxf(v, __uint_as_float(swz_xor16(__float_as_uint(v))));
   return v;
 }
+template <int CTRL>
+__device__ __forceinline__ double rt_dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 template <int L>
 __device__ __forceinline__ double rt_row_max(double v) {
-#pragma unroll
-  for (int d = 1; d < L; d <<= 1) v = fmax(v, __shfl_xor(v, d));
+  v = fmax(v, rt_dpp<0xB1>(v));        // lane ^ 1, lane ^ 2, then mirrors as for float
+  v = fmax(v, rt_dpp<0x4E>(v));
+  v = fmax(v, rt_dpp<0x141>(v));
+  v = fmax(v, rt_dpp<0x140>(v));
+  if (L > 16) v = fmax(v, __shfl_xor(v, 16));
   return v;
 }
 template <int L, typename T>
@@ -101,8 +111,8 @@ struct RtGroups {
 };
 
 __device__ __forceinline__ void rt_top2(double& m1, double& m2, double v) {
-  m2 = v > m1 ? m1 : (v > m2 ? v : m2);
-  m1 = v > m1 ? v : m1;
+  m2 = fmax(m2, fmin(m1, v));
+  m1 = fmax(m1, v);
 }
 __device__ __forceinline__ void rt_top2(float& m1, float& m2, float v) {
   m2 = __builtin_amdgcn_fmed3f(m1, m2, v);
@@ -176,6 +186,7 @@ __device__ __forceinline__ bool rt_groups(const RouteArgs& a, int sub, int lane,
 // chosen.
 template <int L, int V, typename K>
 __device__ __forceinline__ void rt_select(const RouteArgs& a, int lane, uint64_t seg, K (&key)[V], int32_t* chosen) {
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     K best = key[0];
     int slot = 0;
@@ -248,6 +259,37 @@ __device__ __forceinline__ bool rt_select_keys(int rounds, int lane, const uint3
 }
 
 constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
+
+// exp in 64 bits for finite x <= 709: x = n ln 2 + r, |r| <= ln 2 / 2, and r's Taylor polynomial
+// (the term after the last is below 2^-57); about two units of rounding.  The second pass is rare
+// and its code cold, so it is short.
+__device__ __forceinline__ double rt_exp64(double x) {
+  x = fmax(x, -745.0);                               // below, exp is 0 in 64 bits
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
+  r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);   // ln 2 in two parts
+  double p = 1.0 / 6227020800.0;                     // 1 / 13!
+  p = __builtin_fma(p, r, 1.0 / 479001600.0);
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.0);
+  p = __builtin_fma(p, r, 1.0);
+  return __builtin_ldexp(p, (int)n);
+}
+// 1 / d for d in [1, inf]: the hardware's approximation and two Newton steps.
+__device__ __forceinline__ double rt_rcp64(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
 
 __device__ __forceinline__ float rt_fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
@@ -381,13 +423,16 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          key2[i] = softmax ? exp((double)x[i] - (double)top) : 1.0 / (1.0 + exp(-(double)x[i]));
+          // a masked logit's score does not matter below; exp(-x) stays finite (sigmoids from 2^-1021)
+          const double d = softmax ? (double)x[i] - (double)top : fmin(-(double)x[i], 708.0);
+          key2[i] = rt_exp64(d);
           sum += key2[i];
         }
         if (softmax) sum = rt_row_sum<L>(sum);
+        const double inv = softmax ? 1.0 / sum : 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          if (softmax) key2[i] = key2[i] / sum;
+          key2[i] = softmax ? key2[i] * inv : rt_rcp64(1.0 + key2[i]);
           key2[i] = x[i] > -RT_INF ? key2[i] + (double)bias[i] : -(double)RT_INF;
         }
         if constexpr (GROUPS != 0) rt_groups<L, V, GROUPS, K2>(a, sub, lane, key2, gs2, 0.0);

@@ -84,7 +84,7 @@ def check_apply(c, d, planned, scaled=True):
 
 @pytest.mark.parametrize("planned", [False, True])
 @pytest.mark.parametrize("T,K,N,r,E", [
-    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (65, 2056, 300, 16, 9),
+    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (65, 2056, 300, 16, 9), (2, 8200, 2100, 17, 3), (5, 520, 70, 128, 2),
     (33, 256, 64, 32, 1), (100, 520, 130, 33, 2), (97, 128, 257, 64, 5), (200, 200, 72, 128, 3), (130, 64, 40, 100, 40),
     (300, 96, 2000, 8, 1000), (1000, 1024, 96, 4, 7)])
 def test_apply(T, K, N, r, E, planned):
@@ -190,4 +190,5 @@ def test_binding_checks():
     with pytest.raises(ValueError):
         fq.qf_row_plan(d["ids"], 1025)
     with pytest.raises(fq.QFError):
-        fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], fq.qf_row_plan(d["ids"], 4), d["Y"],
+                                 ws=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -91,9 +91,12 @@ def test_lora_apply_refusals():
         for k in ("X", "A", "B", "Y"):
             assert c(**{k: None}) == 1
         assert c(X=P(0x10000008)) == 3 and c(A=P(0x10000008)) == 3 and c(ldx=68) == 3 and c(B=P(0x10000001)) == 3
-        assert c(Y=P(0x10000001)) == 3 and c(S=P(0x10000002)) == 3 and c(ws=P(0x10000008)) == 3
-        need = L.qf_lora_apply_workspace(10, 64, 8, 4, int(planned))
-        assert need > 0 and c(ws=None) == 4 and c(wsb=need - 1) == 4
+        assert c(Y=P(0x10000001)) == 3 and c(S=P(0x10000002)) == 3
+        rows = 10 if planned else 1000                     # few rows without a plan need no workspace
+        need = L.qf_lora_apply_workspace(rows, 64, 8, 4, int(planned))
+        assert need > 0 and c(rows=rows, ws=None) == 4 and c(rows=rows, wsb=need - 1) == 4
+        assert c(rows=rows, ws=P(0x10000008)) == 3
+    assert L.qf_lora_apply_workspace(64, 64, 8, 4, 0) == 0
     assert call(ids=None) == 1 and call(ids=P(0x10000002)) == 3
     for k in ("off", "order", "tiles"):
         assert call(True, **{k: None}) == 1 and call(True, **{k: P(0x10000002)}) == 3
