@@ -184,7 +184,10 @@ struct RowPlanArgs {
 hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
 
 // ------------------------------------------------- adapters beside a product ---
-constexpr int LORA_APPLY_ROW_FORM = 64;     // rows up to which a call without a plan goes row by row
+// Rows up to which a call without a plan goes row by row.  Microseconds row by row / in tiles, for
+// 1 and 64 adapters: 4096 -> 6144 rank 16, 256 rows 8.6 / 18 and 14 / 23, 512 rows 16 / 19 and
+// 24 / 25; 4096 -> 4096 rank 64, 256 rows 31 / 36 and 47 / 65, 512 rows 59 / 48 and 88 / 76.
+constexpr int LORA_APPLY_ROW_FORM = QF_LORA_APPLY_FEW;
 constexpr int LORA_APPLY_MAX_SPLITS = 8;    // K parts
 
 struct LoraApplyArgs {

@@ -28,7 +28,6 @@ constexpr int LA_WG = 256, LA_WAVES = LA_WG / 64;
 constexpr int LA_KSTEP = 128;                      // K per wave and step, at most
 constexpr int LA_NSTEP = 64;                       // N per wave and step: 128 bytes of every row
 constexpr int LR_WG = 1024, LR_WAVES = LR_WG / 64; // the rows form
-constexpr int LR_RANKS = 8;                        // adapter rows per wave and pass there
 
 __device__ __forceinline__ float la_wave_sum(float v) {
   v += __uint_as_float(dpp_xor1(__float_as_uint(v)));
@@ -81,8 +80,9 @@ __device__ __forceinline__ void la_swap8(uint4& v0, uint4& v1, bool low) {
 // again (its adapter's A comes from L2 after the first), which is shorter than a second launch.
 // The waves split K (kw of them, each lane 8 columns at a time) and, where K has fewer than 16
 // waves' columns, the adapter rows; their sums meet in LDS in a fixed order.  The first outputs'
-// B rows and Y are loaded before S is there.
-template <bool VEC>
+// B rows and Y are loaded before S is there.  RANKS: adapter rows per wave and pass (all their
+// loads in flight at once); C: groups of 8 of B's columns loaded at once.
+template <int RANKS, int C, bool VEC>
 __global__ __launch_bounds__(LR_WG) void k_lora_rows(LoraApplyArgs a) {
   __shared__ float part[LR_WAVES * QF_LORA_APPLY_MAX_R];
   __shared__ float s[QF_LORA_APPLY_MAX_R];
@@ -95,31 +95,34 @@ __global__ __launch_bounds__(LR_WG) void k_lora_rows(LoraApplyArgs a) {
   const uint16_t* B = a.B + (int64_t)e * a.N * a.r;
   const int n1 = std::min(a.N, (int)(blockIdx.x + 1) * a.n_part);
   int n = blockIdx.x * a.n_part + threadIdx.x;
-  uint4 b0 = {0, 0, 0, 0}, b1 = {0, 0, 0, 0};
+  uint4 b[C];
   uint32_t y0 = 0;
+  auto load_b = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) b[c] = la_rank8<VEC>(B + (int64_t)n * a.r, k + 8 * c, a.r);
+  };
   if (n < n1) {
     y0 = a.Y[(int64_t)row * a.ldy + n];
-    b0 = la_rank8<VEC>(B + (int64_t)n * a.r, 0, a.r);
-    b1 = la_rank8<VEC>(B + (int64_t)n * a.r, 8, a.r);
+    load_b(0);
   }
 
   int kw = 1;
   while (kw < LR_WAVES && kw * 512 < a.K) kw *= 2;
   const int groups = LR_WAVES / kw, per = (a.r + groups - 1) / groups;
   const int kwave = wave & (kw - 1), r0 = wave / kw * per, r1 = std::min(a.r, r0 + per);
-  for (int rc = r0; rc < r1; rc += LR_RANKS) {
-    float acc[LR_RANKS];
+  for (int rc = r0; rc < r1; rc += RANKS) {
+    float acc[RANKS];
 #pragma unroll
-    for (int j = 0; j < LR_RANKS; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < RANKS; ++j) acc[j] = 0.0f;
     for (int k = (kwave * 64 + lane) * 8; k < a.K; k += kw * 512) {
       const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
-      uint4 w[LR_RANKS];
+      uint4 w[RANKS];
 #pragma unroll
-      for (int j = 0; j < LR_RANKS; ++j) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)std::min(rc + j, r1 - 1) * a.K + k);
+      for (int j = 0; j < RANKS; ++j) w[j] = *reinterpret_cast<const uint4*>(A + (int64_t)std::min(rc + j, r1 - 1) * a.K + k);
       float xf[8];
       la_unpack8(xv, xf);
 #pragma unroll
-      for (int j = 0; j < LR_RANKS; ++j) {
+      for (int j = 0; j < RANKS; ++j) {
         float f[8];
         la_unpack8(w[j], f);
 #pragma unroll
@@ -127,7 +130,7 @@ __global__ __launch_bounds__(LR_WG) void k_lora_rows(LoraApplyArgs a) {
       }
     }
 #pragma unroll
-    for (int j = 0; j < LR_RANKS; ++j) {
+    for (int j = 0; j < RANKS; ++j) {
       acc[j] = la_wave_sum(acc[j]);
       if (lane == 0 && rc + j < r1) part[kwave * a.r + rc + j] = acc[j];
     }
@@ -144,24 +147,21 @@ __global__ __launch_bounds__(LR_WG) void k_lora_rows(LoraApplyArgs a) {
   __syncthreads();
   while (n < n1) {
     float acc = __uint_as_float(y0 << 16);
-    float f[8];
-    la_unpack8(b0, f);
+    for (int k = 0; k < a.r; k += 8 * C) {
+      if (k > 0) load_b(k);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[i], acc);
-    la_unpack8(b1, f);
+      for (int c = 0; c < C; ++c) {                // zero past r on both sides
+        float f[8];
+        la_unpack8(b[c], f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[8 + i], acc);
-    for (int k = 16; k < a.r; k += 8) {
-      la_unpack8(la_rank8<VEC>(B + (int64_t)n * a.r, k, a.r), f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[k + i], acc);
+        for (int i = 0; i < 8; ++i) acc = __builtin_fmaf(f[i], s[k + 8 * c + i], acc);
+      }
     }
     a.Y[(int64_t)row * a.ldy + n] = (uint16_t)pack_bf16x2(acc, 0.0f);
     n += LR_WG;
     if (n < n1) {
       y0 = a.Y[(int64_t)row * a.ldy + n];
-      b0 = la_rank8<VEC>(B + (int64_t)n * a.r, 0, a.r);
-      b1 = la_rank8<VEC>(B + (int64_t)n * a.r, 8, a.r);
+      load_b(0);
     }
   }
 }
@@ -463,8 +463,10 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
     const int parts = std::min(most, std::max(1, 256 / a.rows));
     a.n_part = ((a.N + parts - 1) / parts + 63) / 64 * 64;
     const dim3 g((unsigned)((a.N + a.n_part - 1) / a.n_part), (unsigned)a.rows);
-    if (vb) k_lora_rows<true><<<g, LR_WG, 0, s>>>(a);
-    else k_lora_rows<false><<<g, LR_WG, 0, s>>>(a);
+    if (a.r <= 16 && vb) k_lora_rows<8, 2, true><<<g, LR_WG, 0, s>>>(a);
+    else if (a.r <= 16) k_lora_rows<8, 2, false><<<g, LR_WG, 0, s>>>(a);
+    else if (vb) k_lora_rows<16, 4, true><<<g, LR_WG, 0, s>>>(a);
+    else k_lora_rows<16, 4, false><<<g, LR_WG, 0, s>>>(a);
     return hipGetLastError();
   }
   const dim3 g1((unsigned)n_tiles, (unsigned)a.splits);

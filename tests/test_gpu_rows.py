@@ -84,8 +84,8 @@ def check_apply(c, d, planned, scaled=True):
 
 @pytest.mark.parametrize("planned", [False, True])
 @pytest.mark.parametrize("T,K,N,r,E", [
-    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (65, 2056, 300, 16, 9), (2, 8200, 2100, 17, 3), (5, 520, 70, 128, 2),
-    (33, 256, 64, 32, 1), (100, 520, 130, 33, 2), (97, 128, 257, 64, 5), (200, 200, 72, 128, 3), (130, 64, 40, 100, 40),
+    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (384, 2056, 300, 16, 9), (385, 2056, 300, 16, 9), (2, 8200, 2100, 17, 3), (5, 520, 70, 128, 2),
+    (33, 256, 64, 32, 1), (100, 520, 130, 33, 2), (97, 128, 257, 64, 5), (200, 200, 72, 128, 3), (430, 64, 40, 100, 40), (500, 640, 72, 128, 3), (444, 520, 130, 33, 2),
     (300, 96, 2000, 8, 1000), (1000, 1024, 96, 4, 7)])
 def test_apply(T, K, N, r, E, planned):
     c, d = case(T, K, N, r, E, T + r)
@@ -114,7 +114,7 @@ def test_apply_token_expert_pairs(T, planned):
 
 @pytest.mark.parametrize("planned", [False, True])
 def test_apply_all_and_none(planned):
-    for T in (20, 300):
+    for T in (20, 500):
         c, d = case(T, 128, 96, 16, 4, 10, none=1.1)
         check_apply(c, d, planned)
         c, d = case(T, 128, 96, 16, 4, 11, none=0.0)
@@ -135,7 +135,7 @@ def test_rows_without_adapter_are_not_read():
 
 def test_forms_agree_with_a_prefix():
     """A plan of fewer ids than adapters, and an empty batch."""
-    c, d = case(200, 128, 96, 16, 6, 13, none=0.0)
+    c, d = case(500, 128, 96, 16, 6, 13, none=0.0)
     c["ids"] %= 4
     d["ids"] %= 4
     plan = fq.qf_row_plan(d["ids"], 4)
