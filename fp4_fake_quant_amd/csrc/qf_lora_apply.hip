@@ -329,19 +329,21 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   }
   uint4 yv[2][2];
   auto load_y = [&](int at) {
-    const int n = at + off;
+    if (VEC_Y && at + LA_NSTEP <= a.N) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int v = 0; v < 2; ++v) yv[b][v] = *reinterpret_cast<const uint4*>(y[b][v] + at);
+      return;
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        if (VEC_Y && n + 8 <= a.N) {
-          yv[b][v] = *reinterpret_cast<const uint4*>(y[b][v] + at);
-          continue;
-        }
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (n + j < a.N) w[j >> 1] |= (uint32_t)y[b][v][at + j] << (16 * (j & 1));
+          if (at + off + j < a.N) w[j >> 1] |= (uint32_t)y[b][v][at + j] << (16 * (j & 1));
         yv[b][v] = uint4{w[0], w[1], w[2], w[3]};
       }
   };
@@ -349,33 +351,54 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
   uint4 sv[2][RB];
+  {
+    float v[2][RB][8];
+    const float* s[2];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const float* s = a.S + (int64_t)(t.first + std::min(16 * b + i, t.count - 1)) * a.rpad + (g & 1) * 8;
-    float v[RB][8];
-#pragma unroll
-    for (int k = 0; k < RB; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
-    for (int p = 0; p < a.splits; ++p, s += (int64_t)a.rows * a.rpad)
+    for (int b = 0; b < 2; ++b) {
+      s[b] = a.S + (int64_t)(t.first + std::min(16 * b + i, t.count - 1)) * a.rpad + (g & 1) * 8;
 #pragma unroll
       for (int k = 0; k < RB; ++k)
-        if (k * 16 < a.r) {
-          const float4 u = reinterpret_cast<const float4*>(s + k * 16)[0], w = reinterpret_cast<const float4*>(s + k * 16)[1];
-          v[k][0] += u.x; v[k][1] += u.y; v[k][2] += u.z; v[k][3] += u.w;
-          v[k][4] += w.x; v[k][5] += w.y; v[k][6] += w.z; v[k][7] += w.w;
-        }
 #pragma unroll
-    for (int k = 0; k < RB; ++k) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v0 = v[k][2 * j] * scale, v1 = v[k][2 * j + 1] * scale;
-        const uint32_t hi = pack_bf16x2(v0, v1);
-        w[j] = g < 2 ? hi : pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
-      }
-      sv[b][k] = uint4{w[0], w[1], w[2], w[3]};
+        for (int j = 0; j < 8; ++j) v[b][k][j] = 0.0f;
     }
+    for (int p = 0; p < a.splits; ++p) {
+      float4 u[2][RB][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)                // blocks past r repeat the last one, and are dropped
+            u[b][k][h] = reinterpret_cast<const float4*>(s[b] + std::min(k * 16, a.rpad - 16))[h];
+        s[b] += (int64_t)a.rows * a.rpad;
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            v[b][k][4 * h] += u[b][k][h].x;
+            v[b][k][4 * h + 1] += u[b][k][h].y;
+            v[b][k][4 * h + 2] += u[b][k][h].z;
+            v[b][k][4 * h + 3] += u[b][k][h].w;
+          }
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int k = 0; k < RB; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float v0 = v[b][k][2 * j] * scale, v1 = v[b][k][2 * j + 1] * scale;
+          const uint32_t hi = pack_bf16x2(v0, v1);
+          w[j] = g < 2 ? hi : pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
+          if (k * 16 >= a.r) w[j] = 0;
+        }
+        sv[b][k] = uint4{w[0], w[1], w[2], w[3]};
+      }
   }
   const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
   while (left > 0) {
@@ -399,11 +422,12 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int m = at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3);
+        // rows past N repeat the last one (not stored), columns past r the last ones (S is zero there)
+        const int m = std::min(at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3), a.N - 1);
 #pragma unroll
         for (int k = 0; k < RB; ++k) {
-          uint4 bv = {0, 0, 0, 0};
-          if (m < a.N) bv = la_rank8<VEC_B>(B + (int64_t)m * a.r, k * 16 + (g & 1) * 8, a.r);
+          const int c = k * 16 + (g & 1) * 8;
+          const uint4 bv = la_rank8<VEC_B>(B + (int64_t)m * a.r, VEC_B ? std::min(c, a.r - 8) : c, a.r);
 #pragma unroll
           for (int b = 0; b < 2; ++b)
             acc[b][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf16x8, bv),
@@ -417,19 +441,19 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) la_swap8(yc[b][0], yc[b][1], low);
-    const int n = at + off;
+    const bool whole = VEC_Y && at + LA_NSTEP <= a.N;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         if (row[b][v] < 0) continue;
-        if (VEC_Y && n + 8 <= a.N) {
+        if (whole) {
           *reinterpret_cast<uint4*>(y[b][v] + at) = yc[b][v];
         } else {
           const uint32_t w[4] = {yc[b][v].x, yc[b][v].y, yc[b][v].z, yc[b][v].w};
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (n + j < a.N) y[b][v][at + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+            if (at + off + j < a.N) y[b][v][at + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
         }
       }
   }
