@@ -188,7 +188,7 @@ hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
 // 1 and 64 adapters: 4096 -> 6144 rank 16, 256 rows 8.6 / 18 and 14 / 23, 512 rows 16 / 19 and
 // 24 / 25; 4096 -> 4096 rank 64, 256 rows 31 / 36 and 47 / 65, 512 rows 59 / 48 and 88 / 76.
 constexpr int LORA_APPLY_ROW_FORM = QF_LORA_APPLY_FEW;
-constexpr int LORA_APPLY_MAX_SPLITS = 8;    // K parts
+constexpr int LORA_APPLY_MAX_SPLITS = 4;    // K parts
 
 struct LoraApplyArgs {
   const uint16_t* X;
@@ -204,7 +204,7 @@ struct LoraApplyArgs {
   float* S;                 // tiles form: workspace [splits][positions][rpad]
   int32_t rows, rows_per_x, K, N, r, rpad, n_adapters, n_ids, splits, n_part;
 };
-inline int lora_apply_rpad(int r) { return (r + 15) / 16 * 16; }   // S's row length
+inline int lora_apply_rpad(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }   // S's row length
 int lora_apply_splits(int64_t tiles, int K);
 hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipStream_t s);
 

@@ -289,7 +289,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
       if (at < t.count)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
-          if (n * 16 < a.r)
+          if (n * 16 < a.rpad)
             a.S[((int64_t)split * a.rows + t.first + at) * a.rpad + n * 16 + i] = n * 16 + i < a.r ? acc[b][n][j] : 0.0f;
     }
 }
@@ -298,10 +298,12 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
 // tile's rows (two blocks of 16).  Row m of instruction `half` stands for n = n0 + 8 (m / 4) +
 // 4 half + m % 4 of a 32-wide step q, so that a lane's two results are 8 consecutive n of its row
 // and the four lanes of a row hold 64 contiguous bytes; the steps q = 0, 1 are the halves of a
-// 128-byte line, exchanged between lanes so that Y is accessed in whole lines.  The
-// instruction's 32 products are 16 adapter rows twice: S's high part in the first 16, its low part
-// in the others, B the same in both.  The next step's Y is loaded during this one's products.
-template <int RB, bool VEC_B, bool VEC_Y>
+// 128-byte line, exchanged between lanes so that Y is accessed in whole lines.  S is summed over
+// the K parts, scaled and split into its two bf16 once per workgroup, in LDS.  Up to rank 16 the
+// instruction's 32 products are 16 adapter rows twice, S's high part in the first 16, its low part
+// in the others, B the same in both; above, 32 adapter rows, one instruction for each part.  The
+// next step's Y is loaded during this one's products.  RK: blocks of 32 adapter rows (0: rank 16).
+template <int RK, bool VEC_B, bool VEC_Y>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   static_assert(LA_NSTEP == 64, "a step of the wave is one 128-byte line of every row");
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -350,56 +352,33 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   if (left > 0) load_y(n0);
 
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
-  uint4 sv[2][RB];
-  {
-    float v[2][RB][8];
-    const float* s[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      s[b] = a.S + (int64_t)(t.first + std::min(16 * b + i, t.count - 1)) * a.rpad + (g & 1) * 8;
-#pragma unroll
-      for (int k = 0; k < RB; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[b][k][j] = 0.0f;
+  constexpr int RP = RK == 0 ? 16 : 32 * RK, NS = RK == 0 ? 1 : 2, NK = RK == 0 ? 1 : RK;
+  __shared__ uint2 sp[2][QF_ROW_TILE][RP / 4 + 2];      // high and low parts; rows 16 bytes apart in banks
+  for (int c = threadIdx.x; c < QF_ROW_TILE * RP / 4; c += LA_WG) {
+    const int at = c / (RP / 4), k = c % (RP / 4) * 4;
+    const float* p = a.S + (int64_t)(t.first + std::min(at, t.count - 1)) * RP + k;
+    float4 v = *reinterpret_cast<const float4*>(p);
+    for (int q = 1; q < a.splits; ++q) {
+      const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)q * a.rows * RP);
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
-    for (int p = 0; p < a.splits; ++p) {
-      float4 u[2][RB][2];
+    v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+    const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
+    sp[0][at][k / 4] = uint2{h0, h1};
+    sp[1][at][k / 4] = uint2{pack_bf16x2(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
+                             pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1))};
+  }
+  __syncthreads();
+  // the lane's 8 adapter rows of block k
+  const int col = RK == 0 ? (g & 1) * 8 : g * 8;
+  uint4 sv[NS][2][NK];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int k = 0; k < RB; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)                // blocks past r repeat the last one, and are dropped
-            u[b][k][h] = reinterpret_cast<const float4*>(s[b] + std::min(k * 16, a.rpad - 16))[h];
-        s[b] += (int64_t)a.rows * a.rpad;
-      }
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int k = 0; k < RB; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            v[b][k][4 * h] += u[b][k][h].x;
-            v[b][k][4 * h + 1] += u[b][k][h].y;
-            v[b][k][4 * h + 2] += u[b][k][h].z;
-            v[b][k][4 * h + 3] += u[b][k][h].w;
-          }
-    }
+  for (int h = 0; h < NS; ++h)
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float v0 = v[b][k][2 * j] * scale, v1 = v[b][k][2 * j + 1] * scale;
-          const uint32_t hi = pack_bf16x2(v0, v1);
-          w[j] = g < 2 ? hi : pack_bf16x2(v0 - bf16_lo(hi), v1 - bf16_hi(hi));
-          if (k * 16 >= a.r) w[j] = 0;
-        }
-        sv[b][k] = uint4{w[0], w[1], w[2], w[3]};
-      }
-  }
+      for (int k = 0; k < NK; ++k)
+        sv[h][b][k] = *reinterpret_cast<const uint4*>(&sp[RK == 0 ? g >> 1 : h][16 * b + i][(k * 32 + col) / 4]);
   const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
   while (left > 0) {
     const int at = n0;
@@ -425,13 +404,15 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
         // rows past N repeat the last one (not stored), columns past r the last ones (S is zero there)
         const int m = std::min(at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3), a.N - 1);
 #pragma unroll
-        for (int k = 0; k < RB; ++k) {
-          const int c = k * 16 + (g & 1) * 8;
+        for (int k = 0; k < NK; ++k) {
+          const int c = k * 32 + col;
           const uint4 bv = la_rank8<VEC_B>(B + (int64_t)m * a.r, VEC_B ? std::min(c, a.r - 8) : c, a.r);
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
-            acc[b][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(la_bf16x8, bv),
-                                                                   __builtin_bit_cast(la_bf16x8, sv[b][k]), acc[b][half], 0, 0, 0);
+          for (int h = 0; h < NS; ++h)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              acc[b][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(la_bf16x8, bv), __builtin_bit_cast(la_bf16x8, sv[h][b][k]), acc[b][half], 0, 0, 0);
         }
       }
 #pragma unroll
@@ -460,12 +441,12 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 }
 
 namespace {
-template <int RB>
+template <int RK>
 void launch_up(const LoraApplyArgs& a, dim3 g, bool vb, bool vy, hipStream_t s) {
-  if (vb && vy) k_lora_tile_up<RB, true, true><<<g, LA_WG, 0, s>>>(a);
-  else if (vb) k_lora_tile_up<RB, true, false><<<g, LA_WG, 0, s>>>(a);
-  else if (vy) k_lora_tile_up<RB, false, true><<<g, LA_WG, 0, s>>>(a);
-  else k_lora_tile_up<RB, false, false><<<g, LA_WG, 0, s>>>(a);
+  if (vb && vy) k_lora_tile_up<RK, true, true><<<g, LA_WG, 0, s>>>(a);
+  else if (vb) k_lora_tile_up<RK, true, false><<<g, LA_WG, 0, s>>>(a);
+  else if (vy) k_lora_tile_up<RK, false, true><<<g, LA_WG, 0, s>>>(a);
+  else k_lora_tile_up<RK, false, false><<<g, LA_WG, 0, s>>>(a);
 }
 }  // namespace
 
@@ -506,10 +487,10 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
   const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1536 / n_tiles));
   a.n_part = ((a.N + parts - 1) / parts + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP) * (LA_WAVES * LA_NSTEP);
   const dim3 g2((unsigned)n_tiles, (unsigned)((a.N + a.n_part - 1) / a.n_part));
-  if (a.r <= 16) launch_up<1>(a, g2, vb, vy, s);
-  else if (a.r <= 32) launch_up<2>(a, g2, vb, vy, s);
-  else if (a.r <= 64) launch_up<4>(a, g2, vb, vy, s);
-  else launch_up<8>(a, g2, vb, vy, s);
+  if (a.r <= 16) launch_up<0>(a, g2, vb, vy, s);
+  else if (a.r <= 32) launch_up<1>(a, g2, vb, vy, s);
+  else if (a.r <= 64) launch_up<2>(a, g2, vb, vy, s);
+  else launch_up<4>(a, g2, vb, vy, s);
   return hipGetLastError();
 }
 
