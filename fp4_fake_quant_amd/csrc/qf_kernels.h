@@ -184,10 +184,12 @@ struct RowPlanArgs {
 hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
 
 // ------------------------------------------------- adapters beside a product ---
-// Rows up to which a call without a plan goes row by row.  Microseconds row by row / in tiles, for
-// 1 and 64 adapters: 4096 -> 6144 rank 16, 256 rows 8.6 / 18 and 14 / 23, 512 rows 16 / 19 and
-// 24 / 25; 4096 -> 4096 rank 64, 256 rows 31 / 36 and 47 / 65, 512 rows 59 / 48 and 88 / 76.
-constexpr int LORA_APPLY_ROW_FORM = QF_LORA_APPLY_FEW;
+// Rows up to which a call without a plan goes row by row: the whole adapter is read again for
+// every row, so fewer of higher ranks.  Microseconds row by row / plan and tiles, for 1 and for 64
+// adapters: 4096 -> 6144 rank 16, 256 rows 8.9 / 15.6 and 13.5 / 19.2, 512 rows 16.2 / 16.8 and
+// 24.1 / 21.2; 4096 -> 4096, rank 32, 256 rows 12.8 / 16.9 and 19.8 / 21.2; rank 64, 32 rows
+// 16.4 / 19.4 and 20.9 / 19.6, 96 rows 21.8 / 19.5 and 31.7 / 26.3; rank 128, 16 rows 28.9 / 24.5.
+inline int lora_apply_few(int r) { return r <= 32 ? QF_LORA_APPLY_FEW : r <= 64 ? 32 : 8; }
 constexpr int LORA_APPLY_MAX_SPLITS = 4;    // K parts
 
 struct LoraApplyArgs {

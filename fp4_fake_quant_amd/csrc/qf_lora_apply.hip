@@ -505,7 +505,7 @@ bool sizes_ok(int64_t rows, int64_t K, int64_t N, int r, int n_adapters) {
          N < (1 << 22) && r >= 1 && r <= QF_LORA_APPLY_MAX_R && n_adapters >= 1 && n_adapters <= QF_ROW_MAX_IDS;
 }
 
-bool row_form(int64_t rows) { return rows <= qf::LORA_APPLY_ROW_FORM; }
+bool row_form(int64_t rows, int r) { return rows <= qf::lora_apply_few(r); }
 
 // The workspace's parts: S, then the plan that a call without one makes for itself.
 struct Space {
@@ -514,7 +514,7 @@ struct Space {
 Space space_of(int64_t rows, int64_t K, int r, int n_adapters, bool planned) {
   Space o;
   memset(&o, 0, sizeof(o));
-  if (!planned && row_form(rows)) return o;
+  if (!planned && row_form(rows, r)) return o;
   const int64_t n_tiles = qf_row_plan_tiles(rows, n_adapters);
   int64_t at = up256(rows * qf::lora_apply_rpad(r) * 4 * qf::lora_apply_splits(n_tiles, (int)K));
   if (!planned) {
@@ -550,7 +550,7 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
   const Space sp = space_of(rows, K, r, n_adapters, planned);
   if (sp.total > 0 && (!ws || ws_bytes < (size_t)sp.total)) return QF_ERR_WORKSPACE;
   if (sp.total > 0 && bad(ws, 16)) return QF_ERR_ALIGN;
-  const bool tiled = planned || !row_form(rows);
+  const bool tiled = planned || !row_form(rows, r);
   char* base = (char*)ws;
   if (tiled && !planned) {
     int32_t* o = (int32_t*)(base + sp.offsets);
