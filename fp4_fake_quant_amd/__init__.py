@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from ._lib import AdamwHyper, AdamwTensor, GgufTensor, LoraDesc, LoraExpertsDesc, RouteDesc, StTensor, TensorDesc, lib
+from ._lib import AdamwHyper, AdamwPlan, AdamwTensor, GgufTensor, LoraDesc, LoraExpertsDesc, RouteDesc, StTensor, TensorDesc, lib
 
 QF_OK = 0
 QF_QDQ_A, QF_QDQ_W, QF_FP4_CORES, QF_MX_NOCLIP = 1, 2, 4, 8
@@ -744,8 +744,12 @@ class AdamwBatch:
     items: list of dict(p, g, m, v, m_scale=None, v_scale=None, p16=None, weight_decay=0.0) of
     contiguous device tensors with the same element count: p float32, g float32 or bfloat16,
     m and v float32 (state_bits 32) or uint8 with float32 scales per 256 elements (8), p16
-    bfloat16.  The tensors must keep their storage while the batch is used.
+    bfloat16.  The tensors must keep their storage while the batch is used.  More than FEW
+    tensors are described by a table in device memory (built here, outside a stream capture),
+    so that a step is one launch per gradient type.
     """
+
+    FEW = 8
 
     def __init__(self, items, state_bits=32):
         if state_bits not in (8, 32):
@@ -775,6 +779,13 @@ class AdamwBatch:
                 d.p16 = _flat(it["p16"], "p16", torch.bfloat16, n)
             d.n, d.weight_decay = n, float(it.get("weight_decay", 0.0))
         self.ref = ctypes.byref(self.arr)
+        self.plan = self.table = None
+        if self.n > self.FEW:
+            host = torch.empty(lib().qf_adamw_table_bytes(self.n), dtype=torch.uint8)
+            self.plan = AdamwPlan()
+            _check(lib().qf_adamw_table(self.ref, self.n, state_bits, host.data_ptr(), host.numel(),
+                                        ctypes.byref(self.plan)), "qf_adamw_table")
+            self.table = host.to(torch.device("cuda", self.device))
 
 
 def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_lr=None, d_step=None,
@@ -792,7 +803,10 @@ def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_l
             raise TypeError(f"{name} must be one {kinds[0]} on the tensors' device")
     h = AdamwHyper(lr, beta1, beta2, eps, step, _ptr(d_lr), _ptr(d_step), _ptr(d_grad_scale), _ptr(d_skip),
                    seed & 0xFFFFFFFF)
-    _call(batch.device, "qf_adamw_step", batch.ref, batch.n, batch.state_bits, ctypes.byref(h))
+    if batch.table is None:
+        _call(batch.device, "qf_adamw_step", batch.ref, batch.n, batch.state_bits, ctypes.byref(h))
+    else:
+        _call(batch.device, "qf_adamw_step_table", ctypes.byref(batch.plan), batch.table.data_ptr(), ctypes.byref(h))
 
 
 # ------------------------------------------------------------- dequant ----

@@ -80,6 +80,12 @@ class AdamwHyper(ctypes.Structure):
                 ("d_grad_scale", c_void_p), ("d_skip", c_void_p), ("seed", c_u32)]
 
 
+class AdamwPlan(ctypes.Structure):
+    """Mirror of qf_adamw_plan in include/qf.h."""
+    _fields_ = [("state_bits", ctypes.c_int32), ("capacity", ctypes.c_int32), ("tensors", ctypes.c_int32 * 2),
+                ("workgroups", c_u32 * 2)]
+
+
 # name -> (restype, argtypes); every entry point declared in include/qf.h
 SIGNATURES = {
     "qf_version": (c_u32, []),
@@ -156,6 +162,9 @@ SIGNATURES = {
     "qf_lora_apply_planned": (c_int, [c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p,
                                       c_void_p, c_int, c_void_p, c_i64, c_i64, c_i64, c_i64, c_int, c_void_p, c_size_t,
                                       c_void_p]),
+    "qf_adamw_table_bytes": (c_size_t, [c_int]),
+    "qf_adamw_table": (c_int, [c_void_p, c_int, c_int, c_void_p, c_size_t, c_void_p]),
+    "qf_adamw_step_table": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p]),
     "qf_adamw_step": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p]),
     "qf_noalloc_scratch_bytes": (c_size_t, []),
     "qf_nvfp4_tensor_scale_grouped_noalloc": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p]),

@@ -298,18 +298,39 @@ __device__ __forceinline__ void aw_blocks(const Args& a, const AdamwTensor& t, u
   }
 }
 
+// The tensor of workgroup wg: the last one that begins at or before it.  In the arguments all
+// beginnings are compared at once (scalar); in a table the wave's lanes compare 64 at a time, every
+// stride-th one first.
+template <int N>
+__device__ __forceinline__ const AdamwTensor& aw_find(const AdamwArgs<N>& a, uint32_t wg, uint32_t lane, uint32_t& begin) {
+  int ti = -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) ti += wg >= a.begin[i];
+  begin = a.begin[ti];
+  return a.t[ti];
+}
+__device__ __forceinline__ const AdamwTensor& aw_find(const AdamwTableArgs& a, uint32_t wg, uint32_t lane, uint32_t& begin) {
+  int lo = 0, len = a.n;
+  while (len > 1) {
+    const int stride = (len + 63) / 64, i = (int)lane * stride;
+    const uint64_t in = __ballot(i < len && wg >= a.begin[lo + (i < len ? i : 0)]);    // bit 0 always
+    lo += (__popcll(in) - 1) * stride;
+    len = stride < a.n - lo ? stride : a.n - lo;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  begin = a.begin[lo];
+  return a.t[lo];
+}
+
 template <int BITS, typename G, typename Args>
 __global__ __launch_bounds__(AW_WG) void k_adamw(Args a) {
   if (a.skip && *a.skip) return;
-  const uint32_t wg = blockIdx.x;
-  int ti = -1;
-#pragma unroll
-  for (int i = 0; i < Args::TENSORS; ++i) ti += wg >= a.begin[i];
-  const AdamwTensor& t = a.t[ti];
   const uint32_t lane = threadIdx.x & 63u;
+  uint32_t begin;
+  const AdamwTensor& t = aw_find(a, blockIdx.x, lane, begin);
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   constexpr int PER = aw_per_wave(BITS);
-  const uint32_t b0 = ((wg - a.begin[ti]) * (AW_WG / 64) + wave) * PER;   // first block of the wave
+  const uint32_t b0 = ((blockIdx.x - begin) * (AW_WG / 64) + wave) * PER;   // first block of the wave
   if ((uint64_t)(b0 + PER) * AW_BLOCK <= t.n)
     aw_blocks<BITS, G, true>(a, t, b0, lane);
   else if ((uint64_t)b0 * AW_BLOCK < t.n)
@@ -348,22 +369,26 @@ hipError_t launch_adamw(const AdamwArgs<AW_TENSORS>& a, int n, uint32_t grid, in
   return launch(f, grid, bits, g_bf16, s);
 }
 
+hipError_t launch_adamw_table(const AdamwTableArgs& a, uint32_t grid, int bits, bool g_bf16, hipStream_t s) {
+  return launch(a, grid, bits, g_bf16, s);
+}
+
 }  // namespace qf
 
 namespace {
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) != 0; }
-}  // namespace
 
-extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const qf_adamw_hyper* h,
-                                   void* stream) {
-  if (n < 0 || (state_bits != 32 && state_bits != 8)) return QF_ERR_ARG;
-  if (!h || (n > 0 && !t)) return QF_ERR_NULL;
+qf_status check_hyper(const qf_adamw_hyper* h) {
   // written so that a NaN fails
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0 && h->beta2 >= 0.0 && h->beta2 < 1.0 && h->eps >= 0.0)) return QF_ERR_ARG;
   if (!h->d_step && h->step < 1) return QF_ERR_ARG;
   if (!h->d_lr && !(h->lr >= 0.0 && h->lr <= 1e30)) return QF_ERR_ARG;
   if (misaligned(h->d_lr, 4) || misaligned(h->d_step, 8) || misaligned(h->d_grad_scale, 4) || misaligned(h->d_skip, 4))
     return QF_ERR_ALIGN;
+  return QF_OK;
+}
+
+qf_status check_tensors(const qf_adamw_tensor* t, int n, int state_bits) {
   for (int i = 0; i < n; ++i) {
     const qf_adamw_tensor& d = t[i];
     if (d.n < 0 || d.n >= (1ll << 31)) return QF_ERR_SHAPE;
@@ -376,7 +401,22 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
         misaligned(d.p16, 16) || misaligned(d.m_scale, 4) || misaligned(d.v_scale, 4))
       return QF_ERR_ALIGN;
   }
-  qf::AdamwArgs<qf::AW_TENSORS> a;
+  return QF_OK;
+}
+
+void fill(qf::AdamwTensor& o, const qf_adamw_tensor& d) {
+  o.p = d.p;
+  o.g = d.g;
+  o.m = d.m;
+  o.v = d.v;
+  o.ms = d.m_scale;
+  o.vs = d.v_scale;
+  o.p16 = d.p16;
+  o.n = (uint32_t)d.n;
+  o.weight_decay = d.weight_decay;
+}
+
+void common(qf::AdamwCommon& a, const qf_adamw_hyper* h) {
   a.beta1 = h->beta1;
   a.beta2 = h->beta2;
   a.eps = h->eps;
@@ -387,21 +427,27 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
   a.d_grad_scale = h->d_grad_scale;
   a.skip = h->d_skip;
   qf::adamw_host_scalars(a.s, h->lr, h->beta1, h->beta2, h->step, h->seed);
+}
+
+size_t table_begin(int n) { return sizeof(qf::AdamwTensor) * (size_t)n; }
+}  // namespace
+
+extern "C" {
+
+qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const qf_adamw_hyper* h, void* stream) {
+  if (n < 0 || (state_bits != 32 && state_bits != 8)) return QF_ERR_ARG;
+  if (!h || (n > 0 && !t)) return QF_ERR_NULL;
+  qf_status st = check_hyper(h);
+  if (st == QF_OK) st = check_tensors(t, n, state_bits);
+  if (st != QF_OK) return st;
+  qf::AdamwArgs<qf::AW_TENSORS> a;
+  common(a, h);
   for (int bf = 0; bf < 2; ++bf) {          // one run of launches per gradient type
     int k = 0;
     uint32_t grid = 0;
     for (int i = 0; i <= n; ++i) {
       if (i < n && t[i].n > 0 && t[i].g_bf16 == bf) {
-        qf::AdamwTensor& o = a.t[k];
-        o.p = t[i].p;
-        o.g = t[i].g;
-        o.m = t[i].m;
-        o.v = t[i].v;
-        o.ms = t[i].m_scale;
-        o.vs = t[i].v_scale;
-        o.p16 = t[i].p16;
-        o.n = (uint32_t)t[i].n;
-        o.weight_decay = t[i].weight_decay;
+        fill(a.t[k], t[i]);
         a.begin[k++] = grid;
         grid += qf::adamw_chunks(t[i].n, state_bits);
       }
@@ -416,3 +462,62 @@ extern "C" qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bi
   }
   return QF_OK;
 }
+
+size_t qf_adamw_table_bytes(int n) { return n <= 0 ? 0 : table_begin(n) + sizeof(uint32_t) * (size_t)n; }
+
+qf_status qf_adamw_table(const qf_adamw_tensor* t, int n, int state_bits, void* table, size_t bytes, qf_adamw_plan* plan) {
+  if (n < 0 || (state_bits != 32 && state_bits != 8)) return QF_ERR_ARG;
+  if (!plan || (n > 0 && (!t || !table))) return QF_ERR_NULL;
+  if (bytes < qf_adamw_table_bytes(n)) return QF_ERR_WORKSPACE;
+  const qf_status st = check_tensors(t, n, state_bits);
+  if (st != QF_OK) return st;
+  *plan = qf_adamw_plan{};
+  plan->state_bits = state_bits;
+  plan->capacity = n;
+  int at = 0;
+  for (int bf = 0; bf < 2; ++bf) {
+    uint64_t grid = 0;
+    const int first = at;
+    for (int i = 0; i < n; ++i) {
+      if (t[i].n == 0 || t[i].g_bf16 != bf) continue;
+      qf::AdamwTensor o{};
+      fill(o, t[i]);
+      const uint32_t begin = (uint32_t)grid;
+      memcpy((char*)table + sizeof(o) * at, &o, sizeof(o));
+      memcpy((char*)table + table_begin(n) + sizeof(begin) * at, &begin, sizeof(begin));
+      ++at;
+      grid += qf::adamw_chunks(t[i].n, state_bits);
+      if (grid >= (1ull << 31)) return QF_ERR_SHAPE;
+    }
+    plan->tensors[bf] = at - first;
+    plan->workgroups[bf] = (uint32_t)grid;
+  }
+  return QF_OK;
+}
+
+qf_status qf_adamw_step_table(const qf_adamw_plan* plan, const void* d_table, const qf_adamw_hyper* h, void* stream) {
+  if (!plan || !h) return QF_ERR_NULL;
+  if (plan->state_bits != 32 && plan->state_bits != 8) return QF_ERR_ARG;
+  if (plan->tensors[0] < 0 || plan->tensors[1] < 0 || plan->capacity < 0 ||
+      (int64_t)plan->tensors[0] + plan->tensors[1] > plan->capacity)
+    return QF_ERR_ARG;
+  const qf_status st = check_hyper(h);
+  if (st != QF_OK) return st;
+  if (plan->tensors[0] + plan->tensors[1] > 0 && !d_table) return QF_ERR_NULL;
+  if (misaligned(d_table, 8)) return QF_ERR_ALIGN;
+  qf::AdamwTableArgs a;
+  common(a, h);
+  int at = 0;
+  for (int bf = 0; bf < 2; ++bf) {
+    if (plan->tensors[bf] == 0) continue;
+    a.t = (const qf::AdamwTensor*)d_table + at;
+    a.begin = (const uint32_t*)((const char*)d_table + table_begin(plan->capacity)) + at;
+    a.n = plan->tensors[bf];
+    at += a.n;
+    const hipError_t e = qf::launch_adamw_table(a, plan->workgroups[bf], plan->state_bits, bf == 1, (hipStream_t)stream);
+    if (e != hipSuccess) return qf::status_of(e);
+  }
+  return QF_OK;
+}
+
+}  // extern "C"

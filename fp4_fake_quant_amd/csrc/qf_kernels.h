@@ -165,6 +165,12 @@ struct AdamwArgs : AdamwCommon {
   uint32_t begin[N];            // first workgroup of each tensor; 0xFFFFFFFF past the last
   AdamwTensor t[N];
 };
+// The same for any number of tensors, in device memory.
+struct AdamwTableArgs : AdamwCommon {
+  const AdamwTensor* t;
+  const uint32_t* begin;
+  int n;
+};
 
 // -------------------------------------------------------------- row plan ---
 constexpr int RP_ONE_LAUNCH = 16384;  // rows up to which every workgroup counts all of them itself

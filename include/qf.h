@@ -538,7 +538,13 @@ qf_status qf_lora_apply_planned(const uint16_t* X, int64_t ldx, int64_t rows_per
  * (QF_ERR_ALIGN).  QF_ERR_ARG: n < 0, state_bits not 8 or 32, g_bf16 not 0 or 1, a beta outside
  * [0, 1), negative or NaN lr / eps / weight_decay, step < 1 without d_step.  QF_ERR_SHAPE: a
  * size outside [0, 2^31).  A tensor may appear once per call; arrays must not overlap.
- * Launches: one per 48 tensors (and per gradient type), no workspace. */
+ * Launches: one per 48 tensors (and per gradient type), no workspace.
+ *
+ * Many tensors in one launch per gradient type: qf_adamw_table checks the descriptors and
+ * fills qf_adamw_table_bytes(n) of HOST memory (QF_ERR_WORKSPACE if bytes is less) and *plan;
+ * the caller copies the bytes to the device once (8-byte aligned) and qf_adamw_step_table
+ * takes that copy with the plan, for as long as the tensors stay where they are.  Same
+ * arithmetic, same bits. */
 #define QF_ADAMW_BLOCK 256
 typedef struct qf_adamw_tensor {
   float* p;
@@ -562,6 +568,15 @@ typedef struct qf_adamw_hyper {
   uint32_t seed;
 } qf_adamw_hyper;
 qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const qf_adamw_hyper* h, void* stream);
+typedef struct qf_adamw_plan {
+  int32_t state_bits, capacity;   /* as given to qf_adamw_table            */
+  int32_t tensors[2];             /* with an fp32 and with a bf16 gradient */
+  uint32_t workgroups[2];
+} qf_adamw_plan;
+size_t qf_adamw_table_bytes(int n);
+qf_status qf_adamw_table(const qf_adamw_tensor* t, int n, int state_bits, void* table, size_t bytes,
+                         qf_adamw_plan* plan);
+qf_status qf_adamw_step_table(const qf_adamw_plan* plan, const void* d_table, const qf_adamw_hyper* h, void* stream);
 
 /* ------------------------------------------------------------ dequant ---- */
 /* Packed engine layout -> BF16, the inverse direction of the pack calls ("Method":

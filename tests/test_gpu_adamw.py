@@ -92,6 +92,35 @@ def test_many_tensors_mixed_gradients(bits):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [9, 64, 65, 130, 4200])
+def test_table_and_host_descriptors_agree(bits, count):
+    """The table's one launch against the descriptors in the arguments, for counts around the
+    lookup's 64 lanes and its third level."""
+    def items():
+        rng = np.random.default_rng(count)
+        flat = {k: torch.from_numpy(rng.standard_normal(count * 512).astype(np.float32)).cuda() for k in ("p", "g")}
+        out = []
+        for i in range(count):
+            n = int(rng.integers(0, 500))
+            it = {k: flat[k][512 * i:512 * i + n] for k in ("p", "g")}
+            if i % 5 == 0:
+                it["g"] = it["g"].bfloat16()
+            it.update({k: torch.zeros_like(v) for k, v in fq.adamw_state(n, bits).items()})
+            out.append(dict(it, weight_decay=0.1 * (i % 2)))
+        return out
+    a, b = items(), items()
+    ba, bb = fq.AdamwBatch(a, bits), fq.AdamwBatch(b, bits)
+    assert ba.table is not None
+    bb.table = None                                      # through qf_adamw_step
+    for step in (1, 2):
+        fq.qf_adamw_step(ba, 1e-3, step, seed=8)
+        fq.qf_adamw_step(bb, 1e-3, step, seed=8)
+    for x, y in zip(a, b):
+        for k in names(bits):
+            assert torch.equal(x[k], y[k])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_against_float64(bits):
     n, lr, step, gs = 50000, 1e-3, 12, 0.25
     it, h = make(n, 7, bits, False, wd=0.1)

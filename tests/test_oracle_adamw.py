@@ -137,6 +137,42 @@ def test_refusals():
     assert L.qf_adamw_step(ctypes.byref(t), 1, 32, None, None) == 1
 
 
+def test_table_refusals():
+    L = _lib.lib()
+    t = (_lib.AdamwTensor * 3)()
+    for i in range(3):
+        for j, k in enumerate(("p", "g", "m", "v", "m_scale", "v_scale")):
+            setattr(t[i], k, 0x10000000 + (8 * i + j) * 0x100000)
+        t[i].n, t[i].g_bf16 = 5000 * i, i % 2
+    need = L.qf_adamw_table_bytes(3)
+    buf = (ctypes.c_uint8 * need)()
+    plan = _lib.AdamwPlan()
+    assert L.qf_adamw_table_bytes(0) == 0 and L.qf_adamw_table_bytes(-1) == 0 and need > 0
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 8, buf, need, ctypes.byref(plan)) == 0
+    # the empty tensor is left out; 5000 and 10000 elements in workgroups of 2048
+    assert list(plan.tensors) == [1, 1] and list(plan.workgroups) == [5, 3] and plan.capacity == 3
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 8, buf, need - 1, ctypes.byref(plan)) == 4
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 9, buf, need, ctypes.byref(plan)) == 7
+    assert L.qf_adamw_table(None, 3, 8, buf, need, ctypes.byref(plan)) == 1
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 8, None, need, ctypes.byref(plan)) == 1
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 8, buf, need, None) == 1
+    t[1].m = 0x10000008
+    assert L.qf_adamw_table(ctypes.byref(t), 3, 8, buf, need, ctypes.byref(plan)) == 3
+    h = _lib.AdamwHyper(1e-3, 0.9, 0.999, 1e-8, 1, None, None, None, None, 0)
+    d = ctypes.c_void_p(0x20000000)
+    empty = _lib.AdamwPlan(8, 0, (0, 0), (0, 0))
+    assert L.qf_adamw_step_table(ctypes.byref(empty), None, ctypes.byref(h), None) == 0
+    assert L.qf_adamw_step_table(None, d, ctypes.byref(h), None) == 1
+    assert L.qf_adamw_step_table(ctypes.byref(empty), d, None, None) == 1
+    assert L.qf_adamw_step_table(ctypes.byref(_lib.AdamwPlan(8, 2, (1, 1), (1, 1))), None, ctypes.byref(h), None) == 1
+    for bad in (_lib.AdamwPlan(7, 2, (1, 1), (1, 1)), _lib.AdamwPlan(8, 1, (1, 1), (1, 1)), _lib.AdamwPlan(8, 2, (-1, 1), (1, 1))):
+        assert L.qf_adamw_step_table(ctypes.byref(bad), d, ctypes.byref(h), None) == 7
+    assert L.qf_adamw_step_table(ctypes.byref(_lib.AdamwPlan(8, 2, (1, 1), (1, 1))), ctypes.c_void_p(0x20000004),
+                                 ctypes.byref(h), None) == 3
+    h.step = 0
+    assert L.qf_adamw_step_table(ctypes.byref(empty), None, ctypes.byref(h), None) == 7
+
+
 def test_binding_refusals():
     import fp4_fake_quant_amd as fq
     cpu = dict(p=torch.zeros(8), g=torch.zeros(8), m=torch.zeros(8), v=torch.zeros(8))
