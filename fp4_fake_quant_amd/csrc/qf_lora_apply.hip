@@ -23,6 +23,7 @@ namespace qf {
 
 typedef __bf16 la_bf16x8 __attribute__((ext_vector_type(8)));
 typedef float la_f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t la_u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int LA_WG = 256, LA_WAVES = LA_WG / 64;
 constexpr int LA_KSTEP = 128;                      // K per wave and step, at most
@@ -303,7 +304,8 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
 // instruction's 32 products are 16 adapter rows twice, S's high part in the first 16, its low part
 // in the others, B the same in both; above, 32 adapter rows, one instruction for each part.  The
 // next step's Y is loaded during this one's products.  RK: blocks of 32 adapter rows (0: rank 16).
-template <int RK, bool VEC_B, bool VEC_Y>
+// NT_Y: Y with the non-temporal policy.
+template <int RK, bool VEC_B, bool VEC_Y, bool NT_Y>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   static_assert(LA_NSTEP == 64, "a step of the wave is one 128-byte line of every row");
   const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -312,11 +314,11 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   LaTile t;
   if (!la_tile(a, la_tile_of(blockIdx.x, gridDim.x), i, t)) return;
   const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part), step = LA_WAVES * LA_NSTEP;
-  // Tiles start at different steps: rows are a multiple of 256 bytes apart as a rule, and all
-  // tiles at one column would share a few memory channels.
+  // An XCD's tiles start at different steps: rows are a multiple of 256 bytes apart as a rule, and all
+  // its tiles at one column would share a few cache channels (lora_prefill 141 -> 135 us).
   const int begin = blockIdx.y * a.n_part + wave * LA_NSTEP;
   const int steps = begin < end ? (end - begin + step - 1) / step : 0;
-  int left = steps, n0 = begin + (steps > 0 ? (int)(blockIdx.x % (unsigned)steps) * step : 0);
+  int left = steps, n0 = begin + (steps > 0 ? (int)((blockIdx.x >> 3) % (unsigned)steps) * step : 0);
   // accesses v = 0, 1 of block b: rows (i & 7) + 8 v of the block, half i / 8 of the line
   int row[2][2];
   uint16_t* y[2][2];
@@ -335,7 +337,10 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int v = 0; v < 2; ++v) yv[b][v] = *reinterpret_cast<const uint4*>(y[b][v] + at);
+        for (int v = 0; v < 2; ++v) {
+          const la_u32x4* p = reinterpret_cast<const la_u32x4*>(y[b][v] + at);
+          yv[b][v] = __builtin_bit_cast(uint4, NT_Y ? __builtin_nontemporal_load(p) : *p);
+        }
       return;
     }
 #pragma unroll
@@ -353,7 +358,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
   constexpr int RP = RK == 0 ? 16 : 32 * RK, NS = RK == 0 ? 1 : 2, NK = RK == 0 ? 1 : RK;
-  __shared__ uint2 sp[2][QF_ROW_TILE][RP / 4 + 2];      // high and low parts; rows 16 bytes apart in banks
+  __shared__ __align__(16) uint2 sp[2][QF_ROW_TILE][RP / 4 + 2];   // high and low parts; rows 16 bytes apart in banks
   for (int c = threadIdx.x; c < QF_ROW_TILE * RP / 4; c += LA_WG) {
     const int at = c / (RP / 4), k = c % (RP / 4) * 4;
     const float* p = a.S + (int64_t)(t.first + std::min(at, t.count - 1)) * RP + k;
@@ -429,7 +434,9 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
       for (int v = 0; v < 2; ++v) {
         if (row[b][v] < 0) continue;
         if (whole) {
-          *reinterpret_cast<uint4*>(y[b][v] + at) = yc[b][v];
+          la_u32x4* p = reinterpret_cast<la_u32x4*>(y[b][v] + at);
+          if (NT_Y) __builtin_nontemporal_store(__builtin_bit_cast(la_u32x4, yc[b][v]), p);
+          else *p = __builtin_bit_cast(la_u32x4, yc[b][v]);
         } else {
           const uint32_t w[4] = {yc[b][v].x, yc[b][v].y, yc[b][v].z, yc[b][v].w};
 #pragma unroll
@@ -441,12 +448,17 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 }
 
 namespace {
+// Y beyond the caches is accessed non-temporally.  Microseconds without / with it, rank 16 and
+// one adapter: Y of 201 MB 133 / 126 (plan and 24 adapters), of 101 MB 49 / 58.
+constexpr int64_t LA_NT_BYTES = 160ll << 20;
+
 template <int RK>
 void launch_up(const LoraApplyArgs& a, dim3 g, bool vb, bool vy, hipStream_t s) {
-  if (vb && vy) k_lora_tile_up<RK, true, true><<<g, LA_WG, 0, s>>>(a);
-  else if (vb) k_lora_tile_up<RK, true, false><<<g, LA_WG, 0, s>>>(a);
-  else if (vy) k_lora_tile_up<RK, false, true><<<g, LA_WG, 0, s>>>(a);
-  else k_lora_tile_up<RK, false, false><<<g, LA_WG, 0, s>>>(a);
+  if (vb && vy && (int64_t)a.rows * a.N * 2 > LA_NT_BYTES) k_lora_tile_up<RK, true, true, true><<<g, LA_WG, 0, s>>>(a);
+  else if (vb && vy) k_lora_tile_up<RK, true, true, false><<<g, LA_WG, 0, s>>>(a);
+  else if (vb) k_lora_tile_up<RK, true, false, false><<<g, LA_WG, 0, s>>>(a);
+  else if (vy) k_lora_tile_up<RK, false, true, false><<<g, LA_WG, 0, s>>>(a);
+  else k_lora_tile_up<RK, false, false, false><<<g, LA_WG, 0, s>>>(a);
 }
 }  // namespace
 
@@ -484,7 +496,7 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
   // N parts: whole passes of the four waves; enough workgroups to fill the chip about once, no
   // more (each pays for its tile's rows and S before its first product)
   const int most = (a.N + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP);
-  const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1536 / n_tiles));
+  const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / n_tiles));
   a.n_part = ((a.N + parts - 1) / parts + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP) * (LA_WAVES * LA_NSTEP);
   const dim3 g2((unsigned)n_tiles, (unsigned)((a.N + a.n_part - 1) / a.n_part));
   if (a.r <= 16) launch_up<0>(a, g2, vb, vy, s);

@@ -538,6 +538,9 @@ qf_status qf_lora_apply_planned(const uint16_t* X, int64_t ldx, int64_t rows_per
  * (QF_ERR_ALIGN).  QF_ERR_ARG: n < 0, state_bits not 8 or 32, g_bf16 not 0 or 1, a beta outside
  * [0, 1), negative or NaN lr / eps / weight_decay, step < 1 without d_step.  QF_ERR_SHAPE: a
  * size outside [0, 2^31).  A tensor may appear once per call; arrays must not overlap.
+ * Inputs must be finite (d_skip is for steps whose gradients are not): a NaN or infinity
+ * stays in its element with fp32 states and spoils its whole block with 8-bit ones.  eps 0
+ * divides 0 by 0 where no gradient has come yet.
  * Launches: one per 48 tensors (and per gradient type), no workspace.
  *
  * Many tensors in one launch per gradient type: qf_adamw_table checks the descriptors and

@@ -123,6 +123,24 @@ def test_apply_all_and_none(planned):
         check_apply(c, d, planned)
 
 
+def test_apply_beyond_the_caches():
+    """Y of more than 160 MiB takes another cache policy; sampled rows against the oracle."""
+    T, K, N, r, E = 7100, 64, 12000, 16, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X, Y = (torch.randn(s, generator=g, device="cuda").bfloat16() for s in ((T, K), (T, N)))
+    A, B = torch.randn((E, r, K), generator=g, device="cuda").bfloat16(), torch.randn((E, N, r), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, E, (T,), generator=g, device="cuda").int()
+    before = Y.clone()
+    fq.qf_lora_apply(X, A, B, ids, Y)
+    pick = np.r_[0:40, 3000:3040, T - 40:T]
+    f = prim.bf16_to_f32
+    at = torch.from_numpy(pick).cuda()
+    y, P, y0 = rows.apply(f(host(X[at])), f(host(A)), f(host(B)), ids[at].cpu().numpy(), f(host(before[at])))
+    assert np.all(np.abs(f(host(Y[at])).astype(np.float64) - y) <= rows.apply_bound(y, P, y0, K, r))
+    none = (ids < 0)
+    assert torch.equal(Y[none], before[none])
+
+
 def test_rows_without_adapter_are_not_read():
     """NaN in the X rows of requests without an adapter reaches nothing."""
     for T in (30, 500):
