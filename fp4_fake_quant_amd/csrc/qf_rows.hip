@@ -57,6 +57,28 @@ __device__ __forceinline__ void rp_add(uint32_t* cnt, uint32_t id, uint32_t n_id
   }
 }
 
+// The lanes with this lane's id.
+__device__ __forceinline__ uint64_t rp_peers(uint32_t id, uint32_t n_ids, int bits) {
+  const RpWave w = rp_wave(id, n_ids);
+  uint64_t peers = w.in;
+  if (!w.one)
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((id >> b) & 1u);
+      peers &= ((id >> b) & 1u) ? set : ~set;
+    }
+  return peers;
+}
+// Writes row i at its id's next position, one per peer, in lane order.
+__device__ __forceinline__ void rp_place(uint32_t* next, uint32_t id, uint32_t n_ids, uint64_t peers, uint32_t lane,
+                                         int64_t i, int32_t* order) {
+  const bool in = id < n_ids;
+  const uint32_t rank = __popcll(peers & ((1ull << lane) - 1ull));
+  uint32_t at = 0;
+  if (in && rank == 0) at = atomicAdd(&next[id], (uint32_t)__popcll(peers));
+  at = __shfl(at, in ? __ffsll((unsigned long long)peers) - 1 : 0) + rank;
+  if (in) order[at] = (int32_t)i;
+}
+
 // Counts rows [lo, hi) into cnt with the whole workgroup.
 __device__ __forceinline__ void rp_count_all(const int32_t* ids, int64_t lo, int64_t hi, uint32_t n_ids, uint32_t* cnt) {
   for (int64_t i0 = lo; i0 < hi; i0 += 16 * RP_WG) {
@@ -139,15 +161,15 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
     const uint32_t id = (threadIdx.x & (pairs - 1)) * 2, pitch = rp_pitch(n_ids);
     if (id < n_ids) {
       uint2 s = {0, 0}, p = {0, 0};
-      for (uint32_t b0 = threadIdx.x / pairs; b0 < gridDim.x; b0 += 16 * (RP_WG / pairs)) {
-        uint2 h[16];
+      for (uint32_t b0 = threadIdx.x / pairs; b0 < gridDim.x; b0 += 32 * (RP_WG / pairs)) {
+        uint2 h[32];                         // all loads in flight: the counts come from other XCDs' caches
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 32; ++j) {
           const uint32_t b = b0 + j * (RP_WG / pairs);
           h[j] = b < gridDim.x ? *reinterpret_cast<const uint2*>(a.hist + (int64_t)b * pitch + id) : uint2{0, 0};
         }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 32; ++j) {
           const bool earlier = b0 + j * (RP_WG / pairs) < blockIdx.x;
           s.x += h[j].x;
           s.y += h[j].y;
@@ -206,33 +228,19 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
   }
   __syncthreads();
 
-  // place the rows: a wave's own counters, so no other wave's work is waited for
+  // place the rows: a wave's own counters, so no other wave's work is waited for; the held rows'
+  // peers are found side by side
   int bits = 0;
   while ((1u << bits) < n_ids) ++bits;
-  for (int64_t i0 = wlo; i0 < whi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const int step = (int)((i0 - wlo) >> 6);
-    uint32_t id;
-    if (step < RP_HELD) {
-      id = held[0];
+  uint64_t peers[RP_HELD];
 #pragma unroll
-      for (int j = 1; j < RP_HELD; ++j) id = step == j ? held[j] : id;
-    } else {
-      id = i < whi ? (uint32_t)a.ids[i] : 0xFFFFFFFFu;
-    }
-    const bool in = id < n_ids;
-    const RpWave w = rp_wave(id, n_ids);
-    uint64_t peers = w.in;
-    if (!w.one)
-      for (int b = 0; b < bits; ++b) {
-        const uint64_t set = __ballot((id >> b) & 1u);
-        peers &= ((id >> b) & 1u) ? set : ~set;
-      }
-    const uint32_t rank = __popcll(peers & ((1ull << lane) - 1ull));
-    uint32_t at = 0;
-    if (in && rank == 0) at = atomicAdd(&cnt[wave][id], (uint32_t)__popcll(peers));
-    at = __shfl(at, in ? __ffsll((unsigned long long)peers) - 1 : 0) + rank;
-    if (in) a.order[at] = (int32_t)i;
+  for (int j = 0; j < RP_HELD; ++j) peers[j] = rp_peers(held[j], n_ids, bits);
+#pragma unroll
+  for (int j = 0; j < RP_HELD; ++j)
+    if (wlo + j * 64 < whi) rp_place(cnt[wave], held[j], n_ids, peers[j], lane, wlo + j * 64 + lane, a.order);
+  for (int64_t i0 = wlo + RP_HELD * 64; i0 < whi; i0 += 64) {
+    const uint32_t id = i0 + lane < whi ? (uint32_t)a.ids[i0 + lane] : 0xFFFFFFFFu;
+    rp_place(cnt[wave], id, n_ids, rp_peers(id, n_ids, bits), lane, i0 + lane, a.order);
   }
 
   // the rest, spread over the grid: offsets, the tile table, the unused end of order
