@@ -633,20 +633,22 @@ def _ids(t, name):
 
 class RowPlan:
     """Rows grouped by id (qf_row_plan): offsets [n_ids + 1], order [n] and tiles [t, 2], int32
-    on the device, for n rows with ids in [0, n_ids)."""
+    on the device, for n rows with ids in [0, n_ids).  One allocation, with the workspace that
+    building it takes."""
 
     def __init__(self, n, n_ids, device):
         self.n, self.n_ids = n, n_ids
-        t = lib().qf_row_plan_tiles(n, n_ids)
-        self.offsets = torch.empty(n_ids + 1, dtype=torch.int32, device=device)
-        self.order = torch.empty(n, dtype=torch.int32, device=device)
-        self.tiles = torch.empty((t, 2), dtype=torch.int32, device=device)
+        t, self.ws_bytes = lib().qf_row_plan_tiles(n, n_ids), lib().qf_row_plan_workspace(n, n_ids)
+        sizes = (2 * t, self.ws_bytes // 4, n_ids + 1, n)        # what is 8-byte aligned first
+        tiles, self.ws, self.offsets, self.order = torch.empty(sum(sizes), dtype=torch.int32,
+                                                               device=device).split_with_sizes(sizes)
+        self.tiles = tiles.view(t, 2)
 
 
 def qf_row_plan(ids, n_ids, plan=None, ws=None):
     """The RowPlan of ids (int32 device tensor, any shape; row i is element i in memory order):
     rows with an id outside [0, n_ids) are in no group.  plan: one of the same n and n_ids to
-    write into."""
+    write into; ws: a workspace other than the plan's own."""
     dev, n, n_ids = _same_gpu(_ids(ids, "ids"), ws), ids.numel(), int(n_ids)
     if plan is None:
         if not 1 <= n_ids <= ROW_MAX_IDS:
@@ -654,11 +656,12 @@ def qf_row_plan(ids, n_ids, plan=None, ws=None):
         plan = RowPlan(n, n_ids, ids.device)
     elif plan.n != n or plan.n_ids != n_ids or plan.offsets.get_device() != dev:
         raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} ids on {plan.offsets.device}")
-    need = lib().qf_row_plan_workspace(n, n_ids)
-    if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    if ws is None:
+        ws, ws_bytes = plan.ws, plan.ws_bytes
+    else:
+        ws_bytes = ws.numel() * ws.element_size()
     _call(dev, "qf_row_plan", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
-          plan.tiles.data_ptr(), _ptr(ws), ws.numel() * ws.element_size() if ws is not None else 0)
+          plan.tiles.data_ptr(), ws.data_ptr(), ws_bytes)
     return plan
 
 
