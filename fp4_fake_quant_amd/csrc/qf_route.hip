@@ -311,9 +311,9 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
 
   float top = -RT_INF, total = 0.0f;       // softmax: the sum of exp(x - top), when it is needed
   const bool softmax = a.scoring == QF_ROUTE_SOFTMAX;
-  float v[V];                      // what is compared
+  float v[V];                      // what is compared (-0 + 0 = +0: one key for both zeros)
 #pragma unroll
-  for (int i = 0; i < V; ++i) v[i] = x[i];
+  for (int i = 0; i < V; ++i) v[i] = x[i] + 0.0f;
   if (softmax && (SCORES || !a.renorm)) {
 #pragma unroll
     for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);

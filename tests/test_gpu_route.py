@@ -94,6 +94,20 @@ def test_ties_and_masks(scoring, groups):
             check(t, 6, scoring, renorm=renorm, bias=off, **groups)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [dict(), dict(n_group=8, topk_group=3), dict(n_group=8, topk_group=3, group_rule="top2")])
+def test_zeros_of_both_signs_tie(scoring, groups):
+    """+0 and -0 are one value (a clipped or masked router gives both): the lower index comes first."""
+    rng = np.random.default_rng(12)
+    v = np.where(rng.integers(0, 2, (200, 64)) == 1, 0.0, -0.0)
+    v[100:] = np.where(rng.integers(0, 4, (100, 64)) == 0, rng.standard_normal((100, 64)), v[100:])
+    x = torch.from_numpy(v).float().cuda()
+    bias = torch.where(torch.arange(64) % 3 == 0, 0.0, -0.0).cuda()
+    for t in (x, x.bfloat16()):
+        check(t, 8, scoring, **groups)
+        check(t, 8, scoring, bias=bias, **groups)
+
+
 def test_near_ties_are_decided_in_64_bits():
     """Biased scores that differ by less than an fp32 rounding."""
     T, E = 2000, 64
