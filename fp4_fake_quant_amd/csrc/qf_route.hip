@@ -687,7 +687,8 @@ qf_status route_args(const qf_route_desc* d, qf::RouteArgs& a) {
   if (d->scoring != QF_ROUTE_SOFTMAX && d->scoring != QF_ROUTE_SIGMOID) return QF_ERR_ARG;
   if (d->renorm != 0 && d->renorm != 1) return QF_ERR_ARG;
   if (!(d->scale >= -3e38f && d->scale <= 3e38f)) return QF_ERR_ARG;
-  if (d->experts < 1 || d->experts > QF_ROUTE_MAX_EXPERTS || d->tokens < 0 || d->tokens >= (1ll << 30)) return QF_ERR_SHAPE;
+  if (d->experts < 1 || d->experts > QF_ROUTE_MAX_EXPERTS || d->tokens < 0 || d->tokens > QF_ROUTE_MAX_TOKENS)
+    return QF_ERR_SHAPE;
   if (d->ld < d->experts) return QF_ERR_SHAPE;
   if (d->k < 1 || d->k > QF_ROUTE_MAX_K || d->k > d->experts) return QF_ERR_ARG;
   a = qf::RouteArgs{};

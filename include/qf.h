@@ -414,7 +414,7 @@ qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int acc
  * largest (scores increase with logits); else by s + bias in 64 bits, each function within
  * a few units of rounding of the exact one.  Weights: fp32, relative error at most
  * (2 D + 60) 2^-24, D the largest distance of a counted logit to the largest (softmax; sigmoid: 0).
- * Limits: experts in 1..QF_ROUTE_MAX_EXPERTS, tokens in [0, 2^30), ld >= experts
+ * Limits: experts in 1..QF_ROUTE_MAX_EXPERTS, tokens in [0, QF_ROUTE_MAX_TOKENS], ld >= experts
  * (QF_ERR_SHAPE); k in 1..QF_ROUTE_MAX_K and at most the experts of topk_group groups, n_group
  * in 1..QF_ROUTE_MAX_GROUPS dividing experts, topk_group in 1..n_group, known constants,
  * flags 0 or 1, scale finite (QF_ERR_ARG).  Arrays aligned to their element (QF_ERR_ALIGN);
@@ -426,6 +426,7 @@ qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int acc
 #define QF_ROUTE_MAX_EXPERTS 1024
 #define QF_ROUTE_MAX_K 32
 #define QF_ROUTE_MAX_GROUPS 64
+#define QF_ROUTE_MAX_TOKENS (1 << 26)      /* 32 lanes a row: a launch holds below 2^32 */
 typedef struct qf_route_desc {
   const void* logits;
   int64_t tokens, ld;

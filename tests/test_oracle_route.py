@@ -94,6 +94,7 @@ def test_refusals():
         assert call(back, tokens=0) == 0
         assert call(back, experts=0) == 2 and call(back, experts=1025, ld=1025) == 2 and call(back, ld=63) == 2
         assert call(back, tokens=-1) == 2 and call(back, tokens=1 << 30) == 2
+        assert call(back, tokens=(1 << 26) + 1) == 2         # one launch holds no more rows
         assert call(back, k=0) == 7 and call(back, k=33) == 7 and call(back, experts=4, k=5) == 7
         assert call(back, scoring=2) == 7 and call(back, renorm=2) == 7 and call(back, logits_bf16=2) == 7
         assert call(back, scale=float("nan")) == 7 and call(back, scale=INF) == 7
