@@ -376,6 +376,8 @@ hipError_t launch_adamw_table(const AdamwTableArgs& a, uint32_t grid, int bits, 
 }  // namespace qf
 
 namespace {
+constexpr uint32_t AW_MAX_GRID = (1u << 24) - 1;   // a launch holds below 2^32 lanes: 256 per workgroup
+
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) != 0; }
 
 qf_status check_hyper(const qf_adamw_hyper* h) {
@@ -446,17 +448,19 @@ qf_status qf_adamw_step(const qf_adamw_tensor* t, int n, int state_bits, const q
     int k = 0;
     uint32_t grid = 0;
     for (int i = 0; i <= n; ++i) {
-      if (i < n && t[i].n > 0 && t[i].g_bf16 == bf) {
-        fill(a.t[k], t[i]);
-        a.begin[k++] = grid;
-        grid += qf::adamw_chunks(t[i].n, state_bits);
-      }
-      if (k == qf::AW_TENSORS || (i == n && k > 0)) {
+      const bool mine = i < n && t[i].n > 0 && t[i].g_bf16 == bf;
+      const uint32_t more = mine ? qf::adamw_chunks(t[i].n, state_bits) : 0;
+      if (k > 0 && (i == n || k == qf::AW_TENSORS || grid + more > AW_MAX_GRID)) {
         for (int j = k; j < qf::AW_TENSORS; ++j) a.begin[j] = 0xFFFFFFFFu;   // no workgroup reaches these
         const hipError_t e = qf::launch_adamw(a, k, grid, state_bits, bf == 1, (hipStream_t)stream);
         if (e != hipSuccess) return qf::status_of(e);
         k = 0;
         grid = 0;
+      }
+      if (mine) {
+        fill(a.t[k], t[i]);
+        a.begin[k++] = grid;
+        grid += more;
       }
     }
   }
@@ -487,7 +491,7 @@ qf_status qf_adamw_table(const qf_adamw_tensor* t, int n, int state_bits, void* 
       memcpy((char*)table + table_begin(n) + sizeof(begin) * at, &begin, sizeof(begin));
       ++at;
       grid += qf::adamw_chunks(t[i].n, state_bits);
-      if (grid >= (1ull << 31)) return QF_ERR_SHAPE;
+      if (grid > AW_MAX_GRID) return QF_ERR_SHAPE;
     }
     plan->tensors[bf] = at - first;
     plan->workgroups[bf] = (uint32_t)grid;

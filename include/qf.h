@@ -542,10 +542,11 @@ qf_status qf_lora_apply_planned(const uint16_t* X, int64_t ldx, int64_t rows_per
  * Inputs must be finite (d_skip is for steps whose gradients are not): a NaN or infinity
  * stays in its element with fp32 states and spoils its whole block with 8-bit ones.  eps 0
  * divides 0 by 0 where no gradient has come yet.
- * Launches: one per 48 tensors (and per gradient type), no workspace.
+ * Launches: one per 48 tensors (and per gradient type; and per 2^34 elements), no workspace.
  *
  * Many tensors in one launch per gradient type: qf_adamw_table checks the descriptors and
- * fills qf_adamw_table_bytes(n) of HOST memory (QF_ERR_WORKSPACE if bytes is less) and *plan;
+ * fills qf_adamw_table_bytes(n) of HOST memory (QF_ERR_WORKSPACE if bytes is less; QF_ERR_SHAPE
+ * above 2^34 - 1024 elements of one gradient type, twice that with 8-bit states) and *plan;
  * the caller copies the bytes to the device once (8-byte aligned) and qf_adamw_step_table
  * takes that copy with the plan, for as long as the tensors stay where they are.  Same
  * arithmetic, same bits. */

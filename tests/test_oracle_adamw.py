@@ -184,3 +184,23 @@ def test_binding_refusals():
         fq.adamw_state(8, state_bits=4, device="cpu")
     s = fq.adamw_state(257, state_bits=8, device="cpu")
     assert s["m"].shape == (257,) and s["m_scale"].shape == (2,) and not s["v"].any()
+
+
+def test_table_refuses_more_than_a_launch():
+    """2^24 workgroups of 256 lanes are past the 32-bit size of a launch."""
+    L = _lib.lib()
+    most = (1 << 31) - 1                                     # elements of a tensor: 2^21 workgroups with fp32 states
+    for bits, n, chunk in ((32, 8, 1024), (8, 16, 2048)):
+        t = (_lib.AdamwTensor * n)()
+        for i in range(n):
+            for j, k in enumerate(("p", "g", "m", "v", "m_scale", "v_scale")):
+                setattr(t[i], k, 0x10000000 + j * 0x100000)
+            t[i].n = most
+        buf = (ctypes.c_uint8 * L.qf_adamw_table_bytes(n))()
+        plan = _lib.AdamwPlan()
+        assert L.qf_adamw_table(ctypes.byref(t), n, bits, buf, len(buf), ctypes.byref(plan)) == 2
+        t[n - 1].n = most - chunk
+        assert L.qf_adamw_table(ctypes.byref(t), n, bits, buf, len(buf), ctypes.byref(plan)) == 0
+        assert plan.workgroups[0] == (1 << 24) - 1
+        t[0].g_bf16, t[n - 1].n = 1, most                    # a launch per gradient type
+        assert L.qf_adamw_table(ctypes.byref(t), n, bits, buf, len(buf), ctypes.byref(plan)) == 0
