@@ -708,6 +708,8 @@ def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
 def qf_lora_apply(X, A, B, ids, Y, scale=None, rows_per_x=1, ws=None):
     """Y[i] += scale[e] * B[e] (A[e] X[i // rows_per_x]), e = ids[i] (none outside [0, E)), in
     place: X [rows / rows_per_x, K], A [E, r, K], B [E, N, r], Y [rows, N] bf16, ids int32."""
+    if isinstance(ids, RowPlan):
+        raise TypeError("ids must be a tensor; qf_lora_apply_planned takes a RowPlan")
     return _lora_apply("qf_lora_apply", X, A, B, ids, Y, scale, rows_per_x, ws)
 
 

@@ -114,3 +114,15 @@ def test_binding_refuses_host_tensors():
     z = torch.zeros(1, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         fq.qf_lora_apply(z.view(1, 1), z.view(1, 1, 1), z.view(1, 1, 1), torch.zeros(1, dtype=torch.int32), z.view(1, 1))
+
+
+def test_binding_refuses_a_plan_for_ids():
+    """A plan's arrays must not reach the entry point that takes ids."""
+    import torch
+    import fp4_fake_quant_amd as fq
+    X, A = torch.zeros((4, 64), dtype=torch.bfloat16), torch.zeros((2, 8, 64), dtype=torch.bfloat16)
+    B, Y = torch.zeros((2, 40, 8), dtype=torch.bfloat16), torch.zeros((4, 40), dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="qf_lora_apply_planned"):
+        fq.qf_lora_apply(X, A, B, fq.RowPlan(4, 2, "cpu"), Y)
+    with pytest.raises(TypeError, match="RowPlan"):
+        fq.qf_lora_apply_planned(X, A, B, torch.zeros(4, dtype=torch.int32), Y)
