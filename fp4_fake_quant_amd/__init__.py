@@ -751,7 +751,8 @@ class AdamwBatch:
     m and v float32 (state_bits 32) or uint8 with float32 scales per 256 elements (8), p16
     bfloat16.  The tensors must keep their storage while the batch is used.  More than FEW
     tensors are described by a table in device memory (built here, outside a stream capture),
-    so that a step is one launch per gradient type.
+    so that a step is one launch per gradient type; a graph that captured the step reads the
+    table on every replay, so the batch must outlive it.
     """
 
     FEW = 8

@@ -570,9 +570,10 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
   // an index given twice adds up: the choices one after another
 #pragma unroll
   for (int p = 0; p < PER; ++p)
-    for (int j = 0; j < L && p * L + j < a.k; ++j)
+    for (int j = 0; j < L && p * L + j < a.k; ++j) {
       if (lane == j && id[p] >= 0) d[id[p]] += g[p];
-  rt_wave_sync();
+      rt_wave_sync();              // the next lane's sum starts from this one's
+    }
   float o[V];
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
