@@ -191,11 +191,15 @@ hipError_t launch_row_plan(RowPlanArgs a, hipStream_t s);
 
 // ------------------------------------------------- adapters beside a product ---
 // Rows up to which a call without a plan goes row by row: the whole adapter is read again for
-// every row, so fewer of higher ranks.  Microseconds row by row / plan and tiles, for 1 and for 64
-// adapters: 4096 -> 6144 rank 16, 256 rows 8.9 / 15.6 and 13.5 / 19.2, 512 rows 16.2 / 16.8 and
-// 24.1 / 21.2; 4096 -> 4096, rank 32, 256 rows 12.8 / 16.9 and 19.8 / 21.2; rank 64, 32 rows
-// 16.4 / 19.4 and 20.9 / 19.6, 96 rows 21.8 / 19.5 and 31.7 / 26.3; rank 128, 16 rows 28.9 / 24.5.
-inline int lora_apply_few(int r) { return r <= 32 ? QF_LORA_APPLY_FEW : r <= 64 ? 32 : 8; }
+// every row, so fewer of higher ranks, and none past rank 64 (an adapter then takes one workgroup
+// longer than two more launches).  Microseconds row by row / plan and tiles, for 1 and for 64
+// adapters: 4096 -> 6144 rank 16, 256 rows 9.2 / 15.0 and 13.6 / 18.9; rank 32, 128 rows, 4096 ->
+// 4096 11.1 / 15.7 and 13.6 / 19.4, 4096 -> 14336 16.9 / 16.5 and 24.5 / 25.1 (256 rows 24.7 / 17.6
+// and 39 / 28); 4096 -> 4096, rank 64, 64 rows 19.3 / 19.8 and 21.2 / 27.2, 96 rows 22.5 / 19.4 and
+// 27.2 / 28.9; rank 128, 4 rows 28.8 / 23.5.
+inline int lora_apply_few(int r) {
+  return r > QF_LORA_APPLY_FEW_R ? 0 : r > 16 ? 16 * QF_LORA_APPLY_FEW / r : QF_LORA_APPLY_FEW;
+}
 constexpr int LORA_APPLY_MAX_SPLITS = 4;    // K parts
 
 struct LoraApplyArgs {

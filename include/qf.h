@@ -488,11 +488,12 @@ qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets
  * 2-byte (QF_ERR_ALIGN); fastest with r a multiple of 8, B and Y 16-byte aligned and ldy a
  * multiple of 8.  ws: qf_lora_apply_workspace bytes, 16-byte aligned, not shared by calls
  * that may overlap.  No array may overlap Y.  A call without a plan makes one launch and needs no
- * workspace up to QF_LORA_APPLY_FEW rows (32 above rank 32, 8 above rank 64), where it is
- * faster than a planned one, and three or four launches above; a planned call makes two. */
+ * workspace up to QF_LORA_APPLY_FEW rows (16 * QF_LORA_APPLY_FEW / r above rank 16, none above
+ * rank QF_LORA_APPLY_FEW_R), and three or four launches above; a planned call makes two. */
 #define QF_LORA_APPLY_MAX_R 128
 #define QF_LORA_APPLY_MAX_ROWS (1 << 24)
 #define QF_LORA_APPLY_FEW 256
+#define QF_LORA_APPLY_FEW_R 64
 size_t qf_lora_apply_workspace(int64_t rows, int64_t K, int r, int n_adapters, int planned);
 qf_status qf_lora_apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16_t* A, const uint16_t* B,
                         const float* d_scale, int n_adapters, const int32_t* ids, uint16_t* Y, int64_t ldy,

@@ -84,7 +84,7 @@ def check_apply(c, d, planned, scaled=True):
 
 @pytest.mark.parametrize("planned", [False, True])
 @pytest.mark.parametrize("T,K,N,r,E", [
-    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (256, 2056, 300, 16, 9), (257, 2056, 300, 16, 9), (2, 8200, 2100, 17, 3), (5, 520, 70, 128, 2), (32, 264, 66, 40, 5), (33, 264, 66, 40, 5), (9, 1000, 130, 72, 2),
+    (1, 8, 1, 1, 1), (1, 4096, 512, 16, 3), (3, 72, 17, 3, 2), (64, 2056, 300, 16, 9), (256, 2056, 300, 16, 9), (257, 2056, 300, 16, 9), (2, 8200, 2100, 17, 3), (5, 520, 70, 128, 2), (32, 264, 66, 40, 5), (33, 264, 66, 40, 5), (64, 520, 1100, 64, 5), (65, 520, 70, 64, 5), (128, 264, 130, 32, 7), (129, 264, 130, 32, 7), (1, 4096, 70, 65, 2), (9, 1000, 130, 72, 2),
     (33, 256, 64, 32, 1), (100, 520, 130, 33, 2), (97, 128, 257, 64, 5), (200, 200, 72, 128, 3), (430, 64, 40, 100, 40), (500, 640, 72, 128, 3), (444, 520, 130, 33, 2),
     (300, 96, 2000, 8, 1000), (1000, 1024, 96, 4, 7)])
 def test_apply(T, K, N, r, E, planned):

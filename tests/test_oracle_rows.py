@@ -96,7 +96,7 @@ def test_lora_apply_refusals():
         need = L.qf_lora_apply_workspace(rows, 64, 8, 4, int(planned))
         assert need > 0 and c(rows=rows, ws=None) == 4 and c(rows=rows, wsb=need - 1) == 4
         assert c(rows=rows, ws=P(0x10000008)) == 3
-    for r, few in ((8, 256), (32, 256), (33, 32), (64, 32), (65, 8), (128, 8)):
+    for r, few in ((8, 256), (16, 256), (17, 240), (32, 128), (64, 64), (65, 0), (128, 0)):
         assert L.qf_lora_apply_workspace(few, 64, r, 4, 0) == 0 and L.qf_lora_apply_workspace(few + 1, 64, r, 4, 0) > 0
     assert call(ids=None) == 1 and call(ids=P(0x10000002)) == 3
     for k in ("off", "order", "tiles"):
