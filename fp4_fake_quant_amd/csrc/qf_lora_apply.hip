@@ -10,7 +10,8 @@
 //          cores (16x16x32).  X is read once; the second step accumulates onto Y in fp32 and
 //          rounds once.  S enters the matrix cores as the sum of two bf16 (hi + lo, relative
 //          error below 2^-16), so its rounding stays far under Y's own.
-// Both are bounded by memory: X and Y pass once, 4 r flops per X element and per Y element.
+// Both are bounded by memory: X and Y pass once, 4 r flops per X element and per Y element.  16384
+// rows of 24 adapters, 4096 -> 6144, rank 16: S 32 us (4.2 TB/s), Y 83 (4.9 TB/s read and written).
 // K is split over workgroups when there are few tiles; the parts of S are summed in a fixed
 // order by the second step (no atomics: same inputs, same bits).
 #include <algorithm>
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_down(LoraApplyArgs a) {
 // the K parts, scaled and split into its two bf16 once per workgroup, in LDS.  Up to rank 16 the
 // instruction's 32 products are 16 adapter rows twice, S's high part in the first 16, its low part
 // in the others, B the same in both; above, 32 adapter rows, one instruction for each part.  The
-// next step's Y is loaded during this one's products.  RK: blocks of 32 adapter rows (0: rank 16).
+// next step's Y (and B) is loaded during this one's products.  RK: blocks of 32 adapter rows (0: rank 16).
 // NT_Y: Y with the non-temporal policy.
 template <int RK, bool VEC_B, bool VEC_Y, bool NT_Y>
 __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
   if (!la_tile(a, la_tile_of(blockIdx.x, gridDim.x), i, t)) return;
   const int end = std::min(a.N, (int)(blockIdx.y + 1) * a.n_part), step = LA_WAVES * LA_NSTEP;
   // An XCD's tiles start at different steps: rows are a multiple of 256 bytes apart as a rule, and all
-  // its tiles at one column would share a few cache channels (lora_prefill 141 -> 135 us).
+  // its tiles at one column would share a few cache channels (16384 rows, N 6144: 6 us of 141).
   const int begin = blockIdx.y * a.n_part + wave * LA_NSTEP;
   const int steps = begin < end ? (end - begin + step - 1) / step : 0;
   int left = steps, n0 = begin + (steps > 0 ? (int)((blockIdx.x >> 3) % (unsigned)steps) * step : 0);
@@ -334,7 +335,27 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 #pragma unroll
     for (int v = 0; v < 2; ++v) y[b][v] = a.Y + (int64_t)std::max(row[b][v], 0) * a.ldy + off;
   }
-  uint4 yv[2][2];
+  constexpr int RP = RK == 0 ? 16 : 32 * RK, NS = RK == 0 ? 1 : 2, NK = RK == 0 ? 1 : RK;
+  const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
+  const int col = RK == 0 ? (g & 1) * 8 : g * 8;       // the lane's 8 adapter rows of block k
+  // The step's B is loaded with its Y, one step ahead: loads return in order, so B loaded for the step
+  // at hand would wait for the next step's Y too.  Above rank 32 the registers for it cost more (4096 ->
+  // 4096, 1000 rows of rank 64 21.6 -> 24.5 us, 8192 rows of rank 128 143 -> 152).
+  constexpr bool AHEAD = RK < 2;
+  uint4 yv[2][2], bv[2][2][NK];
+  auto b_at = [&](int at, int q, int half, int k) {
+    // rows past N repeat the last one (not stored), columns past r the last ones (S is zero there)
+    const int m = std::min(at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3), a.N - 1), c = k * 32 + col;
+    return la_rank8<VEC_B>(B + (int64_t)m * a.r, VEC_B ? std::min(c, a.r - 8) : c, a.r);
+  };
+  auto load_b = [&](int at) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) bv[q][half][k] = b_at(at, q, half, k);
+  };
   auto load_y = [&](int at) {
     if (VEC_Y && at + LA_NSTEP <= a.N) {
 #pragma unroll
@@ -357,10 +378,12 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
         yv[b][v] = uint4{w[0], w[1], w[2], w[3]};
       }
   };
-  if (left > 0) load_y(n0);
+  if (left > 0) {
+    load_y(n0);
+    if (AHEAD) load_b(n0);
+  }
 
   const float scale = a.scale ? a.scale[t.e] : 1.0f;
-  constexpr int RP = RK == 0 ? 16 : 32 * RK, NS = RK == 0 ? 1 : 2, NK = RK == 0 ? 1 : RK;
   __shared__ __align__(16) uint2 sp[2][QF_ROW_TILE][RP / 4 + 2];   // high and low parts; rows 16 bytes apart in banks
   for (int c = threadIdx.x; c < QF_ROW_TILE * RP / 4; c += LA_WG) {
     const int at = c / (RP / 4), k = c % (RP / 4) * 4;
@@ -377,8 +400,6 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
                              pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1))};
   }
   __syncthreads();
-  // the lane's 8 adapter rows of block k
-  const int col = RK == 0 ? (g & 1) * 8 : g * 8;
   uint4 sv[NS][2][NK];
 #pragma unroll
   for (int h = 0; h < NS; ++h)
@@ -387,16 +408,25 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
 #pragma unroll
       for (int k = 0; k < NK; ++k)
         sv[h][b][k] = *reinterpret_cast<const uint4*>(&sp[RK == 0 ? g >> 1 : h][16 * b + i][(k * 32 + col) / 4]);
-  const uint16_t* B = a.B + (int64_t)t.e * a.N * a.r;
   while (left > 0) {
     const int at = n0;
-    uint4 yc[2][2];
+    uint4 yc[2][2], bc[2][2][NK];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          if (AHEAD) bc[q][half][k] = bv[q][half][k];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 2; ++v) yc[b][v] = yv[b][v];
     n0 = n0 + step < end ? n0 + step : begin;
-    if (--left > 0) load_y(n0);
+    if (--left > 0) {
+      load_y(n0);
+      if (AHEAD) load_b(n0);
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b) la_swap8(yc[b][0], yc[b][1], low);    // now this lane's row, steps q = 0, 1
 #pragma unroll
@@ -409,18 +439,15 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        // rows past N repeat the last one (not stored), columns past r the last ones (S is zero there)
-        const int m = std::min(at + 32 * q + 8 * (i >> 2) + 4 * half + (i & 3), a.N - 1);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          const int c = k * 32 + col;
-          const uint4 bv = la_rank8<VEC_B>(B + (int64_t)m * a.r, VEC_B ? std::min(c, a.r - 8) : c, a.r);
+          const uint4 bw = AHEAD ? bc[q][half][k] : b_at(at, q, half, k);
 #pragma unroll
           for (int h = 0; h < NS; ++h)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
               acc[b][half] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  __builtin_bit_cast(la_bf16x8, bv), __builtin_bit_cast(la_bf16x8, sv[h][b][k]), acc[b][half], 0, 0, 0);
+                  __builtin_bit_cast(la_bf16x8, bw), __builtin_bit_cast(la_bf16x8, sv[h][b][k]), acc[b][half], 0, 0, 0);
         }
       }
 #pragma unroll
@@ -496,10 +523,13 @@ hipError_t launch_lora_apply(LoraApplyArgs a, bool tiles, int64_t n_tiles, hipSt
   else k_lora_tile_down<8><<<g1, LA_WG, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // N parts: whole passes of the four waves; enough workgroups to fill the chip about once, no
-  // more (each pays for its tile's rows and S before its first product)
+  // N parts: whole passes of the four waves; enough workgroups to fill the chip once (each pays for its
+  // tile's rows and S before its first product), twice where a part keeps more than two passes.
+  // Microseconds once / twice, rank 16: 16384 rows of 24 adapters, N 6144 (24 passes) 136 / 120; 2048
+  // rows of 40, N 8192 (3 passes at once) 27 / 24; 1024 rows of 16, N 6144 (2 passes) 16.2 / 17.0.
   const int most = (a.N + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP);
-  const int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / n_tiles));
+  int parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 1024 / n_tiles));
+  if (parts * 2 < most) parts = (int)std::min<int64_t>(most, std::max<int64_t>(1, 2048 / n_tiles));
   a.n_part = ((a.N + parts - 1) / parts + LA_WAVES * LA_NSTEP - 1) / (LA_WAVES * LA_NSTEP) * (LA_WAVES * LA_NSTEP);
   const dim3 g2((unsigned)n_tiles, (unsigned)((a.N + a.n_part - 1) / a.n_part));
   if (a.r <= 16) launch_up<0>(a, g2, vb, vy, s);
