@@ -17,7 +17,7 @@
 #include <string.h>
 
 #include "qf_device.h"
-#include "qf_kernels.h"
+#include "qf_operators.h"
 
 namespace qf {
 

@@ -20,7 +20,7 @@
 #include <type_traits>
 
 #include "qf_device.h"
-#include "qf_kernels.h"
+#include "qf_operators.h"
 
 namespace qf {
 

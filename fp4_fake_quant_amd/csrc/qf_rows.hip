@@ -11,7 +11,7 @@
 // bytes from L2 is shorter than a second launch); more take a counting launch first, whose
 // per-workgroup counts every workgroup of the second launch sums.  Bounded by launch, load and
 // LDS latency, not by bytes.
-#include "qf_kernels.h"
+#include "qf_operators.h"
 
 namespace qf {
 
