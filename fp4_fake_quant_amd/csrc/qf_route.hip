@@ -15,7 +15,8 @@
 // than the key's truncation and the fp32 score's error bound.  Only then does the wave select
 // again, on the fp32 logits themselves or on 64-bit scores.  bf16 logits fit a key with their
 // index and need no second pass.  The selection is bounded by vector instructions (k + 1 rounds
-// of about 40), the rest by memory.
+// of about 40), the rest by memory: 32768 rows of 256 experts with bias, 4 of 8 groups and top 8
+// take 26 us (36 MB), 17 of them before any second pass; 7 rows of 128 experts 3.1.
 #include <algorithm>
 #include <type_traits>
 
@@ -486,7 +487,8 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
 //   plain, sigmoid: dx[i_j] = c g_j u_j (1 - u_j);  softmax: dx[e] = c s_e (g_e - sum g u)
 // Lanes and logits are laid out as in the forward pass; the chosen ones (two per lane where k is
 // over L) meet the row in LDS, so that the gradient leaves as one dense, coalesced row.  Bounded
-// by the dense write (and the read, for plain softmax).
+// by the dense write (and the read, for plain softmax): 32768 x 128 bf16 6.3 us, 4099 x 128 fp32 4.1,
+// of which an empty launch is 2.5.
 template <int V, bool VEC>
 __device__ __forceinline__ void rt_store(float* row, int e0, int E, const float (&x)[V]) {
 #pragma unroll
