@@ -557,12 +557,16 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
 #pragma unroll
       for (int p = 0; p < PER; ++p) total += u[p];
       total = rt_row_sum<L>(total);
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      // divided, not times a reciprocal: a lone choice has p = 1 and a gradient of exactly 0
+      float q[PER];
 #pragma unroll
-      for (int p = 0; p < PER; ++p) mean += g[p] * (u[p] * inv);
+      for (int p = 0; p < PER; ++p) {
+        q[p] = total > 0.0f ? u[p] / total : 0.0f;
+        mean += g[p] * q[p];
+      }
       mean = rt_row_sum<L>(mean);
 #pragma unroll
-      for (int p = 0; p < PER; ++p) g[p] = u[p] * inv * (g[p] - mean) * (softmax ? 1.0f : 1.0f - u[p]);
+      for (int p = 0; p < PER; ++p) g[p] = q[p] * (g[p] - mean) * (softmax ? 1.0f : 1.0f - u[p]);
     } else {
 #pragma unroll
       for (int p = 0; p < PER; ++p) g[p] *= u[p] * (1.0f - u[p]);

@@ -212,6 +212,18 @@ def test_backward_against_differences(scoring, renorm):
         assert np.all(np.abs(got[:, e] - diff) <= tol)
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_backward_of_a_lone_choice_is_zero(scoring, bf16):
+    """Over its own sum a single weight is constant: no rounding may leave a gradient for an optimizer to scale up."""
+    x = logits(400, 43, 8, bf16)
+    dw = torch.from_numpy(np.random.default_rng(3).standard_normal((400, 1))).float().cuda()
+    idx, _ = fq.qf_moe_route(x, 1, scoring=scoring)
+    assert int(fq.qf_moe_route_backward(x, idx, dw, scoring=scoring).count_nonzero()) == 0
+    three = torch.cat([idx, torch.full_like(idx, -1), torch.full_like(idx, -1)], 1)
+    assert int(fq.qf_moe_route_backward(x, three, dw.repeat(1, 3), scoring=scoring).count_nonzero()) == 0
+
+
 def test_masked_rows_backward():
     x = logits(6, 32, 3, False)
     x[1] = -INF
