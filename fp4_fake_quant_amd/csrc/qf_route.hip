@@ -528,7 +528,7 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
   float* d = reinterpret_cast<float*>(d4[sub]);
   const bool softmax = a.scoring == QF_ROUTE_SOFTMAX, dense = softmax && !a.renorm;
   int id[PER];
-  float g[PER], x[PER], u[PER];
+  float g[PER], x[PER], u[PER], rest[PER];       // rest: 1 - u of a sigmoid
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int j = lane + p * L;
@@ -550,8 +550,16 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
   if (!dense) {
     if (softmax) top = rt_row_max<L>(top);
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
-      u[p] = id[p] < 0 ? 0.0f : !softmax ? 1.0f / (1.0f + expf(-x[p])) : top > -RT_INF ? expf(x[p] - top) : 0.0f;
+    for (int p = 0; p < PER; ++p) {
+      rest[p] = 1.0f;
+      if (softmax) {
+        u[p] = id[p] >= 0 && top > -RT_INF ? expf(x[p] - top) : 0.0f;
+      } else {                 // for positive x, 1 - u would lose all digits that u's rounding drops
+        const float t = expf(-x[p]);
+        u[p] = id[p] < 0 ? 0.0f : 1.0f / (1.0f + t);
+        rest[p] = x[p] > 0.0f ? t * u[p] : 1.0f - u[p];
+      }
+    }
     if (a.renorm) {
       float total = 0.0f, mean = 0.0f;
 #pragma unroll
@@ -566,10 +574,10 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
       }
       mean = rt_row_sum<L>(mean);
 #pragma unroll
-      for (int p = 0; p < PER; ++p) g[p] = q[p] * (g[p] - mean) * (softmax ? 1.0f : 1.0f - u[p]);
+      for (int p = 0; p < PER; ++p) g[p] = q[p] * (g[p] - mean) * rest[p];
     } else {
 #pragma unroll
-      for (int p = 0; p < PER; ++p) g[p] *= u[p] * (1.0f - u[p]);
+      for (int p = 0; p < PER; ++p) g[p] *= u[p] * rest[p];
     }
   }
   rt_wave_sync();

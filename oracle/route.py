@@ -7,11 +7,17 @@ the gradient.
 import numpy as np
 
 
+def sigmoid(x):
+    """(s, 1 - s), both to a few units of rounding wherever s lies."""
+    t = np.exp(-np.abs(x))
+    return np.where(x >= 0, 1.0, t) / (1.0 + t), np.where(x >= 0, t, 1.0) / (1.0 + t)
+
+
 def scores(x, scoring):
     x = np.asarray(x, np.float64)
     with np.errstate(over="ignore"):
         if scoring == "sigmoid":
-            return 1.0 / (1.0 + np.exp(-x))
+            return sigmoid(x)[0]
         top = x.max(1, keepdims=True)
         e = np.exp(x - np.where(np.isfinite(top), top, 0.0))
         total = e.sum(1, keepdims=True)
@@ -69,6 +75,7 @@ def backward(x, idx, dw, scoring, renorm, scale):
     ok = (idx >= 0) & (idx < E)
     at = np.where(ok, idx, 0)
     u = np.where(ok, np.take_along_axis(s, at, 1), 0.0)
+    rest = sigmoid(x)[1]                  # 1 - s without its cancellation
     g = np.where(ok, dw * scale, 0.0)
     ds, mag = np.zeros((T, E)), np.zeros((T, E))
     rows = np.broadcast_to(np.arange(T)[:, None], idx.shape)
@@ -77,12 +84,12 @@ def backward(x, idx, dw, scoring, renorm, scale):
         total = np.where(total > 0, total, 1.0)
         p = u / total
         mean, mmean = (g * p).sum(1, keepdims=True), (np.abs(g) * p).sum(1, keepdims=True)
-        f = p if scoring == "softmax" else p * (1 - u)
+        f = p if scoring == "softmax" else p * np.take_along_axis(rest, at, 1)
         np.add.at(ds, (rows, at), np.where(ok, f * (g - mean), 0.0))
         np.add.at(mag, (rows, at), np.where(ok, f * (np.abs(g) + mmean), 0.0))
         return ds, mag
     np.add.at(ds, (rows, at), g)
     np.add.at(mag, (rows, at), np.abs(g))
     if scoring == "sigmoid":
-        return ds * s * (1 - s), mag * s * (1 - s)
+        return ds * s * rest, mag * s * rest
     return (s * (ds - (ds * s).sum(1, keepdims=True)), s * (mag + (mag * s).sum(1, keepdims=True)))

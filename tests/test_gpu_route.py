@@ -224,6 +224,24 @@ def test_backward_of_a_lone_choice_is_zero(scoring, bf16):
     assert int(fq.qf_moe_route_backward(x, three, dw.repeat(1, 3), scoring=scoring).count_nonzero()) == 0
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_sigmoid_gradient_of_confident_choices(renorm, bf16):
+    """1 - s keeps its digits where s is near 1, under the bound of every other gradient: chosen
+    logits up to 80, where s rounds to 1, beside ones near 0 and down to -80."""
+    for top in (7.0, 8.0, 10.0, 12.0, 15.0, 16.0, 17.0, 20.0, 30.0, 40.0, 80.0):
+        x = logits(40, 32, int(top), False, scale=0.25)
+        x[:, 3] += top
+        x[::2, 17] += top
+        x[::3, 30] -= top
+        x = x.bfloat16() if bf16 else x
+        idx, _ = fq.qf_moe_route(x, 6, scoring="sigmoid", renorm=renorm)
+        idx[::3, 5] = 30                                 # the lowest logit, chosen
+        dw = torch.from_numpy(np.random.default_rng(int(top)).standard_normal((40, 6))).float().cuda()
+        got = check_backward(x, idx, dw, "sigmoid", renorm, 1.5)
+        assert bool((got[:, 3] != 0).all())              # as in the formula
+
+
 def test_masked_rows_backward():
     x = logits(6, 32, 3, False)
     x[1] = -INF

@@ -75,6 +75,18 @@ def test_backward_against_differences(scoring, renorm):
     assert np.all(np.abs(got) <= mag + 1e-15)
 
 
+@pytest.mark.parametrize("x", [-40.0, -9.0, 0.5, 8.0, 20.0, 37.0, 60.0, 300.0])
+def test_sigmoid_gradient_closed_form(x):
+    """s (1 - s) = 1 / (2 + 2 cosh x), also where 1 - s is below the rounding of s; over its sum with
+    a second choice of score 1/2, the derivative by hand."""
+    both, one = np.array([[x, 0.0, -1.0]]), np.ones((1, 1))
+    d, mag = route.backward(both, np.zeros((1, 1), np.int32), one, "sigmoid", False, 1.0)
+    assert np.allclose(d[0], [1 / (2 + 2 * math.cosh(x)), 0, 0], rtol=1e-13, atol=0) and np.all(mag >= np.abs(d))
+    d, _ = route.backward(both, np.array([[0, 1]], np.int32), np.array([[1.0, 0.0]]), "sigmoid", True, 1.0)
+    s = 1 / (1 + math.exp(-x))                               # w = s / (s + 1/2): dw/ds = (1/2) / (s + 1/2)^2
+    assert np.allclose(d[0, 0], 0.5 / (s + 0.5) ** 2 / (2 + 2 * math.cosh(x)), rtol=1e-12, atol=0)
+
+
 def test_refusals():
     L = _lib.lib()
     p = 0x10000000
