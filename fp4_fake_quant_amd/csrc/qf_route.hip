@@ -292,6 +292,10 @@ __device__ __forceinline__ double rt_rcp64(double d) {
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
+// Below this logit 1 + exp(x) is 1 to 2^-28, so a sigmoid is exp(x); expf(-x) there comes near its
+// overflow.  A row whose chosen logits are all below it has the sums of a softmax over them.
+constexpr float RT_LOW = -20.0f;
+
 __device__ __forceinline__ float rt_fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 // SCORES: choose by scores plus bias, else by logits.
@@ -459,15 +463,19 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
     first = fmaxf(first, xs[p]);
   }
   float scale = a.scale;
-  if (softmax && a.renorm) {       // relative to the largest chosen logit: the row's other scores cancel
+  bool exps = softmax;
+  if (a.renorm) {       // relative to the largest chosen logit: the row's other scores cancel
     first = rt_row_max<L>(first);
+    exps = softmax || first < RT_LOW;
     if (first == -RT_INF) first = 0.0f;
     top = first;
   }
   float sum = 0.0f;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    u[p] = id[p] < 0 ? 0.0f : softmax ? expf(xs[p] - top) : 1.0f / (1.0f + expf(-xs[p]));
+    const bool low = exps || xs[p] < RT_LOW;
+    const float t = expf(exps ? xs[p] - top : low ? xs[p] : -xs[p]);
+    u[p] = id[p] < 0 ? 0.0f : low ? t : 1.0f / (1.0f + t);
     sum += u[p];
   }
   if (a.renorm) total = rt_row_sum<L>(sum);
@@ -548,17 +556,15 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
     top = fmaxf(top, x[p]);
   }
   if (!dense) {
-    if (softmax) top = rt_row_max<L>(top);
+    if (softmax || a.renorm) top = rt_row_max<L>(top);
+    const bool exps = softmax || (a.renorm && top < RT_LOW);
 #pragma unroll
     for (int p = 0; p < PER; ++p) {
-      rest[p] = 1.0f;
-      if (softmax) {
-        u[p] = id[p] >= 0 && top > -RT_INF ? expf(x[p] - top) : 0.0f;
-      } else {                 // for positive x, 1 - u would lose all digits that u's rounding drops
-        const float t = expf(-x[p]);
-        u[p] = id[p] < 0 ? 0.0f : 1.0f / (1.0f + t);
-        rest[p] = x[p] > 0.0f ? t * u[p] : 1.0f - u[p];
-      }
+      const bool low = exps || x[p] < RT_LOW;
+      const float t = expf(exps ? x[p] - top : low ? x[p] : -x[p]);
+      u[p] = id[p] < 0 || x[p] == -RT_INF ? 0.0f : low ? t : 1.0f / (1.0f + t);
+      // for positive x, 1 - u would lose all digits that u's rounding drops
+      rest[p] = low ? 1.0f : x[p] > 0.0f ? t * u[p] : 1.0f - u[p];
     }
     if (a.renorm) {
       float total = 0.0f, mean = 0.0f;

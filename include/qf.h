@@ -413,7 +413,8 @@ qf_status qf_lora_experts_adapter_grads(const qf_lora_experts* e, int n, int acc
  * Choice: exact with respect to the logits when bias is NULL and groups rank by their
  * largest (scores increase with logits); else by s + bias in 64 bits, each function within
  * a few units of rounding of the exact one.  Weights: fp32, relative error at most
- * (2 D + 60) 2^-24, D the largest distance of a counted logit to the largest (softmax; sigmoid: 0).
+ * (2 D + 60) 2^-24, D the largest distance of a counted logit to the largest (softmax, and sigmoid
+ * with renorm where all chosen logits are below -20; else 0), plus 2^-119 |scale| (the range of fp32).
  * Limits: experts in 1..QF_ROUTE_MAX_EXPERTS, tokens in [0, QF_ROUTE_MAX_TOKENS], ld >= experts
  * (QF_ERR_SHAPE); k in 1..QF_ROUTE_MAX_K and at most the experts of topk_group groups, n_group
  * in 1..QF_ROUTE_MAX_GROUPS dividing experts, topk_group in 1..n_group, known constants,

@@ -24,6 +24,19 @@ def scores(x, scoring):
         return e / np.where(total > 0, total, 1.0)
 
 
+def shares(c, scoring):
+    """Scores of the chosen logits c (minus infinity: none) over their sum, taken relative to the
+    largest, so that small scores do not vanish: softmax exp(c), sigmoid exp(min(c, 0)) / (1 +
+    exp(-|c|)), each divided by the largest exp."""
+    low = c if scoring == "softmax" else np.minimum(c, 0.0)
+    top = low.max(1, keepdims=True)
+    u = np.exp(low - np.where(np.isfinite(top), top, 0.0))
+    if scoring == "sigmoid":
+        u = u / (1.0 + np.exp(-np.abs(c)))
+    total = u.sum(1, keepdims=True)
+    return u / np.where(total > 0, total, 1.0)
+
+
 def route(x, k, scoring, bias=None, n_group=1, topk_group=1, group_rule="max", renorm=True, scale=1.0):
     """(indices, weights): best first, ties to the lower index, -1 and 0 where no expert is left."""
     x = np.asarray(x, np.float64)
@@ -47,12 +60,7 @@ def route(x, k, scoring, bias=None, n_group=1, topk_group=1, group_rule="max", r
     left = np.take_along_axis(key, idx, 1) > -np.inf
     u = np.where(left, np.take_along_axis(s, idx, 1), 0.0)
     if renorm:
-        if scoring == "softmax":       # from the chosen logits alone, so that small scores do not vanish
-            c = np.where(left, np.take_along_axis(x, idx, 1), -np.inf)
-            top = c.max(1, keepdims=True)
-            u = np.where(left, np.exp(c - np.where(np.isfinite(top), top, 0.0)), 0.0)
-        total = u.sum(1, keepdims=True)
-        u = u / np.where(total > 0, total, 1.0)
+        u = shares(np.where(left, np.take_along_axis(x, idx, 1), -np.inf), scoring)
     return np.where(left, idx, -1).astype(np.int32), u * scale
 
 
@@ -80,9 +88,7 @@ def backward(x, idx, dw, scoring, renorm, scale):
     ds, mag = np.zeros((T, E)), np.zeros((T, E))
     rows = np.broadcast_to(np.arange(T)[:, None], idx.shape)
     if renorm:
-        total = u.sum(1, keepdims=True)
-        total = np.where(total > 0, total, 1.0)
-        p = u / total
+        p = shares(np.where(ok, np.take_along_axis(x, at, 1), -np.inf), scoring)
         mean, mmean = (g * p).sum(1, keepdims=True), (np.abs(g) * p).sum(1, keepdims=True)
         f = p if scoring == "softmax" else p * np.take_along_axis(rest, at, 1)
         np.add.at(ds, (rows, at), np.where(ok, f * (g - mean), 0.0))

@@ -242,6 +242,36 @@ def test_sigmoid_gradient_of_confident_choices(renorm, bf16):
         assert bool((got[:, 3] != 0).all())              # as in the formula
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("at", [-15.0, -19.0, -21.0, -50.0, -80.0, -89.0, -95.0, -100.0, -200.0, -700.0, -5000.0, -1e30])
+def test_low_sigmoid_scores(at, renorm):
+    """Scores below fp32's range: their weights over their sum are those of the formula, and so is
+    the gradient; the plain ones vanish as the formula's do."""
+    T, E, k = 60, 48, 5
+    x = logits(T, E, 11, False) + at
+    x[::4, 7] = at / 2                                   # rows with one far larger choice
+    x[1::8, 3:] = at - 70                                # and with far smaller ones
+    x[5::8, 3:] = at - 90
+    x[2::4, 9:] = -INF
+    dw = torch.from_numpy(np.random.default_rng(12).standard_normal((T, k))).float().cuda()
+    for t in (x, x.bfloat16()):
+        xi = np64(t)
+        idx, w = fq.qf_moe_route(t, k, scoring="sigmoid", renorm=renorm, scale=2.0)
+        ri, rw = route.route(xi, k, "sigmoid", renorm=renorm, scale=2.0)
+        assert np.array_equal(idx.cpu().numpy(), ri)
+        best = xi.max(1, keepdims=True)
+        D = np.where(renorm & (best < -20), best - np.where(np.isfinite(xi), xi, np.inf).min(1, keepdims=True), 0.0)
+        assert np.all(np.abs(np64(w) - rw) <= (2 * D + 60) * U * np.abs(rw) + 2.0 ** -119 * 2.0)
+        g = np64(fq.qf_moe_route_backward(t, idx, dw, scoring="sigmoid", renorm=renorm, scale=2.0))
+        ref, mag = route.backward(xi, ri, np64(dw), "sigmoid", renorm, 2.0)
+        tol = (4 * (2 * D + 60) + 64) * U * mag + 2.0 ** -116 * 2.0 * np64(dw.abs().sum(1, keepdim=True))
+        if t.dtype == torch.bfloat16:
+            tol = 2.0 ** -8 * (np.abs(ref) + tol) + tol
+        assert np.all(np.abs(g - ref) <= tol)
+        if renorm:
+            assert np.allclose(np64(w).sum(1), 2.0, rtol=1e-6, atol=0)
+
+
 def test_masked_rows_backward():
     x = logits(6, 32, 3, False)
     x[1] = -INF

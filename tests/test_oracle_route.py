@@ -87,6 +87,18 @@ def test_sigmoid_gradient_closed_form(x):
     assert np.allclose(d[0, 0], 0.5 / (s + 0.5) ** 2 / (2 + 2 * math.cosh(x)), rtol=1e-12, atol=0)
 
 
+@pytest.mark.parametrize("at", [-30.0, -89.0, -800.0, -1e6])
+def test_low_sigmoid_scores(at):
+    """Far below zero a sigmoid is exp(x), so its shares are a softmax's, however small the scores."""
+    x = np.array([[0.0, -1.0, 2.0, -3.0]]) + at
+    idx, w = route.route(x, 3, "sigmoid")
+    e = np.exp(np.array([2.0, 0.0, -1.0]))
+    assert idx.tolist() == [[2, 0, 1]] and np.allclose(w[0], e / e.sum(), rtol=1e-12, atol=0)
+    p, g = e / e.sum(), np.array([0.5, -1.0, 2.0])
+    d, _ = route.backward(x, idx, g[None], "sigmoid", True, 1.0)
+    assert np.allclose(d[0, [2, 0, 1]], p * (g - (g * p).sum()), rtol=1e-11, atol=0) and d[0, 3] == 0
+
+
 def test_refusals():
     L = _lib.lib()
     p = 0x10000000
