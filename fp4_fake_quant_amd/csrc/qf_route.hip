@@ -265,7 +265,7 @@ constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
 // (the term after the last is below 2^-57); about two units of rounding.  The second pass is rare
 // and its code cold, so it is short.
 __device__ __forceinline__ double rt_exp64(double x) {
-  x = fmax(x, -745.0);                               // below, exp is 0 in 64 bits
+  x = fmax(x, -746.0);                               // from there on exp is 0 in 64 bits
   const double n = __builtin_rint(x * 1.4426950408889634);
   double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
   r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);   // ln 2 in two parts
@@ -285,7 +285,7 @@ __device__ __forceinline__ double rt_exp64(double x) {
   p = __builtin_fma(p, r, 1.0);
   return __builtin_ldexp(p, (int)n);
 }
-// 1 / d for d in [1, inf]: the hardware's approximation and two Newton steps.
+// 1 / d for d in [1, 2]: the hardware's approximation and two Newton steps.
 __device__ __forceinline__ double rt_rcp64(double d) {
   double y = __builtin_amdgcn_rcp(d);
   y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
@@ -428,16 +428,15 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
         double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          // a masked logit's score does not matter below; exp(-x) stays finite (sigmoids from 2^-1021)
-          const double d = softmax ? (double)x[i] - (double)top : fmin(-(double)x[i], 708.0);
-          key2[i] = rt_exp64(d);
+          // a masked logit's score does not matter below; sigmoids from exp(-|x|), which cannot overflow
+          key2[i] = rt_exp64(softmax ? (double)x[i] - (double)top : -fabs((double)x[i]));
           sum += key2[i];
         }
         if (softmax) sum = rt_row_sum<L>(sum);
         const double inv = softmax ? 1.0 / sum : 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          key2[i] = softmax ? key2[i] * inv : rt_rcp64(1.0 + key2[i]);
+          key2[i] = softmax ? key2[i] * inv : rt_rcp64(1.0 + key2[i]) * (x[i] < 0.0f ? key2[i] : 1.0);
           key2[i] = x[i] > -RT_INF ? key2[i] + (double)bias[i] : -(double)RT_INF;
         }
         if constexpr (GROUPS != 0) rt_groups<L, V, GROUPS, K2>(a, sub, lane, key2, gs2, 0.0);

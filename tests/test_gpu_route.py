@@ -134,6 +134,15 @@ def test_extreme_logits():
     check(x.clamp(-80, 30), 4, "sigmoid")
 
 
+def test_low_sigmoid_scores_of_groups():
+    """Groups ranked by sums of scores down to the end of 64 bits: distinct logits, distinct sums."""
+    rng = np.random.default_rng(15)
+    v = np.stack([rng.permutation(np.arange(-738, -738 + 24)) for _ in range(100)]).astype(np.float64)
+    x = torch.from_numpy(v).float().cuda()
+    for rule in ("top2", "max"):
+        check(x, 5, "sigmoid", n_group=6, topk_group=2, group_rule=rule)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_poisoned_rows(scoring):
     """A NaN or plus infinity shows in its own row alone."""
