@@ -349,7 +349,7 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
       for (int i = 0; i < V; ++i) bias[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = x[i] == -RT_INF ? -RT_INF : v[i] + bias[i];
+    for (int i = 0; i < V; ++i) v[i] = (x[i] == -RT_INF ? -RT_INF : v[i]) + bias[i];   // NaN for a bias of +inf or NaN
   }
   // a NaN or plus infinity poisons its row: as integers, positive ones are the largest signed
   // numbers, and negative NaN lies above minus infinity among the unsigned

@@ -160,6 +160,27 @@ def test_poisoned_rows(scoring):
                 assert torch.equal(i[t], base_i[t]) and torch.equal(w[t], base_w[t])
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_poisoned_bias(scoring, bad):
+    """A NaN or plus infinity in the bias shows in every row, also in those that mask its expert."""
+    for E, groups in ((48, dict()), (48, dict(n_group=4, topk_group=2)), (45, dict(n_group=3, topk_group=2, group_rule="top2")),
+                      (300, dict(n_group=4, topk_group=2))):
+        x = logits(8, E, 2, False)
+        bias = torch.zeros(E, device="cuda")
+        x[::2, E - 2] = -INF
+        x[5] = -INF
+        clean_i, _ = fq.qf_moe_route(x, 5, scoring=scoring, bias=bias, **groups)
+        assert bool((clean_i[5] == -1).all()) and bool((clean_i[:5] >= 0).all())
+        bias[E - 2] = bad
+        for t in (x, x.bfloat16()):
+            i, w = fq.qf_moe_route(t, 5, scoring=scoring, bias=bias, **groups)
+            assert bool((i == -1).all()) and bool(w.isnan().all())
+        bias[E - 2] = -INF
+        i, w = fq.qf_moe_route(x, 5, scoring=scoring, bias=bias, **groups)
+        assert not bool((i == E - 2).any()) and bool(w.isfinite().all()) and bool((i[:5] >= 0).all())
+
+
 def check_backward(x, idx, dw, scoring, renorm, scale, **kw):
     got = fq.qf_moe_route_backward(x, idx, dw, scoring=scoring, renorm=renorm, scale=scale, **kw)
     xi = np64(x)
