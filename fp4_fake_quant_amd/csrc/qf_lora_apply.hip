@@ -77,6 +77,15 @@ __device__ __forceinline__ void la_swap8(uint4& v0, uint4& v1, bool low) {
   v1 = uint4{b[0], b[1], b[2], b[3]};
 }
 
+// Two values of S as bf16 pairs {high parts, low parts}.  The high part stays finite, or its difference
+// to S would be infinity less infinity: S past the largest bf16 is that and the rest, an infinite or NaN
+// S is in the low part.
+__device__ __forceinline__ uint2 la_split2(float a, float b) {
+  constexpr float MOST = 0x1.fep127f;
+  const uint32_t hi = pack_bf16x2(__builtin_amdgcn_fmed3f(a, -MOST, MOST), __builtin_amdgcn_fmed3f(b, -MOST, MOST));
+  return uint2{hi, pack_bf16x2(a - bf16_lo(hi), b - bf16_hi(hi))};
+}
+
 // ---------------------------------------------------------------- rows form ----
 // A workgroup per row and part of N, both steps in one launch: every part computes the row's S
 // again, which is shorter than a second launch.  Rows are dealt to the 8 XCDs in turn, all parts of
@@ -394,10 +403,9 @@ __global__ __launch_bounds__(LA_WG) void k_lora_tile_up(LoraApplyArgs a) {
       v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
     v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
-    const uint32_t h0 = pack_bf16x2(v.x, v.y), h1 = pack_bf16x2(v.z, v.w);
-    sp[0][at][k / 4] = uint2{h0, h1};
-    sp[1][at][k / 4] = uint2{pack_bf16x2(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
-                             pack_bf16x2(v.z - bf16_lo(h1), v.w - bf16_hi(h1))};
+    const uint2 p0 = la_split2(v.x, v.y), p1 = la_split2(v.z, v.w);
+    sp[0][at][k / 4] = uint2{p0.x, p1.x};
+    sp[1][at][k / 4] = uint2{p0.y, p1.y};
   }
   __syncthreads();
   uint4 sv[NS][2][NK];

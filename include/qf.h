@@ -482,7 +482,9 @@ qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets
  * S = A_e x is accumulated in fp32; Y's row is added in fp32 and rounded once:
  *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) ((gamma_{K+12} + gamma_{2r+34} + 2^-17) P + gamma_{2r+34} |y0|),
  *   P = |scale| sum_k |B| sum |A| |x|, gamma_n = n 2^-24 / (1 - n 2^-24).
- * The order of the sums is fixed for given sizes: same inputs, same bits.
+ * The order of the sums is fixed for given sizes: same inputs, same bits.  Infinities and NaN stay in
+ * the rows and adapters that hold them.  One in X, A or scale (or an overflow of S) gives what the
+ * formula gives; one in B[e][n] may be a NaN instead of an infinity in column n of e's rows.
  * Limits: r in 1..QF_LORA_APPLY_MAX_R, n_adapters in 1..QF_ROW_MAX_IDS, rows_per_x >= 1
  * (QF_ERR_ARG); K a positive multiple of 8 and N >= 1, both below 2^22, rows in [0, 2^24),
  * ldx >= K, ldy >= N (QF_ERR_SHAPE).  X and A 16-byte aligned, ldx a multiple of 8, B and Y

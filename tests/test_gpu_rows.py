@@ -10,6 +10,7 @@ from oracle import rows
 from tests.gpu_util import dev, host
 
 pytestmark = pytest.mark.gpu
+INF = float("inf")
 
 
 def ids_of(n, n_ids, seed, none=0.1, runs=False):
@@ -149,6 +150,66 @@ def test_rows_without_adapter_are_not_read():
         d["X"][none] = float("nan")
         check_apply(c, d, False)
         check_apply(c, d, True)
+
+
+@pytest.mark.parametrize("r", [1, 8, 16, 24, 64, 100])
+@pytest.mark.parametrize("T", [24, 500])
+def test_infinite_and_huge_inner_products(T, r):
+    """A x that overflows, or holds an infinity, gives the infinities of the formula in its own row
+    alone; A x between the largest bf16 and the largest fp32 stays finite."""
+    K, N, E = 64, 72, 2
+    X, A, B = torch.zeros(T, K), torch.zeros(E, r, K), torch.zeros(E, N, r)
+    big = torch.finfo(torch.bfloat16).max
+    X[:, 0] = 1.0
+    X[3, 1], X[5, 1], X[9, 1] = INF, big, big
+    X[9, 2] = 1.5 * 2.0 ** 119                           # above half a bf16 step past the largest
+    A[:, :, 0], A[:, :, 1], A[:, :, 2] = 0.5, 1.0, 1.0
+    A[1, :, 1] = 4.0                                     # overflows
+    B[:] = torch.where(torch.arange(N) % 3 == 0, -1.0, 1.0)[None, :, None] * 2.0 ** -100
+    Y = torch.arange(N).float().repeat(T, 1)
+    ids = torch.arange(T) % 2
+    ids[9], ids[5] = 0, 1
+    s = (X * A[ids, 0]).sum(1, keepdim=True)             # the same for all adapter rows
+    assert s[3, 0] == INF and s[5, 0] == INF and big + 2.0 ** 119 < s[9, 0] < INF
+    want = Y + s * B[0, :, 0] * r
+    X, A, B, Y, ids = (t.cuda() for t in (X.bfloat16(), A.bfloat16(), B.bfloat16(), Y.bfloat16(), ids.int()))
+    plan = fq.qf_row_plan(ids, E)
+    for planned in (False, True):
+        y = Y.clone()
+        if planned:
+            fq.qf_lora_apply_planned(X, A, B, plan, y)
+        else:
+            fq.qf_lora_apply(X, A, B, ids, y)
+        y = y.float().cpu()
+        assert torch.equal(y.isinf(), want.isinf()) and not bool(y.isnan().any())
+        assert torch.equal(y[want.isinf()], want[want.isinf()])
+        fin = want.isfinite()                            # one bf16 rounding, the parts of A x 2^-17, fp32 sums
+        assert bool(((y - want).abs()[fin] <= (2.0 ** -8 + 2.0 ** -14) * want.abs()[fin]).all())
+
+
+@pytest.mark.parametrize("r", [4, 8, 16, 24, 72])
+@pytest.mark.parametrize("T", [24, 500])
+def test_bad_adapter_values_stay_in_their_outputs(T, r):
+    """An infinity or NaN in B[e][n] reaches column n of e's rows alone, one in another adapter nothing."""
+    c, d = case(T, 64, 70, r, 5, 31, none=0.1)
+    d["ids"][d["ids"] == 4] = 0                          # adapter 4 has no rows
+    own = (d["ids"] == 2).nonzero()[:, 0]
+    for planned in (False, True):
+        out = []
+        for bad in (None, INF, float("nan")):
+            A, B, Y = d["A"].clone(), d["B"].clone(), d["Y"].clone()
+            if bad is not None:
+                B[2, 69, r - 1], B[2, 5, 0] = bad, bad
+                A[4], B[4] = bad, bad
+            if planned:
+                fq.qf_lora_apply_planned(d["X"], A, B, fq.qf_row_plan(d["ids"], 5), Y)
+            else:
+                fq.qf_lora_apply(d["X"], A, B, d["ids"], Y)
+            out.append(Y)
+        for Y in out[1:]:
+            assert not bool(Y[own][:, [5, 69]].isfinite().any())
+            Y[own[:, None], torch.tensor([[5, 69]], device="cuda")] = out[0][own[:, None], torch.tensor([[5, 69]], device="cuda")]
+            assert torch.equal(Y, out[0])
 
 
 def test_forms_agree_with_a_prefix():
