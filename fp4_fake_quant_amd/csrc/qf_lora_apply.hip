@@ -203,7 +203,8 @@ __device__ __forceinline__ bool la_tile(const LoraApplyArgs& a, int t, int i, La
   o.first = w.y;
 #pragma unroll
   for (int b = 0; b < 2; ++b) o.row[b] = a.order[std::min(w.y + 16 * b + i, a.rows - 1)];
-  o.count = std::min(std::min(a.offsets[w.x + 1], a.rows) - w.y, (int)QF_ROW_TILE);
+  const int end = std::min(a.offsets[w.x + 1], a.rows);
+  o.count = end > w.y ? std::min(end - w.y, (int)QF_ROW_TILE) : 0;      // compared first: end may be any number
 #pragma unroll
   for (int b = 0; b < 2; ++b)
     if (16 * b + i >= o.count || (uint32_t)o.row[b] >= (uint32_t)a.rows) o.row[b] = -1;

@@ -226,6 +226,29 @@ def test_forms_agree_with_a_prefix():
                      torch.empty(0, dtype=torch.int32, device="cuda"), e)
 
 
+@pytest.mark.parametrize("r", [8, 40, 128])
+def test_foreign_plans_stay_inside_the_call(r):
+    """Plan arrays that hold other numbers (another batch's, or never filled) reach no memory outside
+    the workspace and Y's rows, whatever they are."""
+    T, K, N, E = 77, 64, 70, 5
+    _, d = case(T, K, N, r, E, 41)
+    need = fq.qf_lora_apply_workspace(T, K, r, E, True)
+    rng = np.random.default_rng(r)
+    lo, hi = -2 ** 31, 2 ** 31 - 1
+    for values in ([lo], [lo, 0, 1, 2, 3, 4, 76], [hi, hi - 31, 0, 4], [-1, 0, 1, 40, 76, 77, 78], [lo, lo + 1, lo + 77, 1, 2, 76, hi]):
+        plan = fq.RowPlan(T, E, "cuda")
+        for t in (plan.offsets, plan.order, plan.tiles):
+            t.copy_(torch.from_numpy(rng.choice(np.array(values, np.int32), t.shape)))
+        plan.tiles[:len(plan.tiles) // 2, 0] = torch.from_numpy(rng.integers(0, E, len(plan.tiles) // 2).astype(np.int32))
+        plan.tiles[:len(plan.tiles) // 2, 1] = torch.from_numpy(rng.integers(0, T, len(plan.tiles) // 2).astype(np.int32))
+        ws = torch.full((need + 65536,), 77, dtype=torch.uint8, device="cuda")
+        Y = torch.full((T + 64, N + 2), 7.0, dtype=torch.bfloat16, device="cuda")
+        fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], plan, Y[32:32 + T, :N], ws=ws[32768:32768 + need])
+        torch.cuda.synchronize()
+        assert bool((ws[:32768] == 77).all()) and bool((ws[32768 + need:] == 77).all())
+        assert bool((Y[:32] == 7.0).all()) and bool((Y[32 + T:] == 7.0).all()) and bool((Y[:, N:] == 7.0).all())
+
+
 @pytest.mark.parametrize("T", [24, 5000])
 def test_graph_replays(T):
     """Plan and adapters captured once; ids, X and Y change between replays."""
