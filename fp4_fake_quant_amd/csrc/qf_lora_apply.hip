@@ -591,9 +591,7 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
                 const float* scale, int n_adapters, const int32_t* ids, const int32_t* offsets, const int32_t* order,
                 const int32_t* tiles, int n_ids, bool planned, uint16_t* Y, int64_t ldy, int64_t rows, int64_t N,
                 int64_t K, int r, void* ws, size_t ws_bytes, void* stream) {
-  if (r < 1 || r > QF_LORA_APPLY_MAX_R || n_adapters < 1 || n_adapters > QF_ROW_MAX_IDS || rows_per_x < 1 ||
-      rows_per_x > QF_LORA_APPLY_MAX_ROWS)
-    return QF_ERR_ARG;
+  if (r < 1 || r > QF_LORA_APPLY_MAX_R || n_adapters < 1 || n_adapters > QF_ROW_MAX_IDS || rows_per_x < 1) return QF_ERR_ARG;
   if (planned && (n_ids < 1 || n_ids > n_adapters)) return QF_ERR_ARG;
   if (!sizes_ok(rows, K, N, r, n_adapters) || ldx < K || ldy < N) return QF_ERR_SHAPE;
   if (rows == 0) return QF_OK;
@@ -632,7 +630,7 @@ qf_status apply(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const uint16
   a.tiles = tiles;
   a.S = (float*)base;
   a.rows = (int)rows;
-  a.rows_per_x = (int)rows_per_x;
+  a.rows_per_x = (int)std::min(rows_per_x, rows);      // one row of X for all of Y from there on
   a.K = (int)K;
   a.N = (int)N;
   a.r = r;

@@ -113,6 +113,20 @@ def test_apply_token_expert_pairs(T, planned):
     check_apply(c, d, planned)
 
 
+@pytest.mark.parametrize("T", [24, 500])
+def test_one_row_of_x_for_all(T):
+    c, d = case(T, 96, 72, 16, 3, 33, per=T)
+    for planned in (False, True):
+        got = check_apply(c, d, planned)
+        for per in (T + 1, (1 << 24) + 1, 1 << 40):
+            y = dev(c["Y"])
+            if planned:
+                fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], fq.qf_row_plan(d["ids"], 3), y, scale=d["scale"], rows_per_x=per)
+            else:
+                fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], y, scale=d["scale"], rows_per_x=per)
+            assert np.array_equal(host(y), got)
+
+
 @pytest.mark.parametrize("planned", [False, True])
 def test_apply_all_and_none(planned):
     for T in (20, 500):

@@ -105,6 +105,15 @@ def test_lora_apply_refusals():
     assert L.qf_lora_apply_workspace(10, 60, 8, 4, 0) == 0 and L.qf_lora_apply_workspace(10, 64, 200, 4, 0) == 0
 
 
+def test_rows_per_x_has_no_upper_limit():
+    """X of one row serves any number of rows of Y."""
+    L = _lib.lib()
+    X, A, B, ids, Y, off, order, tiles = (P(0x10000000 + k * 0x100000) for k in range(8))
+    for per in (1, 1 << 24, (1 << 24) + 1, 1 << 40, (1 << 63) - 1):
+        assert L.qf_lora_apply(X, 64, per, A, B, None, 4, ids, Y, 40, 0, 40, 64, 8, None, 0, None) == 0
+        assert L.qf_lora_apply_planned(X, 64, per, A, B, None, 4, off, order, tiles, 4, Y, 40, 0, 40, 64, 8, None, 0, None) == 0
+
+
 def test_binding_refuses_host_tensors():
     import fp4_fake_quant_amd as fq
     with pytest.raises(TypeError):
