@@ -17,6 +17,8 @@
 // index and need no second pass.  The selection is bounded by vector instructions (k + 1 rounds
 // of about 40), the rest by memory: 32768 rows of 256 experts with bias, 4 of 8 groups and top 8
 // take 26 us (36 MB), 17 of them before any second pass; 7 rows of 128 experts 3.1.
+#include <float.h>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -706,7 +708,7 @@ qf_status route_args(const qf_route_desc* d, qf::RouteArgs& a) {
   if (d->logits_bf16 != 0 && d->logits_bf16 != 1) return QF_ERR_ARG;
   if (d->scoring != QF_ROUTE_SOFTMAX && d->scoring != QF_ROUTE_SIGMOID) return QF_ERR_ARG;
   if (d->renorm != 0 && d->renorm != 1) return QF_ERR_ARG;
-  if (!(d->scale >= -3e38f && d->scale <= 3e38f)) return QF_ERR_ARG;
+  if (!(d->scale >= -FLT_MAX && d->scale <= FLT_MAX)) return QF_ERR_ARG;      // written so that a NaN fails
   if (d->experts < 1 || d->experts > QF_ROUTE_MAX_EXPERTS || d->tokens < 0 || d->tokens > QF_ROUTE_MAX_TOKENS)
     return QF_ERR_SHAPE;
   if (d->ld < d->experts) return QF_ERR_SHAPE;

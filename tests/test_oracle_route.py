@@ -132,6 +132,15 @@ def test_refusals():
     assert L.qf_moe_route(None, None, None, None) == 1
 
 
+def test_every_finite_scale_is_taken():
+    L = _lib.lib()
+    p, most = 0x10000000, float(np.finfo(np.float32).max)
+    for scale, want in ((most, 0), (-most, 0), (3.3e38, 0), (0.0, 0), (INF, 7), (-INF, 7), (float("nan"), 7)):
+        d = _lib.RouteDesc(p, 0, 8, None, scale, 0, 8, 2, 0, 1, 1, 1, 0)
+        assert L.qf_moe_route(ctypes.byref(d), p, p, None) == want
+        assert L.qf_moe_route_backward(ctypes.byref(d), p, p, p, 8, None) == want
+
+
 def test_binding_refuses_host_tensors():
     import fp4_fake_quant_amd as fq
     with pytest.raises(TypeError):
