@@ -749,7 +749,8 @@ class AdamwBatch:
     items: list of dict(p, g, m, v, m_scale=None, v_scale=None, p16=None, weight_decay=0.0) of
     contiguous device tensors with the same element count: p float32, g float32 or bfloat16,
     m and v float32 (state_bits 32) or uint8 with float32 scales per 256 elements (8), p16
-    bfloat16.  The tensors must keep their storage while the batch is used.  More than FEW
+    bfloat16.  The batch holds the tensors; they must keep their storage while it is used (a
+    gradient put elsewhere needs a new batch).  More than FEW
     tensors are described by a table in device memory (built here, outside a stream capture),
     so that a step is one launch per gradient type; a graph that captured the step reads the
     table on every replay, so the batch must outlive it.
@@ -760,6 +761,9 @@ class AdamwBatch:
     def __init__(self, items, state_bits=32):
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
+        # own copies of the dicts: the step writes through the tensors' addresses, so they stay alive
+        # here whatever becomes of the caller's
+        items = [dict(it) for it in items]
         self.items, self.state_bits, self.n = items, state_bits, len(items)
         self.arr = (AdamwTensor * max(len(items), 1))()
         self.device = _same_gpu(*[t for it in items for t in it.values() if isinstance(t, torch.Tensor)])

@@ -1,6 +1,9 @@
 """qf_adamw_step on the GPU: bit for bit the stated fp32 sequence, and within counted roundings
 of the float64 formula."""
 
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -204,6 +207,25 @@ def test_grouping_does_not_change_results():
     for (x, _), (y, _) in zip(a, b):
         for k in names(8):
             assert torch.equal(x[k], y[k])
+
+
+@pytest.mark.parametrize("count", [1, 12])
+def test_batch_holds_its_tensors(count):
+    """A caller that puts other tensors into its dicts (new gradients) leaves the batch's alive."""
+    made = [make(300 + i, i, 32, False) for i in range(count)]
+    batch = fq.AdamwBatch([it for it, _ in made])
+    refs = [weakref.ref(it[k]) for it, _ in made for k in ("p", "g", "m", "v", "p16")]
+    kept = [dict(it) for it, _ in made]
+    for it, _ in made:
+        it.clear()
+    held = [{k: batch.items[i][k] for k in k0} for i, k0 in enumerate(kept)]
+    assert all(a[k] is b[k] for a, b in zip(kept, held) for k in a)
+    del kept, held, it
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    fq.qf_adamw_step(batch, 1e-3, 2)
+    for it, (_, h) in zip(batch.items, made):
+        same(it, want(h, 32, 1e-3, 2), 32, "held")
 
 
 def test_binding_checks():
