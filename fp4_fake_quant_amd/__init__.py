@@ -768,12 +768,8 @@ class AdamwBatch:
         self.arr = (AdamwTensor * max(len(items), 1))()
         self.device = _same_gpu(*[t for it in items for t in it.values() if isinstance(t, torch.Tensor)])
         state = torch.uint8 if state_bits == 8 else torch.float32
-        seen = set()
         for i, it in enumerate(items):
             n = it["p"].numel()
-            if n and it["p"].data_ptr() in seen:
-                raise ValueError("a tensor may appear once per batch")
-            seen.add(it["p"].data_ptr())
             d = self.arr[i]
             d.p = _flat(it["p"], "p", torch.float32, n)
             if it["g"].dtype not in (torch.float32, torch.bfloat16):
@@ -788,6 +784,11 @@ class AdamwBatch:
             if it.get("p16") is not None:
                 d.p16 = _flat(it["p16"], "p16", torch.bfloat16, n)
             d.n, d.weight_decay = n, float(it.get("weight_decay", 0.0))
+        # what the step writes, by address: the tensors of a launch run at the same time
+        written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for it in items
+                         for t in map(it.get, ("p", "m", "v", "m_scale", "v_scale", "p16")) if t is not None and t.numel())
+        if any(b[0] < a[1] for a, b in zip(written, written[1:])):
+            raise ValueError("a tensor may appear once per batch, and what a step writes must not overlap")
         self.ref = ctypes.byref(self.arr)
         self.plan = self.table = None
         if self.n > self.FEW:

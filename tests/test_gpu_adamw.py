@@ -209,6 +209,26 @@ def test_grouping_does_not_change_results():
             assert torch.equal(x[k], y[k])
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_shared_and_overlapping_tensors_are_refused(bits):
+    """Two tensors of a batch run at the same time: no state, weight or copy may serve both."""
+    a, b = (make(512, i, bits, False)[0] for i in (1, 2))
+    fq.AdamwBatch([a, b], bits)
+    for k in ("p", "m", "v", "p16") + (("m_scale", "v_scale") if bits == 8 else ()):
+        with pytest.raises(ValueError, match="overlap"):
+            fq.AdamwBatch([a, dict(b, **{k: a[k]})], bits)
+    both = torch.zeros(768, device="cuda")
+    with pytest.raises(ValueError, match="overlap"):
+        fq.AdamwBatch([dict(a, p=both[:512]), dict(b, p=both[256:])], bits)
+    with pytest.raises(ValueError, match="overlap"):
+        fq.AdamwBatch([dict(a, p16=a["p"].view(torch.bfloat16)[:512])], bits)
+    fq.AdamwBatch([a, dict(b, g=a["g"])], bits)          # only read
+    empty = dict(p=a["p"][:0], g=a["g"][:0], m=a["m"][:0], v=a["v"][:0])
+    if bits == 8:
+        empty.update(m_scale=a["m_scale"][:0], v_scale=a["v_scale"][:0])
+    fq.AdamwBatch([a, empty, empty], bits)
+
+
 @pytest.mark.parametrize("count", [1, 12])
 def test_batch_holds_its_tensors(count):
     """A caller that puts other tensors into its dicts (new gradients) leaves the batch's alive."""
