@@ -631,6 +631,13 @@ def _ids(t, name):
     return t
 
 
+def _space(ws):
+    """Bytes of a workspace, which must be one run of memory (an expanded view has less than it counts)."""
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
 class RowPlan:
     """Rows grouped by id (qf_row_plan): offsets [n_ids + 1], order [n] and tiles [t, 2], int32
     on the device, for n rows with ids in [0, n_ids).  One allocation, with the workspace that
@@ -659,7 +666,7 @@ def qf_row_plan(ids, n_ids, plan=None, ws=None):
     if ws is None:
         ws, ws_bytes = plan.ws, plan.ws_bytes
     else:
-        ws_bytes = ws.numel() * ws.element_size()
+        ws_bytes = _space(ws)
     _call(dev, "qf_row_plan", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
           plan.tiles.data_ptr(), ws.data_ptr(), ws_bytes)
     return plan
@@ -694,7 +701,7 @@ def _lora_apply(name, X, A, B, where, Y, scale, rows_per_x, ws):
         if ws_bytes:
             ws = torch.empty(ws_bytes, dtype=torch.uint8, device=X.device)
     else:
-        ws_bytes = ws.numel() * ws.element_size()
+        ws_bytes = _space(ws)
     if plan is None:
         _call(dev, name, X.data_ptr(), ldx, rows_per_x, A.data_ptr(), B.data_ptr(), _ptr(scale), E, where.data_ptr(),
               Y.data_ptr(), ldy, rows, N, K, r, _ptr(ws), ws_bytes)

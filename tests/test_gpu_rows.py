@@ -308,3 +308,17 @@ def test_binding_checks():
     with pytest.raises(fq.QFError):
         fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], fq.qf_row_plan(d["ids"], 4), d["Y"],
                                  ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_workspace_must_be_one_run_of_memory():
+    _, d = case(1000, 64, 40, 8, 4, 1)
+    plan = fq.qf_row_plan(d["ids"], 4)
+    need = max(fq.qf_lora_apply_workspace(1000, 64, 8, 4, p) for p in (False, True))
+    for ws in (torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need),
+               torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.qf_lora_apply(d["X"], d["A"], d["B"], d["ids"], d["Y"], ws=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.qf_lora_apply_planned(d["X"], d["A"], d["B"], plan, d["Y"], ws=ws)
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.qf_row_plan(torch.zeros(20000, dtype=torch.int32, device="cuda"), 4, ws=ws)
