@@ -67,6 +67,30 @@ def test_groups(E, G, kept, k, rule):
             check(x, k, scoring, bias=bias, renorm=False, **kw)
 
 
+@pytest.mark.parametrize("rule", ["max", "top2"])
+@pytest.mark.parametrize("E,G,kept,k", [(300, 4, 2, 8), (384, 8, 3, 8), (510, 5, 2, 32), (513, 3, 2, 9), (1000, 8, 3, 16),
+                                        (1001, 7, 3, 9), (1024, 64, 30, 32), (1023, 33, 4, 31)])
+def test_many_experts_in_groups_of_any_size(E, G, kept, k, rule):
+    for scoring in ("softmax", "sigmoid"):
+        for bf16 in (False, True):
+            x = logits(70, E, E + G, bf16)
+            bias = torch.from_numpy(np.random.default_rng(G).standard_normal(E) * 0.1).float().cuda()
+            kw = dict(n_group=G, topk_group=kept, group_rule=rule)
+            check(x, k, scoring, **kw)
+            check(x, k, scoring, bias=bias, renorm=False, **kw)
+
+
+@pytest.mark.parametrize("E,G", [(64, 4), (256, 8), (512, 4), (1000, 8)])
+def test_groups_of_an_unaligned_view(E, G):
+    for bf16 in (False, True):
+        x = torch.full((40, E + 5), float("nan"), dtype=torch.bfloat16 if bf16 else torch.float32, device="cuda")[:, 1:E + 1]
+        x.copy_(logits(40, E, E, bf16))
+        bias = torch.from_numpy(np.random.default_rng(G).standard_normal(E) * 0.1).float().cuda()
+        for rule in ("max", "top2"):
+            check(x, 6, "softmax", n_group=G, topk_group=2, group_rule=rule)
+            check(x, 6, "sigmoid", bias=bias, n_group=G, topk_group=2, group_rule=rule)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [dict(), dict(n_group=4, topk_group=2, group_rule="top2"), dict(n_group=4, topk_group=2)])
 def test_ties_and_masks(scoring, groups):
