@@ -351,10 +351,10 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
       for (int i = 0; i < V; ++i) bias[i] = 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = (x[i] == -RT_INF ? -RT_INF : v[i]) + bias[i];   // NaN for a bias of +inf or NaN
+    for (int i = 0; i < V; ++i) v[i] += bias[i];
   }
-  // a NaN or plus infinity poisons its row: as integers, positive ones are the largest signed
-  // numbers, and negative NaN lies above minus infinity among the unsigned
+  // a NaN or plus infinity (in a masked expert's bias too) poisons its row: as integers, positive ones
+  // are the largest signed numbers, and negative NaN lies above minus infinity among the unsigned
   int32_t most = INT32_MIN;
   uint32_t mostu = 0;
 #pragma unroll
@@ -362,6 +362,7 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
     most = std::max(most, (int32_t)__float_as_uint(v[i]));
     if (SCORES) most = std::max(most, (int32_t)__float_as_uint(x[i]));
     mostu = umax(mostu, __float_as_uint(v[i]));
+    if (SCORES) v[i] = x[i] == -RT_INF ? -RT_INF : v[i];
   }
   const uint64_t seg = ((1ull << L) - 1ull) << ((threadIdx.x & 63) / L * L);
   const bool bad = (__ballot(most >= 0x7F800000 || mostu > 0xFF800000u) & seg) != 0;
@@ -455,29 +456,40 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
 
   // weights: lane j (and j + L) of a row has its j-th choice
   float u[PER], xs[PER];
-  float first = -RT_INF;
+  bool low = false;
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     const int j = lane + p * L;
     if (!live || bad || j >= a.k) id[p] = -1;
     xs[p] = id[p] >= 0 ? rt_logit(row, id[p]) : -RT_INF;
-    first = fmaxf(first, xs[p]);
+    low |= id[p] >= 0 && xs[p] < RT_LOW;
   }
   float scale = a.scale;
-  bool exps = softmax;
-  if (a.renorm) {       // relative to the largest chosen logit: the row's other scores cancel
-    first = rt_row_max<L>(first);
-    exps = softmax || first < RT_LOW;
-    if (first == -RT_INF) first = 0.0f;
-    top = first;
-  }
   float sum = 0.0f;
+  if (!softmax && __ballot(low) == 0) {       // sigmoids without a low one in the wave
 #pragma unroll
-  for (int p = 0; p < PER; ++p) {
-    const bool low = exps || xs[p] < RT_LOW;
-    const float t = expf(exps ? xs[p] - top : low ? xs[p] : -xs[p]);
-    u[p] = id[p] < 0 ? 0.0f : low ? t : 1.0f / (1.0f + t);
-    sum += u[p];
+    for (int p = 0; p < PER; ++p) {
+      u[p] = id[p] < 0 ? 0.0f : 1.0f / (1.0f + expf(-xs[p]));
+      sum += u[p];
+    }
+  } else {
+    bool exps = softmax;
+    if (a.renorm) {       // relative to the largest chosen logit: the row's other scores cancel
+      float first = -RT_INF;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) first = fmaxf(first, xs[p]);
+      first = rt_row_max<L>(first);
+      exps = softmax || first < RT_LOW;
+      if (first == -RT_INF) first = 0.0f;
+      top = first;
+    }
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+      const bool exp = exps || xs[p] < RT_LOW;
+      const float t = expf(exps ? xs[p] - top : exp ? xs[p] : -xs[p]);
+      u[p] = id[p] < 0 ? 0.0f : exp ? t : 1.0f / (1.0f + t);
+      sum += u[p];
+    }
   }
   if (a.renorm) total = rt_row_sum<L>(sum);
   const bool divide = a.renorm || softmax;
