@@ -775,6 +775,7 @@ class AdamwBatch:
         self.arr = (AdamwTensor * max(len(items), 1))()
         self.device = _same_gpu(*[t for it in items for t in it.values() if isinstance(t, torch.Tensor)])
         state = torch.uint8 if state_bits == 8 else torch.float32
+        written = []                                     # (address, bytes) of what the step writes
         for i, it in enumerate(items):
             n = it["p"].numel()
             d = self.arr[i]
@@ -791,10 +792,16 @@ class AdamwBatch:
             if it.get("p16") is not None:
                 d.p16 = _flat(it["p16"], "p16", torch.bfloat16, n)
             d.n, d.weight_decay = n, float(it.get("weight_decay", 0.0))
-        # what the step writes, by address: the tensors of a launch run at the same time
-        written = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for it in items
-                         for t in map(it.get, ("p", "m", "v", "m_scale", "v_scale", "p16")) if t is not None and t.numel())
-        if any(b[0] < a[1] for a, b in zip(written, written[1:])):
+            if n:
+                size = n * state_bits // 8
+                written += ((d.p, n * 4), (d.m, size), (d.v, size))
+                if state_bits == 8:
+                    written += ((d.m_scale, blocks * 4), (d.v_scale, blocks * 4))
+                if d.p16:
+                    written.append((d.p16, n * 2))
+        # the tensors of a launch run at the same time
+        written.sort()
+        if any(a + size > b for (a, size), (b, _) in zip(written, written[1:])):
             raise ValueError("a tensor may appear once per batch, and what a step writes must not overlap")
         self.ref = ctypes.byref(self.arr)
         self.plan = self.table = None
