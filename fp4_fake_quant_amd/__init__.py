@@ -811,6 +811,7 @@ class AdamwBatch:
             _check(lib().qf_adamw_table(self.ref, self.n, state_bits, host.data_ptr(), host.numel(),
                                         ctypes.byref(self.plan)), "qf_adamw_table")
             self.table = host.to(torch.device("cuda", self.device))
+            self.stream = torch._C._cuda_getCurrentRawStream(self.device)
 
 
 def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_lr=None, d_step=None,
@@ -831,6 +832,9 @@ def qf_adamw_step(batch, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, seed=0, d_l
     if batch.table is None:
         _call(batch.device, "qf_adamw_step", batch.ref, batch.n, batch.state_bits, ctypes.byref(h))
     else:
+        # a step on another stream than the table's: the allocator keeps the table until that step is done
+        if torch._C._cuda_getCurrentRawStream(batch.device) != batch.stream and not torch.cuda.is_current_stream_capturing():
+            batch.table.record_stream(torch.cuda.current_stream(batch.device))
         _call(batch.device, "qf_adamw_step_table", ctypes.byref(batch.plan), batch.table.data_ptr(), ctypes.byref(h))
 
 

@@ -209,6 +209,25 @@ def test_grouping_does_not_change_results():
             assert torch.equal(x[k], y[k])
 
 
+def test_table_outlives_a_step_on_another_stream():
+    """A batch dropped while its step waits on another stream: the table's memory is not given out again."""
+    made = [make(300 + i, i, 32, False) for i in range(20)]
+    batch = fq.AdamwBatch([it for it, _ in made])
+    at, size = batch.table.data_ptr(), batch.table.numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)                    # cycles; the step is queued behind it
+        fq.qf_adamw_step(batch, 1e-3, 2)
+    busy = not side.query()
+    del batch
+    fresh = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    assert busy and all(t.data_ptr() != at for t in fresh)
+    torch.cuda.synchronize()
+    for it, h in made:
+        same(it, want(h, 32, 1e-3, 2), 32, "side stream")
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_shared_and_overlapping_tensors_are_refused(bits):
     """Two tensors of a batch run at the same time: no state, weight or copy may serve both."""
