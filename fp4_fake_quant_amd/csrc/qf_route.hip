@@ -569,15 +569,29 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route_backward(RouteArgs
     top = fmaxf(top, x[p]);
   }
   if (!dense) {
-    if (softmax || a.renorm) top = rt_row_max<L>(top);
-    const bool exps = softmax || (a.renorm && top < RT_LOW);
+    if (softmax) {
+      top = rt_row_max<L>(top);
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-      const bool low = exps || x[p] < RT_LOW;
-      const float t = expf(exps ? x[p] - top : low ? x[p] : -x[p]);
-      u[p] = id[p] < 0 || x[p] == -RT_INF ? 0.0f : low ? t : 1.0f / (1.0f + t);
-      // for positive x, 1 - u would lose all digits that u's rounding drops
-      rest[p] = low ? 1.0f : x[p] > 0.0f ? t * u[p] : 1.0f - u[p];
+      for (int p = 0; p < PER; ++p) {
+        u[p] = id[p] >= 0 && top > -RT_INF ? expf(x[p] - top) : 0.0f;
+        rest[p] = 1.0f;
+      }
+    } else {
+      bool low = false;
+#pragma unroll
+      for (int p = 0; p < PER; ++p) low |= id[p] >= 0 && x[p] < RT_LOW;
+      const bool any = __ballot(low) != 0;       // in the wave
+      if (any && a.renorm) top = rt_row_max<L>(top);
+#pragma unroll
+      for (int p = 0; p < PER; ++p) {
+        const float t = expf(-x[p]);
+        u[p] = id[p] < 0 ? 0.0f : 1.0f / (1.0f + t);
+        rest[p] = x[p] > 0.0f ? t * u[p] : 1.0f - u[p];      // 1 - u would lose the digits that u's rounding drops
+        if (any && x[p] < RT_LOW) {
+          u[p] = x[p] == -RT_INF ? 0.0f : expf(a.renorm && top < RT_LOW ? x[p] - top : x[p]);
+          rest[p] = 1.0f;
+        }
+      }
     }
     if (a.renorm) {
       float total = 0.0f, mean = 0.0f;
