@@ -33,7 +33,8 @@ constexpr float AW_MIN_MAX = 7.888609052210118e-31f;   // 2^-100: smaller block 
 
 static_assert(AW_BLOCK == 256, "a wave of 64 lanes holds one block, 4 elements per lane");
 
-// 32-bit finaliser: xor-shifts and two odd multipliers.
+// 32-bit finaliser: xor-shifts and two odd multipliers, the constants of Wellons's published search
+// for integer hashes of low bias (2018).
 __host__ __device__ inline uint32_t aw_hash(uint32_t x) {
   x ^= x >> 16;
   x *= 0x7FEB352Du;
@@ -82,7 +83,7 @@ __device__ __forceinline__ uint32_t aw_e4m3_stochastic(float y, uint32_t rnd) {
 
 // The correctly rounded square root of v >= 0 that is 0 or at least 2^-96 (below, the residuals
 // underflow): the hardware's, which is at most one unit off, and its two neighbours tested by
-// the sign of v - s s'.
+// the sign of v - s s' (Tuckerman's rounding test; Agarwal and others, IBM J. Res. Dev. 30, 1986).
 __device__ __forceinline__ float aw_sqrt(float v) {
   float s = __builtin_amdgcn_sqrtf(v);
   const float down = __uint_as_float(__float_as_uint(s) - 1u), up = __uint_as_float(__float_as_uint(s) + 1u);

@@ -16,7 +16,8 @@
 // again, on the fp32 logits themselves or on 64-bit scores.  bf16 logits fit a key with their
 // index and need no second pass.  The selection is bounded by vector instructions (k + 1 rounds
 // of about 40), the rest by memory: 32768 rows of 256 experts with bias, 4 of 8 groups and top 8
-// take 26 us (36 MB), 17 of them before any second pass; 7 rows of 128 experts 3.1.
+// take 26.5 us (36 MB), 17 of them before any second pass; 7 rows of 128 experts 3.2, 32768 rows of 128
+// experts without bias or groups 9.5 (bf16 7.0).
 #include <float.h>
 
 #include <algorithm>
@@ -263,14 +264,14 @@ __device__ __forceinline__ bool rt_select_keys(int rounds, int lane, const uint3
 
 constexpr int rt_log2(int v) { return v <= 1 ? 0 : 1 + rt_log2(v / 2); }
 
-// exp in 64 bits for finite x <= 709: x = n ln 2 + r, |r| <= ln 2 / 2, and r's Taylor polynomial
-// (the term after the last is below 2^-57); about two units of rounding.  The second pass is rare
-// and its code cold, so it is short.
+// exp in 64 bits for x <= 709: x = n ln 2 + r with ln 2 in two parts (Cody and Waite's reduction),
+// |r| <= ln 2 / 2, and r's Taylor polynomial (the term after the last is below 2^-57); about two
+// units of rounding.  The second pass is rare and its code cold, so it is short.
 __device__ __forceinline__ double rt_exp64(double x) {
   x = fmax(x, -746.0);                               // from there on exp is 0 in 64 bits
   const double n = __builtin_rint(x * 1.4426950408889634);
   double r = __builtin_fma(n, -0x1.62e42fefa39efp-1, x);
-  r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);   // ln 2 in two parts
+  r = __builtin_fma(n, -0x1.abc9e3b39803fp-56, r);
   double p = 1.0 / 6227020800.0;                     // 1 / 13!
   p = __builtin_fma(p, r, 1.0 / 479001600.0);
   p = __builtin_fma(p, r, 1.0 / 39916800.0);
@@ -506,9 +507,10 @@ __global__ __launch_bounds__(RT_WAVE * RT_WAVES) void k_route(RouteArgs a) {
 // Gradient of the weights with respect to the logits.  With p_j = u_j / sum u:
 //   renormalised, softmax:  dx[i_j] = c p_j (g_j - sum g p);   sigmoid: times (1 - u_j)
 //   plain, sigmoid: dx[i_j] = c g_j u_j (1 - u_j);  softmax: dx[e] = c s_e (g_e - sum g u)
+// with 1 - u of a sigmoid as exp(-x) u for positive x, and as 1 below RT_LOW.
 // Lanes and logits are laid out as in the forward pass; the chosen ones (two per lane where k is
 // over L) meet the row in LDS, so that the gradient leaves as one dense, coalesced row.  Bounded
-// by the dense write (and the read, for plain softmax): 32768 x 128 bf16 6.3 us, 4099 x 128 fp32 4.1,
+// by the dense write (and the read, for plain softmax): 32768 x 128 bf16 6.4 us, 4099 x 128 fp32 4.1,
 // of which an empty launch is 2.5.
 template <int V, bool VEC>
 __device__ __forceinline__ void rt_store(float* row, int e0, int E, const float (&x)[V]) {
