@@ -16,7 +16,8 @@ quant        E4M3 codes of x / s with one fp32 scale s = max |x| / 448 per block
 swiglu       a = u g / (1 + exp(-g)) of h = [g, u], quantized in rows;  swiglu_bwd: dh from da
 gemm         y = sum over blocks b of 128 of sx[m, b] sw[n / 128, b] sum_(k in b) x[m, k] w[n, k]
 experts      the same with w of the expert that position p belongs to
-wgrad        dw[e] = sum over the blocks of expert e's rows of sy[n, b] sx[k, b] sum dy[p, n] x[p, k]
+wgrad        dw[e] = sum over the blocks of expert e's rows of sy[n, b] sx[k, b] sum dy[p, n] x[p, k],
+             in bf16 as the optimizer and the straight-through accumulation read it
 """
 
 import math
@@ -55,7 +56,7 @@ def listed():
         # a prefill through 64 experts
         dict(name="experts_prefill", op="experts", T=4096, k=8, E=64, N=4096, K=4096, none=0.0),
         # the weight gradients of an experts' share
-        dict(name="wgrad_experts", op="wgrad", T=4096, k=8, E=64, N=2048, K=2048, dtype="f32", none=0.0),
+        dict(name="wgrad_experts", op="wgrad", T=4096, k=8, E=64, N=2048, K=2048, none=0.0),
     ]
 
 
@@ -80,10 +81,7 @@ def draw(rng):
     if op == "gemm":
         return dict(op=op, M=_log(rng, 1, 8192), N=_log(rng, 16, 8192), K=16 * _log(rng, 1, 512))
     E = _log(rng, 1, 64)
-    c = dict(op=op, T=_log(rng, 1, 2048), k=rng.randint(1, 8), E=E, N=8 * _log(rng, 8, 256), K=16 * _log(rng, 4, 128), none=none)
-    if op == "wgrad":
-        c["dtype"] = rng.choice(["f32", "bf16"])
-    return c
+    return dict(op=op, T=_log(rng, 1, 2048), k=rng.randint(1, 8), E=E, N=8 * _log(rng, 8, 256), K=16 * _log(rng, 4, 128), none=none)
 
 
 # ------------------------------------------------------------------ inputs ----
@@ -326,8 +324,7 @@ def _plain_wgrad(s):
         return pad.view(c["E"], most * B, cols)
 
     dy, x = groups(s["yc"], s["ys"], c["N"]), groups(s["xc"], s["xs"], c["K"])
-    dw = torch.bmm(dy.transpose(1, 2), x)
-    return dw.bfloat16() if c["dtype"] == "bf16" else dw
+    return torch.bmm(dy.transpose(1, 2), x).bfloat16()
 
 
 # ------------------------------------------------------------------- passes ----
@@ -363,8 +360,7 @@ def run(state):
         return fq.qf_gemm_fp8(s["xc"], s["xs"], s["wc"], s["ws"])
     if op == "experts":
         return fq.qf_gemm_fp8_grouped(s["xc"], s["xs"], s["wc"], s["ws"], s["plan"], Y=s["y"])
-    return fq.qf_gemm_fp8_wgrad(s["yc"], s["ys"], s["xc"], s["xs"], s["plan"],
-                                dtype=torch.bfloat16 if c["dtype"] == "bf16" else torch.float32)
+    return fq.qf_gemm_fp8_wgrad(s["yc"], s["ys"], s["xc"], s["xs"], s["plan"])
 
 
 # --------------------------------------------------------------------- work ----
@@ -397,7 +393,7 @@ def work(case):
         return dict(bytes=M * K * (1 + 4 / B) + N * K * (1 + 4 / B ** 2) + 2 * M * N, flops=2 * M * N * K)
     if op == "experts":
         return dict(bytes=rows * K * (1 + 4 / B) + met * N * K * (1 + 4 / B ** 2) + 2 * rows * N, flops=2 * rows * N * K)
-    return dict(bytes=rows * (N + K) * (1 + 4 / B) + E * N * K * (4 if c["dtype"] == "f32" else 2), flops=2 * rows * N * K)
+    return dict(bytes=rows * (N + K) * (1 + 4 / B) + 2 * E * N * K, flops=2 * rows * N * K)
 
 
 # -------------------------------------------------------------------- exact ----
