@@ -640,36 +640,338 @@ def _space(ws):
 
 class RowPlan:
     """Rows grouped by id (qf_row_plan): offsets [n_ids + 1], order [n] and tiles [t, 2], int32
-    on the device, for n rows with ids in [0, n_ids).  One allocation, with the workspace that
-    building it takes."""
+    on the device, for n rows with ids in [0, n_ids); positions [n], order's inverse, or None.
+    One allocation, with the workspace that building it takes."""
 
-    def __init__(self, n, n_ids, device):
+    def __init__(self, n, n_ids, device, positions=False):
         self.n, self.n_ids = n, n_ids
         t, self.ws_bytes = lib().qf_row_plan_tiles(n, n_ids), lib().qf_row_plan_workspace(n, n_ids)
-        sizes = (2 * t, self.ws_bytes // 4, n_ids + 1, n)        # what is 8-byte aligned first
-        tiles, self.ws, self.offsets, self.order = torch.empty(sum(sizes), dtype=torch.int32,
-                                                               device=device).split_with_sizes(sizes)
+        sizes = (2 * t, self.ws_bytes // 4, n_ids + 1, n) + ((n,) if positions else ())   # what is 8-byte aligned first
+        tiles, self.ws, self.offsets, self.order, *rest = torch.empty(sum(sizes), dtype=torch.int32,
+                                                                      device=device).split_with_sizes(sizes)
         self.tiles = tiles.view(t, 2)
+        self.positions = rest[0] if positions else None
 
 
-def qf_row_plan(ids, n_ids, plan=None, ws=None):
+def qf_row_plan(ids, n_ids, plan=None, ws=None, positions=False):
     """The RowPlan of ids (int32 device tensor, any shape; row i is element i in memory order):
-    rows with an id outside [0, n_ids) are in no group.  plan: one of the same n and n_ids to
-    write into; ws: a workspace other than the plan's own."""
+    rows with an id outside [0, n_ids) are in no group.  positions: with order's inverse, which
+    qf_moe_combine reads.  plan: one of the same n and n_ids to write into; ws: a workspace other
+    than the plan's own."""
     dev, n, n_ids = _same_gpu(_ids(ids, "ids"), ws), ids.numel(), int(n_ids)
     if plan is None:
         if not 1 <= n_ids <= ROW_MAX_IDS:
             raise ValueError(f"n_ids is 1..{ROW_MAX_IDS}")
-        plan = RowPlan(n, n_ids, ids.device)
+        plan = RowPlan(n, n_ids, ids.device, positions)
     elif plan.n != n or plan.n_ids != n_ids or plan.offsets.get_device() != dev:
         raise ValueError(f"the plan is for {plan.n} rows of {plan.n_ids} ids on {plan.offsets.device}")
+    elif positions and plan.positions is None:
+        raise ValueError("the plan was built without positions")
     if ws is None:
         ws, ws_bytes = plan.ws, plan.ws_bytes
     else:
         ws_bytes = _space(ws)
-    _call(dev, "qf_row_plan", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
-          plan.tiles.data_ptr(), ws.data_ptr(), ws_bytes)
+    if plan.positions is None:
+        _call(dev, "qf_row_plan", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
+              plan.tiles.data_ptr(), ws.data_ptr(), ws_bytes)
+    else:
+        _call(dev, "qf_row_plan_positions", ids.data_ptr(), n, n_ids, plan.offsets.data_ptr(), plan.order.data_ptr(),
+              plan.tiles.data_ptr(), plan.positions.data_ptr(), ws.data_ptr(), ws_bytes)
     return plan
+
+
+# ----------------------------------------- rows into expert order and back ----
+def _plan(plan):
+    if not isinstance(plan, RowPlan):
+        raise TypeError("plan must be a RowPlan")
+    return plan
+
+
+def _out16(t, name, rows, cols, device):
+    """A bf16 output [rows, cols] and its row stride."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device), cols
+    if tuple(_bf16(t, name).shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, want {(rows, cols)}")
+    return t, _mat(t, name)[2]
+
+
+def _x_rows(rows, n, rows_per_x):
+    if rows_per_x < 1 or rows != (n + rows_per_x - 1) // rows_per_x:
+        raise ValueError(f"x has {rows} rows for {n} rows of the plan and rows_per_x={rows_per_x}")
+
+
+def qf_moe_dispatch(X, plan, rows_per_x=1, out=None):
+    """out[p] = X[plan.order[p] // rows_per_x], bf16 [plan.n, H]: rows into the order of the plan's
+    groups.  Rows behind the last group are left as they were (unspecified where out is new)."""
+    dev = _same_gpu(X, out, _plan(plan).order)
+    rows, H, ldx = _mat(_bf16(X, "X"), "X")
+    _x_rows(rows, plan.n, rows_per_x)
+    out, ldo = _out16(out, "out", plan.n, H, X.device)
+    _call(dev, "qf_moe_dispatch", X.data_ptr(), ldx, rows_per_x, plan.order.data_ptr(), plan.n, H, out.data_ptr(), ldo)
+    return out
+
+
+def _combine(plan, R, weights, k):
+    if _plan(plan).positions is None:
+        raise ValueError("the plan must be built with positions=True")
+    if weights is not None:
+        if weights.dim() != 2 or k not in (None, weights.shape[1]):
+            raise ValueError("weights must have shape [tokens, k]")
+        k = weights.shape[1]
+        _dense(weights, "weights", torch.float32, (plan.n // k if k else 0, k))
+    if not k or k < 1 or plan.n % k:
+        raise ValueError(f"k={k} does not divide the plan's {plan.n} rows")
+    return plan.n // k, k
+
+
+def qf_moe_combine(R, plan, weights=None, k=None, Y=None):
+    """Y[t] = sum_j weights[t, j] * R[plan.positions[t * k + j]], bf16 [tokens, H], from R [plan.n,
+    H] in the order of the plan's groups: weights float32 [tokens, k], or None with k given (all 1:
+    the gradient of qf_moe_dispatch with rows_per_x = k).  Rows in no group add nothing."""
+    tokens, k = _combine(plan, R, weights, k)
+    dev = _same_gpu(R, weights, Y, plan.order)
+    rows, H, ldr = _mat(_bf16(R, "R"), "R")
+    if rows != plan.n:
+        raise ValueError(f"R has {rows} rows, the plan {plan.n}")
+    Y, ldy = _out16(Y, "Y", tokens, H, R.device)
+    _call(dev, "qf_moe_combine", R.data_ptr(), ldr, plan.positions.data_ptr(), _ptr(weights), tokens, k, H, Y.data_ptr(), ldy)
+    return Y
+
+
+def qf_moe_combine_backward(dY, R, plan, weights=None, k=None, d_rows=None, d_weights=None, want=(True, True)):
+    """(d_rows bf16 [plan.n, H], d_weights float32 [tokens, k]) of qf_moe_combine: d_rows[p] =
+    weights * dY[t], d_weights = <R[p], dY[t]>; None for what is not wanted.  Rows of d_rows behind
+    the last group are left as they were (unspecified where d_rows is new)."""
+    tokens, k = _combine(plan, R, weights, k)
+    if not want[1]:
+        R = None
+    dev = _same_gpu(dY, R, weights, d_rows, d_weights, plan.order)
+    rows, H, ldd = _mat(_bf16(dY, "dY"), "dY")
+    if rows != tokens:
+        raise ValueError(f"dY has {rows} rows for {tokens} tokens")
+    ldr = ldo = H
+    if want[1]:
+        if tuple(_bf16(R, "R").shape) != (plan.n, H):
+            raise ValueError(f"R has shape {tuple(R.shape)}, want {(plan.n, H)}")
+        ldr = _mat(R, "R")[2]
+        if d_weights is None:
+            d_weights = torch.empty((tokens, k), dtype=torch.float32, device=dY.device)
+        else:
+            _dense(d_weights, "d_weights", torch.float32, (tokens, k))
+    if want[0]:
+        d_rows, ldo = _out16(d_rows, "d_rows", plan.n, H, dY.device)
+    _call(dev, "qf_moe_combine_backward", dY.data_ptr(), ldd, _ptr(R), ldr, plan.positions.data_ptr(), _ptr(weights), tokens,
+          k, H, d_rows.data_ptr() if want[0] else None, ldo, d_weights.data_ptr() if want[1] else None)
+    return (d_rows if want[0] else None), (d_weights if want[1] else None)
+
+
+# ------------------------------------------------- 8-bit blocks of 128 ----
+FP8_BLOCK = 128
+
+
+def _codes(t, name, shape=None):
+    """A uint8 matrix of codes with contiguous rows: its row stride."""
+    if t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be torch.uint8")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, want {shape}")
+    return _mat(t, name)[2]
+
+
+def _row_codes(rows, cols, device, codes, scales):
+    """Outputs of a row quantization, with their row strides."""
+    blocks = (cols + FP8_BLOCK - 1) // FP8_BLOCK
+    if codes is None:
+        codes, ldc = torch.empty((rows, cols), dtype=torch.uint8, device=device), cols
+    else:
+        ldc = _codes(codes, "codes", (rows, cols))
+    if scales is None:
+        return codes, ldc, torch.empty((blocks, rows), dtype=torch.float32, device=device), rows
+    return codes, ldc, scales, _scales(scales, "scales", blocks, rows)
+
+
+def _scales(t, name, blocks, rows):
+    """Block-major scales [blocks, rows]: their row stride."""
+    if t.dtype != torch.float32 or tuple(t.shape) != (blocks, rows):
+        raise ValueError(f"{name} must be a float32 tensor of shape {(blocks, rows)}")
+    ld = _mat(t, name)[2]
+    return max(ld, rows)
+
+
+def qf_quant_fp8(x, plan=None, rows_per_x=None, codes=None, scales=None):
+    """(codes uint8 [rows, cols], scales float32 [ceil(cols / 128), rows]): E4M3 codes of x bf16 in
+    blocks of 128 along its rows.  plan: with rows_per_x, row p is x[plan.order[p] // rows_per_x]
+    (rows into expert order on the way); without, x's rows are in that order already.  Rows behind
+    the plan's last group are left as they were (unspecified in new outputs)."""
+    rows, cols, ldx = _mat(_bf16(x, "x"), "x")
+    dev = _same_gpu(x, codes, scales, None if plan is None else _plan(plan).order)
+    order = used = None
+    if plan is not None:
+        _x_rows(rows, plan.n, 1 if rows_per_x is None else rows_per_x)
+        rows = plan.n
+        if rows_per_x is None:
+            used = plan.offsets.data_ptr() + 4 * plan.n_ids
+        else:
+            order = plan.order.data_ptr()
+    elif rows_per_x is not None:
+        raise ValueError("rows_per_x needs a plan")
+    codes, ldc, scales, lds = _row_codes(rows, cols, x.device, codes, scales)
+    _call(dev, "qf_quant_fp8", x.data_ptr(), ldx, rows, cols, order, rows_per_x or 1, used, codes.data_ptr(), ldc,
+          scales.data_ptr(), lds)
+    return codes, scales
+
+
+def qf_fp8_panels(rows, n_ids=1):
+    """Panels of 128 rows that rows in n_ids groups fill at most."""
+    return lib().qf_fp8_panels(int(rows), int(n_ids))
+
+
+def qf_quant_fp8_panels(x, plan=None, rows_per_x=None, codes=None, scales=None):
+    """(codes uint8 [panels, cols, 128], scales float32 [panels, cols]): E4M3 codes of x bf16 in blocks
+    of 128 rows of one group of the plan (None: all rows are one), transposed, the operands of
+    qf_gemm_fp8_wgrad.  rows_per_x as qf_quant_fp8.  Panels behind the last are left as they were."""
+    rows, cols, ldx = _mat(_bf16(x, "x"), "x")
+    dev = _same_gpu(x, codes, scales, None if plan is None else _plan(plan).order)
+    order = offsets = None
+    n_ids = 1
+    if plan is not None:
+        _x_rows(rows, plan.n, 1 if rows_per_x is None else rows_per_x)
+        rows, n_ids, offsets = plan.n, plan.n_ids, plan.offsets.data_ptr()
+        order = None if rows_per_x is None else plan.order.data_ptr()
+    elif rows_per_x is not None:
+        raise ValueError("rows_per_x needs a plan")
+    panels = lib().qf_fp8_panels(rows, n_ids)
+    if codes is None:
+        codes = torch.empty((panels, cols, FP8_BLOCK), dtype=torch.uint8, device=x.device)
+    else:
+        _dense(codes, "codes", torch.uint8, (panels, cols, FP8_BLOCK))
+    if scales is None:
+        scales = torch.empty((panels, cols), dtype=torch.float32, device=x.device)
+    else:
+        _dense(scales, "scales", torch.float32, (panels, cols))
+    _call(dev, "qf_quant_fp8_panels", x.data_ptr(), ldx, rows, cols, order, rows_per_x or 1, offsets, n_ids,
+          codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def qf_quant_fp8_tiles(x, transpose=False, codes=None, scales=None, codes_t=None, scales_t=None):
+    """(codes, scales) of x bf16 [rows, cols] or [count, rows, cols] in tiles of 128 x 128: codes of
+    x's shape, scales float32 [..., ceil(rows / 128), ceil(cols / 128)]; with transpose also
+    (codes_t, scales_t), the same values as codes and scales of x's transpose."""
+    if _bf16(x, "x").dim() not in (2, 3):
+        raise ValueError("x must be a 2-D or 3-D tensor")
+    dev = _same_gpu(x, codes, scales, codes_t, scales_t)
+    count = x.shape[0] if x.dim() == 3 else 1
+    lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
+    ld = x.stride(-2) if rows > 1 else max(cols, x.stride(-2))
+    if (x.stride(-1) != 1 and cols > 1) or (count > 1 and x.stride(0) != rows * ld):
+        raise ValueError("x must have contiguous rows, and its matrices must follow one another")
+    rt, ct = (rows + FP8_BLOCK - 1) // FP8_BLOCK, (cols + FP8_BLOCK - 1) // FP8_BLOCK
+    outs = [(codes, "codes", torch.uint8, lead + (rows, cols)), (scales, "scales", torch.float32, lead + (rt, ct))]
+    if transpose:
+        outs += [(codes_t, "codes_t", torch.uint8, lead + (cols, rows)), (scales_t, "scales_t", torch.float32, lead + (ct, rt))]
+    elif codes_t is not None or scales_t is not None:
+        raise ValueError("codes_t and scales_t need transpose=True")
+    outs = [torch.empty(shape, dtype=kind, device=x.device) if t is None else _dense(t, name, kind, shape)
+            for t, name, kind, shape in outs]
+    _call(dev, "qf_quant_fp8_tiles", x.data_ptr(), ld, count, rows, cols, outs[0].data_ptr(), outs[1].data_ptr(),
+          outs[2].data_ptr() if transpose else None, outs[3].data_ptr() if transpose else None)
+    return tuple(outs)
+
+
+def qf_swiglu_quant_fp8(h, plan=None, y=None, codes=None, scales=None):
+    """(codes uint8 [rows, cols], scales float32 [ceil(cols / 128), rows]) of u * g * sigmoid(g), h bf16
+    [rows, 2 cols] = [g, u], as qf_quant_fp8 lays them out; y (bf16 [rows, cols]) gets the product as
+    well.  plan: rows behind its last group are left as they were."""
+    rows, wide, ldh = _mat(_bf16(h, "h"), "h")
+    dev = _same_gpu(h, y, codes, scales, None if plan is None else _plan(plan).order)
+    if wide % 2 or (plan is not None and plan.n != rows):
+        raise ValueError(f"h has shape {tuple(h.shape)}" + ("" if plan is None else f" for {plan.n} rows of the plan"))
+    cols = wide // 2
+    codes, ldc, scales, lds = _row_codes(rows, cols, h.device, codes, scales)
+    ldy = cols
+    if y is not None:
+        y, ldy = _out16(y, "y", rows, cols, h.device)
+    _call(dev, "qf_swiglu_quant_fp8", h.data_ptr(), ldh, rows, cols,
+          None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_ids, codes.data_ptr(), ldc, scales.data_ptr(), lds,
+          _ptr(y), ldy)
+    return codes, scales
+
+
+def qf_swiglu_backward(h, da, plan=None, dh=None):
+    """dh bf16 [rows, 2 cols] of a = u * g * sigmoid(g), h = [g, u], from da bf16 [rows, cols].  plan: rows
+    behind its last group are left as they were (unspecified where dh is new)."""
+    rows, wide, ldh = _mat(_bf16(h, "h"), "h")
+    dev = _same_gpu(h, da, dh, None if plan is None else _plan(plan).order)
+    if wide % 2 or (plan is not None and plan.n != rows) or tuple(_bf16(da, "da").shape) != (rows, wide // 2):
+        raise ValueError(f"shapes h {tuple(h.shape)}, da {tuple(da.shape)} do not fit")
+    dh, ldo = _out16(dh, "dh", rows, wide, h.device)
+    _call(dev, "qf_swiglu_backward", h.data_ptr(), ldh, da.data_ptr(), _mat(da, "da")[2], rows, wide // 2,
+          None if plan is None else plan.offsets.data_ptr() + 4 * plan.n_ids, dh.data_ptr(), ldo)
+    return dh
+
+
+def qf_gemm_fp8(Xc, Xs, Wc, Ws, Y=None):
+    """Y bf16 [M, N] = X W^T of E4M3 codes: Xc [M, K] and Xs [ceil(K / 128), M] as qf_quant_fp8 gives
+    them, Wc [N, K] and Ws [ceil(N / 128), ceil(K / 128)] as qf_quant_fp8_tiles."""
+    dev = _same_gpu(Xc, Xs, Wc, Ws, Y)
+    ldx, ldw = _codes(Xc, "Xc"), _codes(Wc, "Wc")
+    (M, K), (N, K2) = Xc.shape, Wc.shape
+    if K != K2:
+        raise ValueError(f"Xc has K={K} but Wc has K={K2}")
+    blocks = (K + FP8_BLOCK - 1) // FP8_BLOCK
+    ldxs = _scales(Xs, "Xs", blocks, M)
+    _dense(Ws, "Ws", torch.float32, ((N + FP8_BLOCK - 1) // FP8_BLOCK, blocks))
+    Y, ldy = _out16(Y, "Y", M, N, Xc.device)
+    _call(dev, "qf_gemm_fp8", Xc.data_ptr(), ldx, Xs.data_ptr(), ldxs, Wc.data_ptr(), ldw, Ws.data_ptr(), Y.data_ptr(), ldy,
+          M, N, K)
+    return Y
+
+
+def qf_gemm_fp8_grouped(Xc, Xs, Wc, Ws, plan, Y=None):
+    """qf_gemm_fp8 for rows in a plan's order, each group with its own weights: Wc [n_ids, N, K], Ws
+    [n_ids, ceil(N / 128), ceil(K / 128)].  Rows of Y behind the last group are left as they were
+    (unspecified where Y is new)."""
+    dev = _same_gpu(Xc, Xs, Wc, Ws, Y, _plan(plan).order)
+    ldx = _codes(Xc, "Xc")
+    if Wc.dtype != torch.uint8 or Wc.dim() != 3 or not Wc.is_contiguous():
+        raise ValueError("Wc must be a contiguous 3-D uint8 tensor")
+    (M, K), (E, N, K2) = Xc.shape, Wc.shape
+    if K != K2 or M != plan.n or E != plan.n_ids:
+        raise ValueError(f"shapes Xc {tuple(Xc.shape)}, Wc {tuple(Wc.shape)} do not fit a plan of {plan.n} rows, {plan.n_ids} ids")
+    blocks = (K + FP8_BLOCK - 1) // FP8_BLOCK
+    ldxs = _scales(Xs, "Xs", blocks, M)
+    _dense(Ws, "Ws", torch.float32, (E, (N + FP8_BLOCK - 1) // FP8_BLOCK, blocks))
+    Y, ldy = _out16(Y, "Y", M, N, Xc.device)
+    _call(dev, "qf_gemm_fp8_grouped", Xc.data_ptr(), ldx, Xs.data_ptr(), ldxs, Wc.data_ptr(), K, Ws.data_ptr(),
+          plan.offsets.data_ptr(), plan.tiles.data_ptr(), E, Y.data_ptr(), ldy, M, N, K)
+    return Y
+
+
+def qf_gemm_fp8_wgrad(Dc, Ds, Xc, Xs, plan=None, dW=None):
+    """dW bf16 [n_ids, N, K] (plan None: [N, K]) from the panels of dY (Dc [panels, N, 128], Ds
+    [panels, N]) and X (Xc [panels, K, 128], Xs) under the same plan (qf_quant_fp8_panels): the
+    gradient of qf_gemm_fp8_grouped's weights, zero for a group without rows."""
+    dev = _same_gpu(Dc, Ds, Xc, Xs, dW, None if plan is None else _plan(plan).order)
+    if Dc.dim() != 3 or Xc.dim() != 3:
+        raise ValueError("Dc and Xc must be panels [panels, cols, 128]")
+    panels, N, K = Dc.shape[0], Dc.shape[1], Xc.shape[1]
+    rows = panels * FP8_BLOCK if plan is None else plan.n
+    n_ids = 1 if plan is None else plan.n_ids
+    if plan is not None and panels != lib().qf_fp8_panels(rows, n_ids):
+        raise ValueError(f"{panels} panels for a plan of {rows} rows, {n_ids} ids")
+    for c, s, cols, name in ((Dc, Ds, N, "D"), (Xc, Xs, K, "X")):
+        _dense(c, name + "c", torch.uint8, (panels, cols, FP8_BLOCK))
+        _dense(s, name + "s", torch.float32, (panels, cols))
+    shape = (N, K) if plan is None else (n_ids, N, K)
+    if dW is None:
+        dW = torch.empty(shape, dtype=torch.bfloat16, device=Dc.device)
+    else:
+        _dense(dW, "dW", torch.bfloat16, shape)
+    _call(dev, "qf_gemm_fp8_wgrad", Dc.data_ptr(), Ds.data_ptr(), Xc.data_ptr(), Xs.data_ptr(),
+          None if plan is None else plan.offsets.data_ptr(), n_ids, rows, dW.data_ptr(), N, K)
+    return dW
 
 
 # ------------------------------------- adapters of many requests at once ----

@@ -156,6 +156,27 @@ SIGNATURES = {
     "qf_row_plan_tiles": (c_i64, [c_i64, c_int]),
     "qf_row_plan_workspace": (c_size_t, [c_i64, c_int]),
     "qf_row_plan": (c_int, [c_void_p, c_i64, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qf_row_plan_positions": (c_int, [c_void_p, c_i64, c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                      c_void_p]),
+    "qf_moe_dispatch": (c_int, [c_void_p, c_i64, c_i64, c_void_p, c_i64, c_i64, c_void_p, c_i64, c_void_p]),
+    "qf_moe_combine": (c_int, [c_void_p, c_i64, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_void_p, c_i64, c_void_p]),
+    "qf_moe_combine_backward": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_void_p,
+                                        c_i64, c_void_p, c_void_p]),
+    "qf_quant_fp8": (c_int, [c_void_p, c_i64, c_i64, c_i64, c_void_p, c_i64, c_void_p, c_void_p, c_i64, c_void_p, c_i64,
+                             c_void_p]),
+    "qf_fp8_panels": (c_i64, [c_i64, c_int]),
+    "qf_quant_fp8_panels": (c_int, [c_void_p, c_i64, c_i64, c_i64, c_void_p, c_i64, c_void_p, c_int, c_void_p, c_void_p,
+                                    c_void_p]),
+    "qf_quant_fp8_tiles": (c_int, [c_void_p, c_i64, c_i64, c_i64, c_i64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "qf_swiglu_quant_fp8": (c_int, [c_void_p, c_i64, c_i64, c_i64, c_void_p, c_void_p, c_i64, c_void_p, c_i64, c_void_p,
+                                    c_i64, c_void_p]),
+    "qf_swiglu_backward": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_i64, c_i64, c_void_p, c_void_p, c_i64, c_void_p]),
+    "qf_gemm_fp8": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_void_p, c_i64, c_i64, c_i64, c_i64,
+                            c_void_p]),
+    "qf_gemm_fp8_grouped": (c_int, [c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_void_p, c_void_p, c_int,
+                                    c_void_p, c_i64, c_i64, c_i64, c_i64, c_void_p]),
+    "qf_gemm_fp8_wgrad": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_i64, c_void_p,
+                                  c_i64, c_i64, c_void_p]),
     "qf_lora_apply_workspace": (c_size_t, [c_i64, c_i64, c_int, c_int, c_int]),
     "qf_lora_apply": (c_int, [c_void_p, c_i64, c_i64, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_i64,
                               c_i64, c_i64, c_i64, c_int, c_void_p, c_size_t, c_void_p]),

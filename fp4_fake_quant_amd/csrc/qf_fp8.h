@@ -1,0 +1,107 @@
+// What the 8-bit operators share: E4M3 blocks of 128 with an fp32 scale, and the place of a unit of
+// rows among the groups of a row plan.
+#pragma once
+#include "qf_device.h"
+#include "qf_kernels.h"
+
+namespace qf {
+
+constexpr int FB = QF_FP8_BLOCK;
+constexpr float F8_TOP = 448.0f;                  // largest E4M3 value
+constexpr float F8_LIVE = 0x1p-100f;              // blocks below are all zero: 448 / amax must stay finite
+
+// Scale of a block whose largest magnitude has the fp32 bits `top`, and the factor of its codes.
+// A block with a NaN or an infinity gets a NaN scale, which whatever reads the block then is.
+struct F8Scale {
+  float scale, inv;
+};
+__device__ __forceinline__ F8Scale f8_scale(uint32_t top) {
+  const float a = __uint_as_float(top);
+  const bool live = a >= F8_LIVE;
+  F8Scale o = {live ? a / F8_TOP : 0.0f, live ? F8_TOP / a : 0.0f};
+  if (top >= 0x7F800000u) o.scale = __uint_as_float(0x7FC00000u);
+  return o;
+}
+
+// Four codes of y[0..3] (already times inv): round to nearest even (v_cvt_pk_fp8_f32), at most 448.
+__device__ __forceinline__ float f8_clamp(float y) { return __builtin_amdgcn_fmed3f(y, -F8_TOP, F8_TOP); }
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(f8_clamp(a), f8_clamp(b), 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(f8_clamp(c), f8_clamp(d), v, true);
+  return (uint32_t)v;
+}
+
+// Unit `u` of the groups' rows, each group cut into units of `unit` rows from its own first row:
+// the group (-1: there are fewer units), the unit's first position, its rows, its index in the group.
+struct GroupUnit {
+  int group, first, rows, index;
+};
+
+// The sum of v over the lanes below this one, and over all.
+__device__ __forceinline__ uint32_t wave_before(uint32_t v, uint32_t* total) {
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(x, d);
+    if (lane >= (uint32_t)d) x += y;
+  }
+  *total = __shfl(x, 63);
+  return x - v;
+}
+// Offset i of the plan, inside [0, n].
+__device__ __forceinline__ int group_offset(const int32_t* offsets, int i, int n) {
+  const int v = offsets[i];
+  return v < 0 ? 0 : v > n ? n : v;
+}
+__device__ __forceinline__ uint32_t units_of(int lo, int hi, int unit) {
+  return hi > lo ? (uint32_t)(hi - lo + unit - 1) / (uint32_t)unit : 0u;
+}
+// Called by whole waves; every wave finds it for itself.  Up to 64 groups a pass; more take a first
+// pass over runs of groups.
+__device__ __forceinline__ GroupUnit find_unit(const int32_t* offsets, int n_ids, int n, int unit, uint32_t u) {
+  const int lane = threadIdx.x & 63;
+  const int per = (n_ids + 63) / 64;             // groups per lane, 1..16
+  int g0 = 0;                                    // first group of the run that holds the unit
+  uint32_t total, left = u;
+  if (per > 1) {
+    uint32_t mine = 0;
+    int lo = group_offset(offsets, min(lane * per, n_ids), n);
+    for (int j = 0; j < per; ++j) {
+      const int hi = group_offset(offsets, min(lane * per + j + 1, n_ids), n);
+      mine += units_of(lo, hi, unit);
+      lo = hi;
+    }
+    const uint32_t before = wave_before(mine, &total);
+    const uint64_t hit = __ballot(u >= before && u - before < mine);
+    if (!hit) return GroupUnit{-1, 0, 0, 0};
+    const int at = __ffsll((unsigned long long)hit) - 1;
+    g0 = at * per;
+    left = u - (uint32_t)__builtin_amdgcn_readlane((int)before, at);
+  }
+  const int g = g0 + lane;
+  const bool in = lane < per * (per > 1 ? 1 : 64) && g < n_ids;
+  const int lo = in ? group_offset(offsets, g, n) : 0, hi = in ? group_offset(offsets, g + 1, n) : 0;
+  const uint32_t mine = units_of(lo, hi, unit);
+  const uint32_t before = wave_before(mine, &total);
+  const uint64_t hit = __ballot(left >= before && left - before < mine);
+  if (!hit) return GroupUnit{-1, 0, 0, 0};
+  const int at = __ffsll((unsigned long long)hit) - 1;
+  const int index = (int)(left - (uint32_t)__builtin_amdgcn_readlane((int)before, at));
+  const int first = __builtin_amdgcn_readlane(lo, at) + index * unit;
+  const int last = __builtin_amdgcn_readlane(hi, at);
+  return GroupUnit{g0 + at, first, min(unit, last - first), index};
+}
+// Units of the groups before group g.
+__device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, int n, int unit) {
+  uint32_t sum = 0, total;
+  for (int i = threadIdx.x & 63; i < g; i += 64)
+    sum += units_of(group_offset(offsets, i, n), group_offset(offsets, i + 1, n), unit);
+  wave_before(sum, &total);
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)total);
+}
+
+inline bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
+inline bool plan_sizes_ok(int64_t n, int n_ids) { return n >= 0 && n < QF_ROW_MAX_ROWS && n_ids >= 1 && n_ids <= QF_ROW_MAX_IDS; }
+
+}  // namespace qf

@@ -63,6 +63,7 @@ struct RowPlanArgs {
   int32_t n_ids;
   int32_t* offsets;        // [n_ids + 1]
   int32_t* order;          // [n]
+  int32_t* positions;      // [n], the inverse of order (null: not wanted)
   int32_t* tiles;          // [n_tiles][2]
   int64_t n_tiles;
   uint32_t* hist;          // workspace [workgroups][n_ids rounded up to even] (null: one launch)

@@ -69,15 +69,17 @@ __device__ __forceinline__ uint64_t rp_peers(uint32_t id, uint32_t n_ids, int bi
     }
   return peers;
 }
-// Writes row i at its id's next position, one per peer, in lane order.
+// Writes row i (below end where it has an id) at its id's next position, one per peer, in lane order, and
+// that position, or -1, beside the row.
 __device__ __forceinline__ void rp_place(uint32_t* next, uint32_t id, uint32_t n_ids, uint64_t peers, uint32_t lane,
-                                         int64_t i, int32_t* order) {
+                                         int64_t i, int64_t end, int32_t* order, int32_t* positions) {
   const bool in = id < n_ids;
   const uint32_t rank = __popcll(peers & ((1ull << lane) - 1ull));
   uint32_t at = 0;
   if (in && rank == 0) at = atomicAdd(&next[id], (uint32_t)__popcll(peers));
   at = __shfl(at, in ? __ffsll((unsigned long long)peers) - 1 : 0) + rank;
   if (in) order[at] = (int32_t)i;
+  if (positions && i < end) positions[i] = in ? (int32_t)at : -1;
 }
 
 // Counts rows [lo, hi) into cnt with the whole workgroup.
@@ -238,10 +240,10 @@ __global__ __launch_bounds__(RP_WG) void k_row_plan(RowPlanArgs a) {
   for (int j = 0; j < RP_HELD; ++j) peers[j] = rp_peers(held[j], n_ids, bits);
 #pragma unroll
   for (int j = 0; j < RP_HELD; ++j)
-    if (wlo + j * 64 < whi) rp_place(cnt[wave], held[j], n_ids, peers[j], lane, wlo + j * 64 + lane, a.order);
+    if (wlo + j * 64 < whi) rp_place(cnt[wave], held[j], n_ids, peers[j], lane, wlo + j * 64 + lane, whi, a.order, a.positions);
   for (int64_t i0 = wlo + RP_HELD * 64; i0 < whi; i0 += 64) {
     const uint32_t id = i0 + lane < whi ? (uint32_t)a.ids[i0 + lane] : 0xFFFFFFFFu;
-    rp_place(cnt[wave], id, n_ids, rp_peers(id, n_ids, bits), lane, i0 + lane, a.order);
+    rp_place(cnt[wave], id, n_ids, rp_peers(id, n_ids, bits), lane, i0 + lane, whi, a.order, a.positions);
   }
 
   // the rest, spread over the grid: offsets, the tile table, the unused end of order
@@ -299,13 +301,14 @@ size_t qf_row_plan_workspace(int64_t n, int n_ids) {
   return qf::row_plan_hist_bytes(n, n_ids);
 }
 
-qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
-                      void* ws, size_t ws_bytes, void* stream) {
+static qf_status row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
+                          int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
   if (n < 0 || n >= QF_ROW_MAX_ROWS) return QF_ERR_SHAPE;
   if (n_ids < 1 || n_ids > QF_ROW_MAX_IDS) return QF_ERR_ARG;
   if (!offsets || (n > 0 && (!ids || !order || !tiles))) return QF_ERR_NULL;
   const size_t need = qf_row_plan_workspace(n, n_ids);
-  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)order) % 4 || (uintptr_t)tiles % 8 || (need > 0 && (uintptr_t)ws % 8))
+  if (((uintptr_t)ids | (uintptr_t)offsets | (uintptr_t)order | (uintptr_t)positions) % 4 || (uintptr_t)tiles % 8 ||
+      (need > 0 && (uintptr_t)ws % 8))
     return QF_ERR_ALIGN;
   if (need > 0 && (!ws || ws_bytes < need)) return QF_ERR_WORKSPACE;
   qf::RowPlanArgs a;
@@ -316,9 +319,21 @@ qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets
   a.offsets = offsets;
   a.order = order;
   a.tiles = tiles;
+  a.positions = positions;
   a.n_tiles = qf_row_plan_tiles(n, n_ids);
   a.hist = (uint32_t*)ws;
   return qf::status_of(qf::launch_row_plan(a, (hipStream_t)stream));
+}
+
+qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
+                      void* ws, size_t ws_bytes, void* stream) {
+  return row_plan(ids, n, n_ids, offsets, order, tiles, nullptr, ws, ws_bytes, stream);
+}
+
+qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
+                                int32_t* positions, void* ws, size_t ws_bytes, void* stream) {
+  if (n > 0 && !positions) return QF_ERR_NULL;
+  return row_plan(ids, n, n_ids, offsets, order, tiles, positions, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -466,6 +466,39 @@ size_t qf_row_plan_workspace(int64_t n, int n_ids);
 qf_status qf_row_plan(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
                       void* ws, size_t ws_bytes, void* stream);
 
+/* The same with the inverse: positions device int32[n], positions[order[p]] = p, -1 for a row
+ * in no group.  What takes rows back out of their groups' order reads it (qf_moe_combine). */
+qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_t* offsets, int32_t* order, int32_t* tiles,
+                                int32_t* positions, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------- rows into expert order and back ---- */
+/* Tokens and experts: row i = t * k + j of a plan stands for expert j of token t (the ids that
+ * qf_moe_route writes), position p of the plan for row order[p].  bf16 matrices with rows of H:
+ *   dispatch           out[p] = X[order[p] / rows_per_x]
+ *   combine            Y[t] = sum_j weights[t, j] R[positions[t k + j]]
+ *   combine_backward   dR[p] = weights[t, j] dY[t] for p = positions[t k + j];
+ *                      dW[t, j] = <R[p], dY[t]>
+ * combine without weights (NULL: all 1) is the gradient of dispatch.  An order entry outside [0, n)
+ * (behind the last group) leaves its row of out as it was, likewise rows of dR that no position
+ * names; a positions entry outside [0, tokens * k) adds nothing to Y, whatever its weight, and gets
+ * dW 0.  positions must name no row twice (a plan's do not).  Sums in fp32, j (dW: the columns) in a fixed order, one rounding to bf16:
+ *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) gamma_k sum_j |w| |r|;  |dr - w dy| <= (2^-8 + 2^-24) |w dy|;
+ *   |dw - dw_exact| <= gamma_H sum |r| |dy|;  gamma_n = n 2^-24 / (1 - n 2^-24).
+ * Values that are NaN or infinite follow the formulas.  dR or dW may be NULL to skip it (R is
+ * not read without dW).
+ * Limits: H a positive multiple of 8 below QF_MOE_MAX_COLS, leading dimensions >= H, n and
+ * tokens * k in [0, QF_ROW_MAX_ROWS) (QF_ERR_SHAPE); rows_per_x >= 1, k >= 1 (QF_ERR_ARG); matrices
+ * 16-byte aligned, leading dimensions multiples of 8 (QF_ERR_ALIGN).  X has ceil(n / rows_per_x)
+ * rows, R and dR tokens * k.  Outputs must not overlap inputs.  One launch, no workspace. */
+#define QF_MOE_MAX_COLS (1 << 22)
+qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const int32_t* order, int64_t n, int64_t H,
+                          uint16_t* out, int64_t ldo, void* stream);
+qf_status qf_moe_combine(const uint16_t* R, int64_t ldr, const int32_t* positions, const float* weights, int64_t tokens,
+                         int64_t k, int64_t H, uint16_t* Y, int64_t ldy, void* stream);
+qf_status qf_moe_combine_backward(const uint16_t* dY, int64_t lddy, const uint16_t* R, int64_t ldr, const int32_t* positions,
+                                  const float* weights, int64_t tokens, int64_t k, int64_t H, uint16_t* dR, int64_t lddr,
+                                  float* dW, void* stream);
+
 /* -------------------------------------- adapters of many requests at once ---- */
 /* Y[i] += scale[e] * B_e (A_e X[i / rows_per_x]) for every row i of Y, e the adapter of row
  * i: the unmerged adapters beside a projection that all rows share (a rollout batch whose
@@ -680,6 +713,85 @@ qf_status qf_gemm_mxfp4_packed(const uint8_t* Xc, const uint8_t* Xs, const uint8
 qf_status qf_gemm_nvfp4(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
                         uint16_t* Y, int64_t ldy, int64_t M, int64_t N, int64_t K,
                         unsigned flags, const float* d_scale_x, const float* d_scale_w, void* stream);
+
+/* ------------------------------------------------ 8-bit blocks of 128 ---- */
+/* E4M3 codes (the "FN" form: no infinity, largest value 448) with one fp32 scale per block of
+ * QF_FP8_BLOCK elements, for products in 8 bits beside the 4-bit grids: activations in blocks along
+ * a row, weights in square tiles, both operands of a weight gradient in blocks along the rows.
+ * Per block, with a the largest |x|:
+ *   scale = fl(a / 448);  code = E4M3(min(max(fl(x fl(448 / a)), -448), 448)), ties to even;
+ * a block with a < 2^-100 gets scale 0 and codes of zeros (448 / a must stay in range); a block with
+ * a NaN or an infinity gets scale NaN, so that whatever is made of it is NaN too, and unspecified codes.
+ *
+ * qf_quant_fp8         rows: codes [rows][ldc], block b of row p: columns 128 b ..; its scale is
+ *   scales[b * lds + p] (block-major: the product reads one block's scales of many rows at a time).
+ *   order NULL: row p of x.  Else row order[p] / rows_per_x of x (a plan's order: rows into expert
+ *   order on the way); an entry outside [0, rows) leaves row p's codes and scales as they were.  d_rows (device int32, or NULL;
+ *   e.g. a plan's offsets + n_ids): rows at and past *d_rows are left as they were.  cols a multiple of 16.
+ * qf_quant_fp8_panels  blocks of 128 rows of one group, transposed: codes [panels][cols][128], scales
+ *   [panels][cols].  offsets (a plan's, n_ids groups) cut the rows into groups, each starts a panel
+ *   of its own and the last one of a group is filled up with code 0; offsets NULL (n_ids 1): one group of
+ *   all rows.  order, rows_per_x as above (an entry outside [0, rows) counts as a row of zeros).
+ *   qf_fp8_panels(rows, n_ids) panels always suffice; those behind the last are left as they were.  cols a multiple of 8.
+ * qf_quant_fp8_tiles   128 x 128 tiles of count stacked matrices x [count][rows][ldx]: codes
+ *   [count][rows][cols], scales [count][ceil(rows / 128)][ceil(cols / 128)], and the transpose, of
+ *   the same values: codes_t [count][cols][rows], scales_t [count][ceil(cols / 128)][ceil(rows / 128)]
+ *   (each pair may be NULL, not both).  cols a multiple of 16, rows too with codes_t; count <= QF_ROW_MAX_IDS.
+ * qf_swiglu_quant_fp8  a = u g / (1 + exp(-g)) of h [rows, 2 cols] = [g, u] (a fused gate/up product), codes
+ *   and scales of a (held in fp32, not rounded in between) as qf_quant_fp8 lays them out; y: a in bf16 as well, or NULL.
+ *   Error of a before rounding at most 16 2^-24 |a| + 2^-119 |u|.
+ * qf_swiglu_backward   dh [rows, 2 cols] = [da u s (1 + g (1 - s)), da g s], s = 1 / (1 + exp(-g)), bf16,
+ *   fp32 arithmetic: error at most 2^-8 of the value plus 32 2^-24 |da u| (1 + |g|) or |da g|.
+ * Limits: rows in [0, QF_ROW_MAX_ROWS) (tiles: below QF_FP8_MAX_COLS), cols in [1, QF_FP8_MAX_COLS), leading
+ * dimensions at least the row length, lds >= rows (QF_ERR_SHAPE); rows_per_x >= 1 with order, n_ids in
+ * 1..QF_ROW_MAX_IDS (QF_ERR_ARG); bf16 arrays 16-byte aligned with leading dimensions multiples of 8, codes 16-byte aligned with
+ * ldc a multiple of 16 (QF_ERR_ALIGN).  Outputs must not overlap inputs.  One launch, no workspace. */
+#define QF_FP8_BLOCK 128
+#define QF_FP8_MAX_COLS (1 << 22)
+qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* order, int64_t rows_per_x,
+                       const int32_t* d_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream);
+int64_t qf_fp8_panels(int64_t rows, int n_ids);           /* 0 for invalid arguments */
+qf_status qf_quant_fp8_panels(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* order,
+                              int64_t rows_per_x, const int32_t* offsets, int n_ids, uint8_t* codes, float* scales,
+                              void* stream);
+qf_status qf_quant_fp8_tiles(const uint16_t* x, int64_t ldx, int64_t count, int64_t rows, int64_t cols, uint8_t* codes,
+                             float* scales, uint8_t* codes_t, float* scales_t, void* stream);
+qf_status qf_swiglu_quant_fp8(const uint16_t* h, int64_t ldh, int64_t rows, int64_t cols, const int32_t* d_rows,
+                              uint8_t* codes, int64_t ldc, float* scales, int64_t lds, uint16_t* y, int64_t ldy,
+                              void* stream);
+qf_status qf_swiglu_backward(const uint16_t* h, int64_t ldh, const uint16_t* da, int64_t ldda, int64_t rows, int64_t cols,
+                             const int32_t* d_rows, uint16_t* dh, int64_t lddh, void* stream);
+
+/* Products of these operands on the FP8 matrix cores, bf16 results:
+ *   qf_gemm_fp8          Y[m, n] = sum_b Xs[b, m] Ws[n / 128, b] sum_(k in block b) X[m, k] W[n, k], [M, ldy]; X as
+ *                        qf_quant_fp8 lays it out (Xs [ceil(K / 128)][ldxs]), W [N, ldw] as qf_quant_fp8_tiles.
+ *   qf_gemm_fp8_grouped  the same for a plan's rows: Y[p] = X[p] W[e]^T for the positions p of group e, W [n_ids][N][ldw]
+ *                        and its scales stacked.  Rows behind the last group are left as they were.
+ *   qf_gemm_fp8_wgrad    dW[e][n, k] = sum over the panels b of group e of Ds[b, n] Xs[b, k] sum_r D[b, n, r] X[b, k, r]:
+ *                        the gradient of the grouped product's weights from the panels of dY (D, N columns) and of X
+ *                        (K columns) under the same plan.  dW [n_ids][N][K] contiguous; a group without rows gets
+ *                        zeros.  offsets NULL (n_ids 1): one group of all rows.  qf_adamw_step takes dW as it is,
+ *                        qf_ste_backward adds it to an fp32 gradient.
+ * The gradient of the rows is the forward product with W's transpose (codes_t, scales_t).
+ * Accuracy: the cores align the products of a group of eight to the largest exponent E among them and drop what lies
+ * below 2^(E - 13); the groups and then the blocks are summed in fp32.  So
+ *   |y - y_ref| <= 2^-8 |y_ref| + (1 + 2^-8) (2^-10 + gamma_(2 L + 4 B + 64)) P,
+ * L the reduction length, B its blocks, P the sum of the terms' magnitudes with codes below 2^-6 counted as 2^-6 (about
+ * 2^-19 P is typical).  Same inputs, same bits.  A NaN scale spoils the rows or tiles that it belongs to and no others;
+ * so does a NaN code (0x7F, 0xFF) its row.
+ * Limits: M and rows in [0, QF_ROW_MAX_ROWS), N in [0, 2^22), K a positive multiple of 16 below QF_FP8_MAX_COLS, ldx,
+ * ldw >= K and below QF_FP8_MAX_COLS, ldxs >= M, ldy >= N (wgrad: N and K multiples of 8 in [0, 2^22)), at most 2^22
+ * tiles of 128 x 128 outputs (QF_ERR_SHAPE); n_ids in 1..QF_ROW_MAX_IDS (QF_ERR_ARG); codes 16-byte aligned with ldx, ldw
+ * multiples of 16, Y 2-byte, dW 16-byte, tiles 8-byte aligned (QF_ERR_ALIGN); fastest with Y 16-byte aligned and N, ldy
+ * multiples of 8.  offsets, tiles: of a qf_row_plan of exactly `rows` rows.  Y must not overlap an operand.  One launch,
+ * no workspace. */
+qf_status qf_gemm_fp8(const uint8_t* Xc, int64_t ldx, const float* Xs, int64_t ldxs, const uint8_t* Wc, int64_t ldw,
+                      const float* Ws, uint16_t* Y, int64_t ldy, int64_t M, int64_t N, int64_t K, void* stream);
+qf_status qf_gemm_fp8_grouped(const uint8_t* Xc, int64_t ldx, const float* Xs, int64_t ldxs, const uint8_t* Wc, int64_t ldw,
+                              const float* Ws, const int32_t* offsets, const int32_t* tiles, int n_ids, uint16_t* Y,
+                              int64_t ldy, int64_t rows, int64_t N, int64_t K, void* stream);
+qf_status qf_gemm_fp8_wgrad(const uint8_t* Dc, const float* Ds, const uint8_t* Xc, const float* Xs, const int32_t* offsets,
+                            int n_ids, int64_t rows, uint16_t* dW, int64_t N, int64_t K, void* stream);
 
 /* ---------------------------------------- forward of the quantized linear ---- */
 /* Y = QDQ(X) . QDQ(W)^T, the product of qf_gemm_mxfp4 / qf_gemm_nvfp4, in two passes

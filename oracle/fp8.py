@@ -1,0 +1,195 @@
+"""8-bit blocks of 128, their products, the gated activation, and rows into expert order and back
+(CPU oracle, numpy; products and activations in float64).
+
+Pins: the codes against a search over all 256 E4M3 values and torch's cast, the panels and tiles
+against row blocks of transposed slices, gradients against differences.
+"""
+
+import numpy as np
+
+B = 128
+LIVE = np.float32(2.0 ** -100)
+
+
+def e4m3_values():
+    """Value of every code (NaN for 0x7F and 0xFF)."""
+    c = np.arange(256)
+    e, m = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, m * 2.0 ** -9, (8 + m) * 2.0 ** (e - 10.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return np.where(c >= 128, -v, v)
+
+
+VALUES = e4m3_values()
+
+
+def encode(y):
+    """Codes of float32 y, |y| <= 448 after clamping, nearest value, ties to the even code."""
+    y = np.clip(np.asarray(y, np.float32), -448, 448).astype(np.float64)
+    a = np.abs(y)
+    grid = VALUES[:127]
+    hi = np.searchsorted(grid, a)                     # first value at or above
+    lo = np.maximum(hi - 1, 0)
+    up = (grid[hi] - a < a - grid[lo]) | ((grid[hi] - a == a - grid[lo]) & (hi % 2 == 0))
+    return (np.where(up, hi, lo) + np.where(np.signbit(y), 128, 0)).astype(np.uint8)
+
+
+def scale_of(a):
+    """(scale, factor of the codes) of blocks with the largest magnitudes a (float32)."""
+    a = np.asarray(a, np.float32)
+    live = a >= LIVE
+    safe = np.where(live, a, np.float32(1))
+    return np.where(live, safe / np.float32(448), np.float32(0)), np.where(live, np.float32(448) / safe, np.float32(0))
+
+
+def blocks_of(n):
+    return (n + B - 1) // B
+
+
+def quant_rows(x):
+    """codes [rows, cols], scales [blocks, rows] of float32 x."""
+    x = np.asarray(x, np.float32)
+    codes = np.zeros(x.shape, np.uint8)
+    scales = np.zeros((blocks_of(x.shape[1]), x.shape[0]), np.float32)
+    for b in range(scales.shape[0]):
+        part = x[:, b * B:(b + 1) * B]
+        scales[b], inv = scale_of(np.abs(part).max(1, initial=0))
+        codes[:, b * B:(b + 1) * B] = encode(part * inv[:, None])
+    return codes, scales
+
+
+def panel_blocks(offsets):
+    """(group, first row, rows) of every panel, in order."""
+    out = []
+    for e in range(len(offsets) - 1):
+        for r in range(offsets[e], offsets[e + 1], B):
+            out.append((e, r, min(B, offsets[e + 1] - r)))
+    return out
+
+
+def quant_panels(x, offsets):
+    """codes [panels, cols, 128], scales [panels, cols] of x's rows in groups."""
+    blocks = panel_blocks(offsets)
+    codes = np.zeros((len(blocks), x.shape[1], B), np.uint8)
+    scales = np.zeros((len(blocks), x.shape[1]), np.float32)
+    for i, (_, r, n) in enumerate(blocks):
+        c, s = quant_rows(np.ascontiguousarray(x[r:r + n].T))
+        codes[i, :, :n], scales[i] = c, s[0]
+    return codes, scales
+
+
+def quant_tiles(x):
+    """codes of x's shape and scales [row tiles, col tiles]."""
+    x = np.asarray(x, np.float32)
+    codes = np.zeros(x.shape, np.uint8)
+    scales = np.zeros((blocks_of(x.shape[0]), blocks_of(x.shape[1])), np.float32)
+    for i in range(scales.shape[0]):
+        for j in range(scales.shape[1]):
+            part = x[i * B:(i + 1) * B, j * B:(j + 1) * B]
+            scales[i, j], inv = scale_of(np.abs(part).max(initial=0))
+            codes[i * B:(i + 1) * B, j * B:(j + 1) * B] = encode(part * inv)
+    return codes, scales
+
+
+def dequant_rows(codes, scales):
+    return VALUES[codes] * np.repeat(scales.T.astype(np.float64), B, 1)[:, :codes.shape[1]]
+
+
+def dequant_tiles(codes, scales):
+    s = np.repeat(np.repeat(scales.astype(np.float64), B, 0)[:codes.shape[0]], B, 1)[:, :codes.shape[1]]
+    return VALUES[codes] * s
+
+
+def dequant_panels(codes, scales):
+    """[panels, 128, cols]"""
+    return (VALUES[codes] * scales.astype(np.float64)[:, :, None]).transpose(0, 2, 1)
+
+
+def magnitudes(codes):
+    """|values| of codes, those below 2^-6 counted as 2^-6: what the matrix cores align products by."""
+    return np.maximum(np.abs(VALUES[codes]), 2.0 ** -6)
+
+
+def rows_magnitudes(codes, scales):
+    return magnitudes(codes) * np.repeat(scales.T.astype(np.float64), B, 1)[:, :codes.shape[1]]
+
+
+def tiles_magnitudes(codes, scales):
+    s = np.repeat(np.repeat(scales.astype(np.float64), B, 0)[:codes.shape[0]], B, 1)[:, :codes.shape[1]]
+    return magnitudes(codes) * s
+
+
+def panels_magnitudes(codes, scales):
+    return (magnitudes(codes) * scales.astype(np.float64)[:, :, None]).transpose(0, 2, 1)
+
+
+def product(xc, xs, wc, ws):
+    """(x w^T, sum of the terms' magnitudes) of row-scaled and tile-scaled operands."""
+    return (dequant_rows(xc, xs) @ dequant_tiles(wc, ws).T, rows_magnitudes(xc, xs) @ tiles_magnitudes(wc, ws).T)
+
+
+def gamma(n):
+    return n * 2.0 ** -24 / (1 - n * 2.0 ** -24)
+
+
+def product_bound(y, P, L):
+    """The stated bound of a product over L elements.  Eight products at a time lose at most 2^(E - 13)
+    each, 2^E at most the largest of their magnitudes (with codes below 2^-6 counted as 2^-6, as their
+    exponent is that of 2^-6), so at most 8 2^-13 of the largest and 2^-10 of the eight's sum."""
+    return 2.0 ** -8 * np.abs(y) + (1 + 2.0 ** -8) * (2.0 ** -10 + gamma(2 * L + 4 * blocks_of(L) + 64)) * P
+
+
+def swiglu(h):
+    """u g sigmoid(g) of h = [g, u] in float64."""
+    h = np.asarray(h, np.float64)
+    n = h.shape[1] // 2
+    g, u = h[:, :n], h[:, n:]
+    return u * g * sigmoid(g)
+
+
+def sigmoid(g):
+    e = np.exp(-np.abs(g))
+    return np.where(g >= 0, 1 / (1 + e), e / (1 + e))
+
+
+def swiglu_backward(h, da):
+    h, da = np.asarray(h, np.float64), np.asarray(da, np.float64)
+    n = h.shape[1] // 2
+    g, u = h[:, :n], h[:, n:]
+    s = sigmoid(g)
+    return np.concatenate([da * u * s * (1 + g * (1 - s)), da * g * s], 1)
+
+
+def positions(order):
+    """The inverse of a plan's order."""
+    pos = np.full(order.size, -1, np.int32)
+    at = np.flatnonzero(order >= 0)
+    pos[order[at]] = at
+    return pos
+
+
+def combine(R, pos, w):
+    """(Y, magnitudes of its terms) in float64; w [tokens, k]."""
+    T, k = w.shape
+    Y, P = np.zeros((T, R.shape[1])), np.zeros((T, R.shape[1]))
+    for t in range(T):
+        for j in range(k):
+            p = pos[t * k + j]
+            if p >= 0:
+                Y[t] += float(w[t, j]) * R[p].astype(np.float64)
+                P[t] += abs(float(w[t, j])) * np.abs(R[p].astype(np.float64))
+    return Y, P
+
+
+def combine_backward(dY, R, pos, w):
+    """(dR, dW, magnitudes of dW's terms); rows that no position names are zero."""
+    T, k = w.shape
+    dR, dW, P = np.zeros(R.shape), np.zeros((T, k)), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            p = pos[t * k + j]
+            if p >= 0:
+                d, r = dY[t].astype(np.float64), R[p].astype(np.float64)
+                dR[p] = float(w[t, j]) * d
+                dW[t, j], P[t, j] = d @ r, np.abs(d) @ np.abs(r)
+    return dR, dW, P
