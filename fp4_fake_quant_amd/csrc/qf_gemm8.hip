@@ -23,7 +23,8 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int64_t G8_MAX_WGS = 1 << 22;
+constexpr int64_t G8_MAX_TILES = 1 << 22;
+constexpr int G8_RUN = 4;                // tile rows that share their columns' w in a cache
 
 // An operand: rows of `row` bytes pitch, blocks of 128 at `blk` bytes pitch.
 struct Gemm8Args {
@@ -39,6 +40,7 @@ struct Gemm8Args {
   int32_t M, N, K;                       // K: elements of a row-major row (panels: 0, every block whole)
   int32_t blocks;                        // blocks of the reduction (grouped over blocks: from the offsets)
   int32_t tiles_m, tiles_n;
+  int32_t y_vec;                         // y takes stores of 8 bytes
 };
 enum { G8_DENSE, G8_ROWS, G8_BLOCKS };   // over what the groups go
 
@@ -47,102 +49,183 @@ __device__ __forceinline__ f32x4_t mfma_f8(i32x8_t a, i32x8_t b, f32x4_t c) {
 }
 
 // ------------------------------------------------------------------ tiles ---
-// 128 x 128 outputs by 4 waves of 64 x 64.
-template <int MODE>
-__global__ __launch_bounds__(256) void k_gemm8(Gemm8Args a) {
-  constexpr int BM = 128, BN = 128, TM = 4, TN = 4;
+// BM x BN outputs by WM x WN waves of 16 TM x 16 TN each.  A step is one block of 128: its codes go from
+// memory straight into LDS (buffer loads that write LDS, 16 bytes a lane: a wave's instruction fills
+// eight rows of 128 bytes), with the block's scales of the tile's rows behind them.  Two stages: while
+// one is computed from, the next is on its way, and its place is refilled as soon as every wave has read
+// its last fragments.
+template <int BM, int BN>
+struct Stage {
+  static constexpr int W = BM * FB, XS = W + BN * FB, WS = XS + BM * 4, BYTES = WS + BN * 4;
+};
+// The 16-byte chunk c of a row lies at c ^ (row / 2) % 8, so that 16 lanes reading one chunk of 16 rows meet
+// 16 different places of 256 bytes.
+__device__ __forceinline__ uint32_t g8_chunk(uint32_t row, uint32_t c) { return row * FB + ((c ^ ((row >> 1) & 7u)) << 4); }
+
+// Waits until at most n vector-memory operations of this wave are in flight, and for its LDS reads.
+#define G8_WAIT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (0 << 8))
+// Workgroup barrier that leaves loads in flight (a __syncthreads() would wait for all); the empty asm
+// keeps the compiler from moving LDS accesses across it.
+#define G8_BARRIER()                 \
+  do {                               \
+    asm volatile("" ::: "memory");   \
+    __builtin_amdgcn_s_barrier();    \
+    asm volatile("" ::: "memory");   \
+  } while (0)
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+template <int MODE, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
+  constexpr int WAVES = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr bool WROWS = MODE == G8_BLOCKS;                  // w has a scale per row and block
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int XW = BM / 8 / WAVES, WW = BN / 8 / WAVES;    // LDS windows (eight rows) that a wave fills per step
+  constexpr int LOADS = XW + WW + 1;
+  static_assert(BM / 64 + BN / 64 == WAVES, "one window of 64 scales per wave");
+  using S = Stage<BM, BN>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::BYTES];
+
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t frow = lane & 15, fk = lane >> 4;
-  const int tn = blockIdx.x % a.tiles_n;
-  int tm = blockIdx.x / a.tiles_n;
-  int m0, rows, group = 0, block0 = 0, blocks = a.blocks;
+  // workgroups go round the XCDs: each XCD takes a run of tiles
+  const uint32_t total = gridDim.x, xcd = blockIdx.x & 7;
+  uint32_t t = xcd * (total >> 3) + min(xcd, total & 7u) + (blockIdx.x >> 3);
+  int group = 0, block0 = 0, blocks = a.blocks;
+  if (MODE == G8_BLOCKS) {
+    group = (int)(t / (uint32_t)(a.tiles_m * a.tiles_n));
+    t -= (uint32_t)group * (uint32_t)(a.tiles_m * a.tiles_n);
+    if (a.offsets) {
+      block0 = (int)units_before(a.offsets, group, a.n, FB);
+      blocks = (int)units_of(group_offset(a.offsets, group, a.n), group_offset(a.offsets, group + 1, a.n), FB);
+    }
+  }
+  // tiles in runs of G8_RUN tile rows, column by column
+  const uint32_t run = t / (uint32_t)(G8_RUN * a.tiles_n), in_run = t - run * (uint32_t)(G8_RUN * a.tiles_n);
+  const uint32_t deep = min((uint32_t)a.tiles_m - run * G8_RUN, (uint32_t)G8_RUN);
+  const int tm = (int)(run * G8_RUN + in_run % deep), tn = (int)(in_run / deep);
+  int m0 = tm * BM, rows = min(BM, a.M - m0);
   if (MODE == G8_ROWS) {
     const GroupUnit g = find_unit(a.offsets, a.n_ids, a.n, BM, (uint32_t)tm);
     if (g.group < 0) return;
     group = g.group;
     m0 = g.first;
     rows = g.rows;
-  } else {
-    if (MODE == G8_BLOCKS) {
-      group = tm / a.tiles_m;
-      tm -= group * a.tiles_m;
-      if (a.offsets) {
-        block0 = (int)units_before(a.offsets, group, a.n, FB);
-        blocks = (int)units_of(group_offset(a.offsets, group, a.n), group_offset(a.offsets, group + 1, a.n), FB);
-      }
-    }
-    m0 = tm * BM;
-    rows = min(BM, a.M - m0);
   }
   const int n0 = tn * BN, cols = min(BN, a.N - n0);
-  const uint32_t wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const uint32_t wm = wave / WN, wn = wave % WN;
   const uint8_t* x = a.x + (int64_t)m0 * a.x_row + (int64_t)block0 * a.x_blk;
   const uint8_t* w = a.w + (int64_t)group * (WROWS ? 0 : a.w_group) + (int64_t)n0 * a.w_row + (int64_t)block0 * a.w_blk;
   const float* xs = a.xs + m0 + (int64_t)block0 * a.xs_blk;
-  const float* ws = WROWS ? a.ws + n0 + (int64_t)block0 * a.ws_blk : a.ws + (int64_t)group * a.ws_group + (n0 / FB) * a.ws_tile;
+  const float* ws = WROWS ? a.ws + n0 + (int64_t)block0 * a.ws_blk
+                          : a.ws + (int64_t)group * a.ws_group + (int64_t)(n0 / FB) * a.ws_tile;
+
+  // the lane's place in window i of its wave: row lane / 8 of its eight, chunk (lane % 8) ^ swizzle, which
+  // goes by the parity of the window
+  static_assert(XW % 2 == 0 && WW % 2 == 0, "the parity of a window is that of its index in the wave");
+  const uint32_t xrow = (8 * XW * wave + (lane >> 3)) * (uint32_t)a.x_row, wrow = (8 * WW * wave + (lane >> 3)) * (uint32_t)a.w_row;
+  const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;      // even windows; odd ones: chunk ^ 64
+  // scales: wave i fills window i of 64 of the BM + BN words behind the codes: x's rows, then w's rows, or
+  // w's tiles (in the first of these windows alone)
+  const bool for_x = wave < BM / 64;
+  const uint32_t sr = for_x ? 64 * wave : 64 * wave - BM;
+  const float* sbase = for_x ? xs : ws;
+  const int64_t sstep = for_x ? a.xs_blk : a.ws_blk;
+  const int64_t sbytes = for_x ? (int64_t)rows * 4 : WROWS ? (int64_t)cols * 4 : ((int64_t)((cols - 1) / FB) * a.ws_tile + 1) * 4;
+  const uint32_t soff = for_x || WROWS ? (sr + lane) * 4 : sr == 0 && lane < BN / FB ? lane * (uint32_t)a.ws_tile * 4 : BUF_OOR;
+  // a row of a row-major operand ends at K, inside the last block; what lies behind must read as zeros
+  const int klen = WROWS ? FB : a.K;
+  auto issue = [&](int b, uint8_t* st) {
+    const int64_t bx = (int64_t)b * a.x_blk, bw = (int64_t)b * a.w_blk;
+    const uint32_t left = WROWS ? (uint32_t)FB : (uint32_t)(a.K - b * FB);
+    const __amdgpu_buffer_rsrc_t rx = make_buf(x + bx, (int64_t)(rows - 1) * a.x_row + klen - (WROWS ? 0 : bx));
+    const __amdgpu_buffer_rsrc_t rw = make_buf(w + bw, (int64_t)(cols - 1) * a.w_row + klen - (WROWS ? 0 : bw));
+    const __amdgpu_buffer_rsrc_t rs = make_buf(sbase + (int64_t)b * sstep, sbytes);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(st + S::XS + wave * 256), 4, soff, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < XW; ++i) {
+      const uint32_t c = chunk ^ (i & 1 ? 64 : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(st + (XW * wave + i) * 1024), 16,
+                                               c < left ? xrow + c + i * 8 * (uint32_t)a.x_row : BUF_OOR, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < WW; ++i) {
+      const uint32_t c = chunk ^ (i & 1 ? 64 : 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(st + S::W + (WW * wave + i) * 1024), 16,
+                                               c < left ? wrow + c + i * 8 * (uint32_t)a.w_row : BUF_OOR, 0, 0, 0);
+    }
+  };
+  auto frag = [&](const uint8_t* base, uint32_t row) {
+    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, 2 * fk));
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, 2 * fk + 1));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
 
   f32x4_t acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-  const i32x8_t zero = {0, 0, 0, 0, 0, 0, 0, 0};
 
+  if (blocks > 0) issue(0, lds);
+  if (blocks > 0) issue(min(1, blocks - 1), lds + S::BYTES);
+#pragma unroll 1
   for (int b = 0; b < blocks; ++b) {
-    const int left = a.K ? a.K - b * FB - (int)fk * 32 : 32;     // bytes of the row from the lane's place on
-    auto load = [&](const uint8_t* p, int64_t row_pitch, int64_t blk, int row, int n) {
-      i32x8_t v = zero;
-      const uint8_t* q = p + (int64_t)row * row_pitch + (int64_t)b * blk + fk * 32;
-      if (row < n && left > 0) {
-        const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(q);
-        const i32x4_t hi = left > 16 ? *reinterpret_cast<const i32x4_t*>(q + 16) : i32x4_t{0, 0, 0, 0};
-        v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
-      return v;
-    };
-    i32x8_t fx[TM], fw[TN];
-    float sx[TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = (int)(wm + 16 * i + frow);
-      fx[i] = load(x, a.x_row, a.x_blk, r, rows);
-      sx[i] = r < rows ? xs[(int64_t)b * a.xs_blk + r] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < TN; ++j) fw[j] = load(w, a.w_row, a.w_blk, (int)(wn + 16 * j + frow), cols);
-    const float sw = WROWS ? 1.0f : ws[(int64_t)b * a.ws_blk];
+    uint8_t* st = lds + (b & 1) * S::BYTES;
+    G8_WAIT(LOADS);                                         // this step's loads have landed, the next one's may fly
+    G8_BARRIER();
+    i32x8_t fw[TN], fx[2];
+    f32x4_t swr[TN];
+    const float sw = WROWS ? 1.0f : *reinterpret_cast<const float*>(st + S::WS + (wn * TN * 16 / FB) * 4);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      f32x4_t swr = {1, 1, 1, 1};
-      if constexpr (WROWS) {
+      const uint32_t r = (wn * TN + j) * 16;
+      fw[j] = frag(st + S::W, r + frow);
+      if constexpr (WROWS) swr[j] = *reinterpret_cast<const f32x4_t*>(st + S::WS + (r + 4 * fk) * 4);
+    }
+    fx[0] = frag(st, wm * TM * 16 + frow);
+    // the products of one row of tiles, and between them the sums of the row before
+    f32x4_t p[2][TN];
+    float sp = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = (int)(wn + 16 * j + 4 * fk) + e;
-          swr[e] = r < cols ? ws[(int64_t)b * a.ws_blk + r] : 0.0f;
+    for (int i = 0; i <= TM; ++i) {
+      const float s = sp;
+      if (i < TM) sp = *reinterpret_cast<const float*>(st + S::XS + ((wm * TM + i) * 16 + frow) * 4) * sw;
+      if (i + 1 < TM) fx[(i + 1) & 1] = frag(st, (wm * TM + i + 1) * 16 + frow);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        if (i < TM) p[i & 1][j] = mfma_f8(fw[j], fx[i & 1], f32x4_t{0, 0, 0, 0});
+        if (i > 0) {
+          const f32x4_t q = p[(i - 1) & 1][j];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i - 1][j][e] = __builtin_fmaf(WROWS ? q[e] * swr[j][e] : q[e], s, acc[i - 1][j][e]);
+          asm volatile("" : "+v"(acc[i - 1][j]));            // the sum stays here, beside the next products
         }
       }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const f32x4_t p = mfma_f8(fw[j], fx[i], f32x4_t{0, 0, 0, 0});
-        const float s = sx[i] * sw;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(WROWS ? p[e] * swr[e] : p[e], s, acc[i][j][e]);
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
+    G8_WAIT(63);                                            // (LDS reads alone)
+    G8_BARRIER();                                           // every wave has read this stage
+    issue(min(b + 2, blocks - 1), st);                      // past the end: the last block again
   }
+  G8_WAIT(0);                                               // no load may still write LDS at the end
 
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int r = (int)(wm + 16 * i + frow);
+    const int r = (int)((wm * TM + i) * 16 + frow);
     if (r >= rows) continue;
+    uint16_t* y = a.y + (MODE == G8_BLOCKS ? (int64_t)group * a.y_group : 0) + (int64_t)(m0 + r) * a.ldy + n0;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const int c = (int)(wn + 16 * j + 4 * fk);
-      const int64_t at = (MODE == G8_BLOCKS ? (int64_t)group * a.y_group : 0) + (int64_t)(m0 + r) * a.ldy + n0 + c;
+      const int c = (int)((wn * TN + j) * 16 + 4 * fk);
+      const uint32_t lo = pack_bf16x2(acc[i][j][0], acc[i][j][1]), hi = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+      if (a.y_vec && c + 3 < cols) {
+        *reinterpret_cast<uint2*>(y + c) = make_uint2(lo, hi);
+      } else {
+        const uint16_t v[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (c + e < cols) a.y[at + e] = (uint16_t)pack_bf16x2(acc[i][j][e], 0.0f);
+        for (int e = 0; e < 4; ++e)
+          if (c + e < cols) y[c + e] = v[e];
       }
     }
   }
@@ -151,12 +234,27 @@ __global__ __launch_bounds__(256) void k_gemm8(Gemm8Args a) {
 bool bad_codes(int64_t K, int64_t ld) { return K < 1 || K % 16 != 0 || ld < K || ld >= QF_FP8_MAX_COLS; }
 constexpr int64_t G8_MAX_N = 1 << 22;
 
-hipError_t launch(const Gemm8Args& a, int mode, int64_t wgs, hipStream_t s) {
-  const dim3 g((unsigned)wgs);
-  if (mode == G8_DENSE) k_gemm8<G8_DENSE><<<g, 256, 0, s>>>(a);
-  else if (mode == G8_ROWS) k_gemm8<G8_ROWS><<<g, 256, 0, s>>>(a);
-  else k_gemm8<G8_BLOCKS><<<g, 256, 0, s>>>(a);
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_tiles(Gemm8Args a, int mode, hipStream_t s) {
+  a.tiles_m = (int32_t)((a.M + BM - 1) / BM + (mode == G8_ROWS ? (a.M < a.n_ids ? a.M : a.n_ids) : 0));
+  a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
+  const dim3 g((unsigned)((int64_t)a.tiles_m * a.tiles_n * (mode == G8_BLOCKS ? a.n_ids : 1))), wg(64 * WM * WN);
+  if (mode == G8_DENSE) k_gemm8<G8_DENSE, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
+  else if (mode == G8_ROWS) k_gemm8<G8_ROWS, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
+  else k_gemm8<G8_BLOCKS, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// 128 x 128 tiles of a product (of all its groups together, at most).
+int64_t small_tiles(const Gemm8Args& a, int mode) {
+  const int64_t m = (a.M + 127) / 128 + (mode == G8_ROWS ? (a.M < a.n_ids ? a.M : a.n_ids) : 0);
+  return m * ((a.N + 127) / 128) * (mode == G8_BLOCKS ? a.n_ids : 1);
+}
+
+hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
+  a.y_vec = a.ldy % 4 == 0 && (uintptr_t)a.y % 8 == 0;
+  if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
+  return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
 
 // The forward product: rows of x (all, or those of a plan's groups) against w or each group's w.
@@ -194,11 +292,9 @@ qf_status forward(const uint8_t* Xc, int64_t ldx, const float* Xs, int64_t ldxs,
   a.M = (int32_t)M;
   a.N = (int32_t)N;
   a.K = (int32_t)K;
-  a.tiles_m = (int32_t)((M + 127) / 128 + (grouped ? (M < n_ids ? M : n_ids) : 0));
-  a.tiles_n = (int32_t)((N + 127) / 128);
-  const int64_t wgs = (int64_t)a.tiles_m * a.tiles_n;
-  if (wgs > G8_MAX_WGS) return QF_ERR_SHAPE;
-  return status_of(launch(a, grouped ? G8_ROWS : G8_DENSE, wgs, s));
+  const int mode = grouped ? G8_ROWS : G8_DENSE;
+  if (small_tiles(a, mode) > G8_MAX_TILES) return QF_ERR_SHAPE;
+  return status_of(launch(a, mode, s));
 }
 
 }  // namespace
@@ -247,11 +343,8 @@ qf_status qf_gemm_fp8_wgrad(const uint8_t* Dc, const float* Ds, const uint8_t* X
   a.M = (int32_t)N;
   a.N = (int32_t)K;
   a.blocks = (int32_t)((rows + FB - 1) / FB);
-  a.tiles_m = (int32_t)((N + 127) / 128);
-  a.tiles_n = (int32_t)((K + 127) / 128);
-  const int64_t wgs = (int64_t)n_ids * a.tiles_m * a.tiles_n;
-  if (wgs > G8_MAX_WGS) return QF_ERR_SHAPE;
-  return status_of(launch(a, G8_BLOCKS, wgs, (hipStream_t)stream));
+  if (small_tiles(a, G8_BLOCKS) > G8_MAX_TILES) return QF_ERR_SHAPE;
+  return status_of(launch(a, G8_BLOCKS, (hipStream_t)stream));
 }
 
 }  // extern "C"
