@@ -155,8 +155,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
     }
   };
   auto frag = [&](const uint8_t* base, uint32_t row) {
-    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, 2 * fk));
-    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, 2 * fk + 1));
+    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, fk));
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, fk + 4));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
@@ -166,47 +166,64 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
 
-  if (blocks > 0) issue(0, lds);
-  if (blocks > 0) issue(min(1, blocks - 1), lds + S::BYTES);
-#pragma unroll 1
-  for (int b = 0; b < blocks; ++b) {
-    uint8_t* st = lds + (b & 1) * S::BYTES;
-    G8_WAIT(LOADS);                                         // this step's loads have landed, the next one's may fly
+  // Row i of the wave's tiles: its products (operands read a row earlier), and beside each the sum of the
+  // row before, whose products are done by then.  The last row of a step waits for the next stage, passes
+  // the step's one barrier (this stage is read, the next has landed), refills this stage and reads the
+  // next step's first operands, so that the matrix cores go on over the step's end.
+  if (blocks > 0) {
+    issue(0, lds);
+    issue(min(1, blocks - 1), lds + S::BYTES);
+    G8_WAIT(LOADS);
     G8_BARRIER();
     i32x8_t fw[TN], fx[2];
-    f32x4_t swr[TN];
-    const float sw = WROWS ? 1.0f : *reinterpret_cast<const float*>(st + S::WS + (wn * TN * 16 / FB) * 4);
+    f32x4_t p[TN], swr[TN];
+    auto read_w = [&](const uint8_t* st, int j) { return frag(st + S::W, (wn * TN + j) * 16 + frow); };
+    auto read_x = [&](const uint8_t* st, int i) { return frag(st, (wm * TM + i) * 16 + frow); };
+    auto read_sx = [&](const uint8_t* st, int i) { return *reinterpret_cast<const float*>(st + S::XS + ((wm * TM + i) * 16 + frow) * 4); };
+    auto read_sw = [&](const uint8_t* st) { return WROWS ? 1.0f : *reinterpret_cast<const float*>(st + S::WS + (wn * TN * 16 / FB) * 4); };
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const uint32_t r = (wn * TN + j) * 16;
-      fw[j] = frag(st + S::W, r + frow);
-      if constexpr (WROWS) swr[j] = *reinterpret_cast<const f32x4_t*>(st + S::WS + (r + 4 * fk) * 4);
+      fw[j] = read_w(lds, j);
+      p[j] = f32x4_t{0, 0, 0, 0};
+      swr[j] = f32x4_t{0, 0, 0, 0};
     }
-    fx[0] = frag(st, wm * TM * 16 + frow);
-    // the products of one row of tiles, and between them the sums of the row before
-    f32x4_t p[2][TN];
-    float sp = 0.0f;
+    fx[0] = read_x(lds, 0);
+    float sw = read_sw(lds), sx = read_sx(lds, 0), before = 0.0f;      // before: scale of the row before
+    auto add = [&](int i, int j) {
 #pragma unroll
-    for (int i = 0; i <= TM; ++i) {
-      const float s = sp;
-      if (i < TM) sp = *reinterpret_cast<const float*>(st + S::XS + ((wm * TM + i) * 16 + frow) * 4) * sw;
-      if (i + 1 < TM) fx[(i + 1) & 1] = frag(st, (wm * TM + i + 1) * 16 + frow);
+      for (int e = 0; e < 4; ++e)
+        acc[i][j][e] = __builtin_fmaf(WROWS ? p[j][e] * swr[j][e] : p[j][e], before, acc[i][j][e]);
+      asm volatile("" : "+v"(acc[i][j]));                    // the sum stays here, beside the next products
+    };
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+      uint8_t* st = lds + (b & 1) * S::BYTES;
+      const uint8_t* next = lds + (~b & 1) * S::BYTES;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        if (i < TM) p[i & 1][j] = mfma_f8(fw[j], fx[i & 1], f32x4_t{0, 0, 0, 0});
-        if (i > 0) {
-          const f32x4_t q = p[(i - 1) & 1][j];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            acc[i - 1][j][e] = __builtin_fmaf(WROWS ? q[e] * swr[j][e] : q[e], s, acc[i - 1][j][e]);
-          asm volatile("" : "+v"(acc[i - 1][j]));            // the sum stays here, beside the next products
+      for (int i = 0; i < TM; ++i) {
+        const float s = sx * sw;
+        if (i == TM - 1) {
+          G8_WAIT(0);
+          G8_BARRIER();
+          issue(min(b + 2, blocks - 1), st);                 // past the end: the last block again
         }
+        fx[(i + 1) & 1] = i + 1 < TM ? read_x(st, i + 1) : read_x(next, 0);
+        sx = i + 1 < TM ? read_sx(st, i + 1) : read_sx(next, 0);
+        if (i == TM - 1) sw = read_sw(next);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          add((i + TM - 1) % TM, j);
+          p[j] = mfma_f8(fw[j], fx[i & 1], f32x4_t{0, 0, 0, 0});
+          if (i == TM - 1) fw[j] = read_w(next, j);
+          if constexpr (WROWS)
+            if (i == 0) swr[j] = *reinterpret_cast<const f32x4_t*>(st + S::WS + ((wn * TN + j) * 16 + 4 * fk) * 4);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        before = s;
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    G8_WAIT(63);                                            // (LDS reads alone)
-    G8_BARRIER();                                           // every wave has read this stage
-    issue(min(b + 2, blocks - 1), st);                      // past the end: the last block again
+#pragma unroll
+    for (int j = 0; j < TN; ++j) add(TM - 1, j);
   }
   G8_WAIT(0);                                               // no load may still write LDS at the end
 
