@@ -92,6 +92,39 @@ __device__ __forceinline__ GroupUnit find_unit(const int32_t* offsets, int n_ids
   const int last = __builtin_amdgcn_readlane(hi, at);
   return GroupUnit{g0 + at, first, min(unit, last - first), index};
 }
+// The same for a wave that asks for many units: up to 64 groups stay in its lanes.
+struct GroupTable {
+  int lo, hi;               // the lane's group
+  uint32_t before, mine;    // units before it, its own
+  uint32_t total;           // of all groups
+};
+__device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, int n, int unit);
+__device__ __forceinline__ GroupTable group_table(const int32_t* offsets, int n_ids, int n, int unit) {
+  GroupTable t = {0, 0, 0, 0, 0};
+  if (n_ids > 64) {
+    t.total = units_before(offsets, n_ids, n, unit);
+    return t;
+  }
+  const int g = threadIdx.x & 63;
+  if (g < n_ids) {
+    t.lo = group_offset(offsets, g, n);
+    t.hi = group_offset(offsets, g + 1, n);
+  }
+  t.mine = units_of(t.lo, t.hi, unit);
+  t.before = wave_before(t.mine, &t.total);
+  t.total = (uint32_t)__builtin_amdgcn_readfirstlane((int)t.total);
+  return t;
+}
+__device__ __forceinline__ GroupUnit unit_at(const GroupTable& t, const int32_t* offsets, int n_ids, int n, int unit, uint32_t u) {
+  if (n_ids > 64) return find_unit(offsets, n_ids, n, unit, u);
+  const uint64_t hit = __ballot(u >= t.before && u - t.before < t.mine);
+  if (!hit) return GroupUnit{-1, 0, 0, 0};
+  const int g = __ffsll((unsigned long long)hit) - 1;
+  const int index = (int)(u - (uint32_t)__builtin_amdgcn_readlane((int)t.before, g));
+  const int first = __builtin_amdgcn_readlane(t.lo, g) + index * unit;
+  return GroupUnit{g, first, min(unit, __builtin_amdgcn_readlane(t.hi, g) - first), index};
+}
+
 // Units of the groups before group g.
 __device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, int n, int unit) {
   uint32_t sum = 0, total;

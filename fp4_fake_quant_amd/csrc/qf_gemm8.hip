@@ -24,6 +24,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int64_t G8_MAX_TILES = 1 << 22;
+constexpr int G8_CUS = 256;
 constexpr int G8_RUN = 4;                // tile rows that share their columns' w in a cache
 
 // An operand: rows of `row` bytes pitch, blocks of 128 at `blk` bytes pitch.
@@ -40,7 +41,7 @@ struct Gemm8Args {
   int32_t M, N, K;                       // K: elements of a row-major row (panels: 0, every block whole)
   int32_t blocks;                        // blocks of the reduction (grouped over blocks: from the offsets)
   int32_t tiles_m, tiles_n;
-  int32_t y_vec;                         // y takes stores of 8 bytes
+  int32_t y_vec;                         // 2: rows of y take whole stores of 16 bytes
 };
 enum { G8_DENSE, G8_ROWS, G8_BLOCKS };   // over what the groups go
 
@@ -75,71 +76,152 @@ __device__ __forceinline__ uint32_t g8_chunk(uint32_t row, uint32_t c) { return 
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
+// Values that are the same in all lanes, kept in scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(uint32_t)uniform((int)v) | ((int64_t)uniform((int)(v >> 32)) << 32);
+}
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) { return (T*)uniform((int64_t)p); }
+
+// A tile of outputs: its first row and column, how many of each there are, its group.
+struct TileAt {
+  int m0, rows, n0, cols, group, blocks;
+};
+
+// Workgroups stay: each takes tiles of its XCD's run one after another, and the blocks of all its tiles are
+// one stream of steps, so that the next tile's first operands are on their way while a tile's last
+// products are formed and its results leave through LDS (the stage that the last step has freed).
 template <int MODE, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
   constexpr int WAVES = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
   constexpr bool WROWS = MODE == G8_BLOCKS;                  // w has a scale per row and block
   constexpr int XW = BM / 8 / WAVES, WW = BN / 8 / WAVES;    // LDS windows (eight rows) that a wave fills per step
-  constexpr int LOADS = XW + WW + 1;
   static_assert(BM / 64 + BN / 64 == WAVES, "one window of 64 scales per wave");
+  static_assert(XW % 2 == 0 && WW % 2 == 0, "the parity of a window is that of its index in the wave");
   using S = Stage<BM, BN>;
+  constexpr int PASSES = (BM * BN * 2 + S::BYTES - 1) / S::BYTES;      // in which a tile leaves through a stage
+  static_assert(PASSES == 1 || PASSES == WM, "a pass takes the rows of one row of waves, or all");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::BYTES];
 
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t frow = lane & 15, fk = lane >> 4;
-  // workgroups go round the XCDs: each XCD takes a run of tiles
-  const uint32_t total = gridDim.x, xcd = blockIdx.x & 7;
-  uint32_t t = xcd * (total >> 3) + min(xcd, total & 7u) + (blockIdx.x >> 3);
-  int group = 0, block0 = 0, blocks = a.blocks;
-  if (MODE == G8_BLOCKS) {
-    group = (int)(t / (uint32_t)(a.tiles_m * a.tiles_n));
-    t -= (uint32_t)group * (uint32_t)(a.tiles_m * a.tiles_n);
-    if (a.offsets) {
-      block0 = (int)units_before(a.offsets, group, a.n, FB);
-      blocks = (int)units_of(group_offset(a.offsets, group, a.n), group_offset(a.offsets, group + 1, a.n), FB);
-    }
-  }
-  // tiles in runs of G8_RUN tile rows, column by column
-  const uint32_t run = t / (uint32_t)(G8_RUN * a.tiles_n), in_run = t - run * (uint32_t)(G8_RUN * a.tiles_n);
-  const uint32_t deep = min((uint32_t)a.tiles_m - run * G8_RUN, (uint32_t)G8_RUN);
-  const int tm = (int)(run * G8_RUN + in_run % deep), tn = (int)(in_run / deep);
-  int m0 = tm * BM, rows = min(BM, a.M - m0);
-  if (MODE == G8_ROWS) {
-    const GroupUnit g = find_unit(a.offsets, a.n_ids, a.n, BM, (uint32_t)tm);
-    if (g.group < 0) return;
-    group = g.group;
-    m0 = g.first;
-    rows = g.rows;
-  }
-  const int n0 = tn * BN, cols = min(BN, a.N - n0);
   const uint32_t wm = wave / WN, wn = wave % WN;
-  const uint8_t* x = a.x + (int64_t)m0 * a.x_row + (int64_t)block0 * a.x_blk;
-  const uint8_t* w = a.w + (int64_t)group * (WROWS ? 0 : a.w_group) + (int64_t)n0 * a.w_row + (int64_t)block0 * a.w_blk;
-  const float* xs = a.xs + m0 + (int64_t)block0 * a.xs_blk;
-  const float* ws = WROWS ? a.ws + n0 + (int64_t)block0 * a.ws_blk
-                          : a.ws + (int64_t)group * a.ws_group + (int64_t)(n0 / FB) * a.ws_tile;
 
+  // tiles of this workgroup: t, t + step, ... below end, inside its XCD's run
+  GroupTable table;
+  uint32_t tiles_m = (uint32_t)a.tiles_m, tiles_n = (uint32_t)a.tiles_n;
+  if (MODE == G8_ROWS) {
+    table = group_table(a.offsets, a.n_ids, a.n, BM);
+    tiles_m = table.total;
+  }
+  const uint32_t total = tiles_m * tiles_n * (MODE == G8_BLOCKS ? (uint32_t)a.n_ids : 1u);
+  const uint32_t xcd = blockIdx.x & 7;
+  const uint32_t first = xcd * (total >> 3) + min(xcd, total & 7u);
+  const uint32_t end = first + (total >> 3) + (xcd < (total & 7u) ? 1u : 0u);
+  const uint32_t step = (gridDim.x - xcd + 7) >> 3;
+  auto tile_at = [&](uint32_t t, int& block0) {
+    TileAt o;
+    o.group = 0;
+    block0 = 0;
+    int blocks = a.blocks;
+    if (MODE == G8_BLOCKS) {
+      o.group = (int)(t / (tiles_m * tiles_n));
+      t -= (uint32_t)o.group * tiles_m * tiles_n;
+      if (a.offsets) {
+        block0 = (int)units_before(a.offsets, o.group, a.n, FB);
+        blocks = (int)units_of(group_offset(a.offsets, o.group, a.n), group_offset(a.offsets, o.group + 1, a.n), FB);
+      }
+    }
+    // runs of G8_RUN tile rows, column by column
+    const uint32_t run = t / (G8_RUN * tiles_n), in_run = t - run * (G8_RUN * tiles_n);
+    const uint32_t deep = min(tiles_m - run * G8_RUN, (uint32_t)G8_RUN);
+    const uint32_t tn = in_run / deep, tm = run * G8_RUN + in_run - tn * deep;
+    o.m0 = (int)tm * BM;
+    o.rows = min(BM, a.M - o.m0);
+    if (MODE == G8_ROWS) {
+      const GroupUnit g = unit_at(table, a.offsets, a.n_ids, a.n, BM, tm);
+      o.group = g.group;
+      o.m0 = g.first;
+      o.rows = g.rows;
+    }
+    o.n0 = uniform((int)tn * BN);
+    o.cols = uniform(min(BN, a.N - o.n0));
+    o.m0 = uniform(o.m0);
+    o.rows = uniform(o.rows);
+    o.group = uniform(o.group);
+    o.blocks = uniform(blocks);
+    return o;
+  };
+  auto out_of = [&](const TileAt& o) {
+    return a.y + (MODE == G8_BLOCKS ? (int64_t)o.group * a.y_group : 0) + (int64_t)o.m0 * a.ldy + o.n0;
+  };
+
+  // ---- loads: a cursor that runs two blocks ahead of the products ----
   // the lane's place in window i of its wave: row lane / 8 of its eight, chunk (lane % 8) ^ swizzle, which
   // goes by the parity of the window
-  static_assert(XW % 2 == 0 && WW % 2 == 0, "the parity of a window is that of its index in the wave");
   const uint32_t xrow = (8 * XW * wave + (lane >> 3)) * (uint32_t)a.x_row, wrow = (8 * WW * wave + (lane >> 3)) * (uint32_t)a.w_row;
   const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;      // even windows; odd ones: chunk ^ 64
   // scales: wave i fills window i of 64 of the BM + BN words behind the codes: x's rows, then w's rows, or
   // w's tiles (in the first of these windows alone)
   const bool for_x = wave < BM / 64;
   const uint32_t sr = for_x ? 64 * wave : 64 * wave - BM;
-  const float* sbase = for_x ? xs : ws;
-  const int64_t sstep = for_x ? a.xs_blk : a.ws_blk;
-  const int64_t sbytes = for_x ? (int64_t)rows * 4 : WROWS ? (int64_t)cols * 4 : ((int64_t)((cols - 1) / FB) * a.ws_tile + 1) * 4;
   const uint32_t soff = for_x || WROWS ? (sr + lane) * 4 : sr == 0 && lane < BN / FB ? lane * (uint32_t)a.ws_tile * 4 : BUF_OOR;
-  // a row of a row-major operand ends at K, inside the last block; what lies behind must read as zeros
-  const int klen = WROWS ? FB : a.K;
-  auto issue = [&](int b, uint8_t* st) {
-    const int64_t bx = (int64_t)b * a.x_blk, bw = (int64_t)b * a.w_blk;
-    const uint32_t left = WROWS ? (uint32_t)FB : (uint32_t)(a.K - b * FB);
-    const __amdgpu_buffer_rsrc_t rx = make_buf(x + bx, (int64_t)(rows - 1) * a.x_row + klen - (WROWS ? 0 : bx));
-    const __amdgpu_buffer_rsrc_t rw = make_buf(w + bw, (int64_t)(cols - 1) * a.w_row + klen - (WROWS ? 0 : bw));
-    const __amdgpu_buffer_rsrc_t rs = make_buf(sbase + (int64_t)b * sstep, sbytes);
+  const int64_t sstep = for_x ? a.xs_blk : a.ws_blk;
+  uint32_t next_t = first + (blockIdx.x >> 3);
+  const uint8_t *x = nullptr, *w = nullptr;
+  const float* sbase = nullptr;
+  int64_t xbytes = 0, wbytes = 0, sbytes = 0;
+  int at = 0, last = 0;                                       // blocks of the cursor's tile: next one, behind the last
+  // tiles begun and not yet stored: the products' own and, at most, the one behind it (the last one opened:
+  // a tile is stored before the second one behind it is begun)
+  int n_m0 = 0, n_rows = 0, n_n0 = 0, n_cols = 0, n_group = 0, n_blocks = 0;
+  int held = 0;
+  // the next tile with blocks, if there is one; tiles without (a group without rows) become zeros at once
+  auto open = [&]() {
+    while (next_t < end) {
+      int block0;
+      const TileAt o = tile_at(next_t, block0);
+      next_t = (uint32_t)uniform((int)(next_t + step));
+      if (MODE == G8_BLOCKS && o.blocks == 0) {
+        uint16_t* y = out_of(o);
+        for (int i = threadIdx.x; i < o.rows * (BN / 4); i += 64 * WAVES) {
+          const int r = i / (BN / 4), c = i % (BN / 4) * 4;
+          if (c < o.cols) *reinterpret_cast<uint2*>(y + (int64_t)r * a.ldy + c) = make_uint2(0, 0);
+        }
+        continue;
+      }
+      x = uniform(a.x + (int64_t)o.m0 * a.x_row + (int64_t)block0 * a.x_blk);
+      w = uniform(a.w + (WROWS ? 0 : (int64_t)o.group * a.w_group) + (int64_t)o.n0 * a.w_row + (int64_t)block0 * a.w_blk);
+      const float* xs = a.xs + o.m0 + (int64_t)block0 * a.xs_blk;
+      const float* ws = WROWS ? a.ws + o.n0 + (int64_t)block0 * a.ws_blk
+                              : a.ws + (int64_t)o.group * a.ws_group + (int64_t)(o.n0 / FB) * a.ws_tile;
+      sbase = uniform(for_x ? xs : ws);
+      sbytes = for_x ? (int64_t)o.rows * 4 : WROWS ? (int64_t)o.cols * 4 : ((int64_t)((o.cols - 1) / FB) * a.ws_tile + 1) * 4;
+      // a row of a row-major operand ends at K, inside the last block; what lies behind must read as zeros
+      xbytes = (int64_t)(o.rows - 1) * a.x_row + (WROWS ? FB : a.K);
+      wbytes = (int64_t)(o.cols - 1) * a.w_row + (WROWS ? FB : a.K);
+      at = 0;
+      last = o.blocks;
+      n_m0 = o.m0;
+      n_rows = o.rows;
+      n_n0 = o.n0;
+      n_cols = o.cols;
+      n_group = o.group;
+      n_blocks = o.blocks;
+      ++held;
+      return;
+    }
+  };
+  auto issue = [&](uint8_t* st) {
+    if (at == last) open();
+    if (at == last) return;                                   // no tile is left
+    const int64_t bx = WROWS ? 0 : (int64_t)at * FB;          // what a row-major row has behind it
+    const uint32_t left = WROWS ? (uint32_t)FB : (uint32_t)(a.K - at * FB);
+    const __amdgpu_buffer_rsrc_t rx = make_buf(x + (int64_t)at * a.x_blk, xbytes - bx);
+    const __amdgpu_buffer_rsrc_t rw = make_buf(w + (int64_t)at * a.w_blk, wbytes - bx);
+    const __amdgpu_buffer_rsrc_t rs = make_buf(sbase + (int64_t)at * sstep, sbytes);
+    ++at;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(st + S::XS + wave * 256), 4, soff, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < XW; ++i) {
@@ -154,97 +236,144 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
                                                c < left ? wrow + c + i * 8 * (uint32_t)a.w_row : BUF_OOR, 0, 0, 0);
     }
   };
+
+  // ---- products ----
   auto frag = [&](const uint8_t* base, uint32_t row) {
     const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, fk));
     const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(base + g8_chunk(row, fk + 4));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
+  auto read_w = [&](const uint8_t* st, int j) { return frag(st + S::W, (wn * TN + j) * 16 + frow); };
+  auto read_x = [&](const uint8_t* st, int i) { return frag(st, (wm * TM + i) * 16 + frow); };
+  auto read_sx = [&](const uint8_t* st, int i) { return *reinterpret_cast<const float*>(st + S::XS + ((wm * TM + i) * 16 + frow) * 4); };
+  auto read_sw = [&](const uint8_t* st) { return WROWS ? 1.0f : *reinterpret_cast<const float*>(st + S::WS + (wn * TN * 16 / FB) * 4); };
 
-  f32x4_t acc[TM][TN];
+  issue(lds);
+  if (held == 0) return;
+  int c_m0 = n_m0, c_rows = n_rows, c_n0 = n_n0, c_cols = n_cols, c_group = n_group, left = n_blocks;
+  issue(lds + S::BYTES);
+  G8_WAIT(0);
+  G8_BARRIER();
+  i32x8_t fw[TN], fx[2];
+  f32x4_t acc[TM][TN], p[TN], swr[TN];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int j = 0; j < TN; ++j) {
+    fw[j] = read_w(lds, j);
+    p[j] = swr[j] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-
+    for (int i = 0; i < TM; ++i) acc[i][j] = f32x4_t{0, 0, 0, 0};
+  }
+  fx[0] = read_x(lds, 0);
+  float sw = read_sw(lds), sx = read_sx(lds, 0), before = 0.0f;        // before: scale of the row before
+  auto add = [&](int i, int j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(WROWS ? p[j][e] * swr[j][e] : p[j][e], before, acc[i][j][e]);
+    asm volatile("" : "+v"(acc[i][j]));                      // the sum stays here, beside the next products
+  };
+  uint32_t parity = 0;
   // Row i of the wave's tiles: its products (operands read a row earlier), and beside each the sum of the
   // row before, whose products are done by then.  The last row of a step waits for the next stage, passes
   // the step's one barrier (this stage is read, the next has landed), refills this stage and reads the
   // next step's first operands, so that the matrix cores go on over the step's end.
-  if (blocks > 0) {
-    issue(0, lds);
-    issue(min(1, blocks - 1), lds + S::BYTES);
-    G8_WAIT(LOADS);
-    G8_BARRIER();
-    i32x8_t fw[TN], fx[2];
-    f32x4_t p[TN], swr[TN];
-    auto read_w = [&](const uint8_t* st, int j) { return frag(st + S::W, (wn * TN + j) * 16 + frow); };
-    auto read_x = [&](const uint8_t* st, int i) { return frag(st, (wm * TM + i) * 16 + frow); };
-    auto read_sx = [&](const uint8_t* st, int i) { return *reinterpret_cast<const float*>(st + S::XS + ((wm * TM + i) * 16 + frow) * 4); };
-    auto read_sw = [&](const uint8_t* st) { return WROWS ? 1.0f : *reinterpret_cast<const float*>(st + S::WS + (wn * TN * 16 / FB) * 4); };
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      fw[j] = read_w(lds, j);
-      p[j] = f32x4_t{0, 0, 0, 0};
-      swr[j] = f32x4_t{0, 0, 0, 0};
-    }
-    fx[0] = read_x(lds, 0);
-    float sw = read_sw(lds), sx = read_sx(lds, 0), before = 0.0f;      // before: scale of the row before
-    auto add = [&](int i, int j) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc[i][j][e] = __builtin_fmaf(WROWS ? p[j][e] * swr[j][e] : p[j][e], before, acc[i][j][e]);
-      asm volatile("" : "+v"(acc[i][j]));                    // the sum stays here, beside the next products
-    };
 #pragma unroll 1
-    for (int b = 0; b < blocks; ++b) {
-      uint8_t* st = lds + (b & 1) * S::BYTES;
-      const uint8_t* next = lds + (~b & 1) * S::BYTES;
+  while (true) {
+    uint8_t* st;
+#pragma unroll 1
+    do {
+    st = lds + parity * S::BYTES;
+    const uint8_t* next = lds + (parity ^ 1) * S::BYTES;
+    --left;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const float s = sx * sw;
-        if (i == TM - 1) {
-          G8_WAIT(0);
-          G8_BARRIER();
-          issue(min(b + 2, blocks - 1), st);                 // past the end: the last block again
-        }
-        fx[(i + 1) & 1] = i + 1 < TM ? read_x(st, i + 1) : read_x(next, 0);
-        sx = i + 1 < TM ? read_sx(st, i + 1) : read_sx(next, 0);
-        if (i == TM - 1) sw = read_sw(next);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          add((i + TM - 1) % TM, j);
-          p[j] = mfma_f8(fw[j], fx[i & 1], f32x4_t{0, 0, 0, 0});
-          if (i == TM - 1) fw[j] = read_w(next, j);
-          if constexpr (WROWS)
-            if (i == 0) swr[j] = *reinterpret_cast<const f32x4_t*>(st + S::WS + ((wn * TN + j) * 16 + 4 * fk) * 4);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        before = s;
+    for (int i = 0; i < TM; ++i) {
+      const float s = sx * sw;
+      if (i == TM - 1) {
+        G8_WAIT(0);
+        G8_BARRIER();
+        if (left > 0) issue(st);
       }
+      fx[(i + 1) & 1] = i + 1 < TM ? read_x(st, i + 1) : read_x(next, 0);
+      sx = i + 1 < TM ? read_sx(st, i + 1) : read_sx(next, 0);
+      if (i == TM - 1) sw = read_sw(next);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        add((i + TM - 1) % TM, j);
+        p[j] = mfma_f8(fw[j], fx[i & 1], f32x4_t{0, 0, 0, 0});
+        if (i == TM - 1) fw[j] = read_w(next, j);
+        if constexpr (WROWS)
+          if (i == 0) swr[j] = *reinterpret_cast<const f32x4_t*>(st + S::WS + ((wn * TN + j) * 16 + 4 * fk) * 4);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      before = s;
     }
+    parity ^= 1;
+    } while (left > 0);
+
+    // ---- the tile is done ----
+    // (the lane's number is made anew, so that no address of the epilogue takes a register in the loop)
+    uint32_t tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const uint32_t erow = tid & 15, ek = (tid >> 4) & 3;
 #pragma unroll
     for (int j = 0; j < TN; ++j) add(TM - 1, j);
-  }
-  G8_WAIT(0);                                               // no load may still write LDS at the end
-
+    const TileAt o = {c_m0, c_rows, c_n0, c_cols, c_group, 0};
+    uint16_t* y = out_of(o);
+    if (a.y_vec == 2) {
+      // 16-byte chunk c of a row lies at c ^ row: rows written by one instruction, and the chunks of a row
+      // read back, meet different banks
+      constexpr uint32_t CH = BN / 8, ROWS = BM / PASSES;
+      const __amdgpu_buffer_rsrc_t ry = make_buf(y, ((int64_t)(o.rows - 1) * a.ldy + o.cols) * 2);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = (int)((wm * TM + i) * 16 + frow);
-    if (r >= rows) continue;
-    uint16_t* y = a.y + (MODE == G8_BLOCKS ? (int64_t)group * a.y_group : 0) + (int64_t)(m0 + r) * a.ldy + n0;
+      for (int pass = 0; pass < PASSES; ++pass) {
+        if (PASSES == 1 || (int)wm == pass) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int c = (int)((wn * TN + j) * 16 + 4 * fk);
-      const uint32_t lo = pack_bf16x2(acc[i][j][0], acc[i][j][1]), hi = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
-      if (a.y_vec && c + 3 < cols) {
-        *reinterpret_cast<uint2*>(y + c) = make_uint2(lo, hi);
-      } else {
-        const uint16_t v[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+          for (int i = 0; i < TM; ++i) {
+            const uint32_t r = (PASSES == 1 ? wm * TM * 16 : 0) + i * 16 + erow;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c + e < cols) y[c + e] = v[e];
+            for (int j = 0; j < TN; ++j) {
+              const uint32_t c = (wn * TN + j) * 2 + (ek >> 1);
+              *reinterpret_cast<uint2*>(st + r * (BN * 2) + ((c ^ (r & (CH - 1))) << 4) + (ek & 1) * 8) =
+                  make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+            }
+          }
+        }
+        __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4) | (0 << 8));
+        G8_BARRIER();
+#pragma unroll
+        for (uint32_t k = 0; k < ROWS * CH / (64 * WAVES); ++k) {
+          const uint32_t u = k * 64 * WAVES + tid, r = u / CH, c = u % CH;
+          const uint4 v = *reinterpret_cast<const uint4*>(st + r * (BN * 2) + ((c ^ (r & (CH - 1))) << 4));
+          const uint32_t row = pass * ROWS + r;
+          buf_store16(ry, (int)row < o.rows && (int)(8 * c) < o.cols ? (row * (uint32_t)a.ldy + 8 * c) * 2 : BUF_OOR, v);
+        }
+        __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4) | (0 << 8));
+        G8_BARRIER();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = (int)((wm * TM + i) * 16 + erow);
+        if (r >= o.rows) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int c = (int)((wn * TN + j) * 16 + 4 * ek);
+          const uint32_t v[2] = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < o.cols) y[(int64_t)r * a.ldy + c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        }
       }
     }
+    if (--held == 0) return;
+    c_m0 = n_m0, c_rows = n_rows, c_n0 = n_n0, c_cols = n_cols, c_group = n_group;
+    left = n_blocks;
+    issue(st);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      p[j] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < TM; ++i) acc[i][j] = f32x4_t{0, 0, 0, 0};
+    }
+    before = 0.0f;
   }
 }
 
@@ -253,9 +382,12 @@ constexpr int64_t G8_MAX_N = 1 << 22;
 
 template <int BM, int BN, int WM, int WN>
 hipError_t launch_tiles(Gemm8Args a, int mode, hipStream_t s) {
-  a.tiles_m = (int32_t)((a.M + BM - 1) / BM + (mode == G8_ROWS ? (a.M < a.n_ids ? a.M : a.n_ids) : 0));
+  a.tiles_m = (int32_t)((a.M + BM - 1) / BM);
   a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
-  const dim3 g((unsigned)((int64_t)a.tiles_m * a.tiles_n * (mode == G8_BLOCKS ? a.n_ids : 1))), wg(64 * WM * WN);
+  // at most as many workgroups as the chip holds at once
+  const int64_t tiles = (a.tiles_m + (mode == G8_ROWS ? (a.M < a.n_ids ? a.M : a.n_ids) : 0)) * (int64_t)a.tiles_n * (mode == G8_BLOCKS ? a.n_ids : 1);
+  const int64_t most = G8_CUS * (160 * 1024 / (2 * Stage<BM, BN>::BYTES));
+  const dim3 g((unsigned)(tiles < most ? tiles : most)), wg(64 * WM * WN);
   if (mode == G8_DENSE) k_gemm8<G8_DENSE, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
   else if (mode == G8_ROWS) k_gemm8<G8_ROWS, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
   else k_gemm8<G8_BLOCKS, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
@@ -269,7 +401,7 @@ int64_t small_tiles(const Gemm8Args& a, int mode) {
 }
 
 hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
-  a.y_vec = a.ldy % 4 == 0 && (uintptr_t)a.y % 8 == 0;
+  a.y_vec = a.ldy % 8 == 0 && (uintptr_t)a.y % 16 == 0 && a.N % 8 == 0 && a.ldy < QF_FP8_MAX_COLS ? 2 : 0;
   if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
   return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
