@@ -92,37 +92,57 @@ __device__ __forceinline__ GroupUnit find_unit(const int32_t* offsets, int n_ids
   const int last = __builtin_amdgcn_readlane(hi, at);
   return GroupUnit{g0 + at, first, min(unit, last - first), index};
 }
-// The same for a wave that asks for many units: up to 64 groups stay in its lanes.
+// The same for workgroups that ask for many units: the groups' offsets and unit counts stay in LDS.
 struct GroupTable {
-  int lo, hi;               // the lane's group
-  uint32_t before, mine;    // units before it, its own
-  uint32_t total;           // of all groups
+  int32_t off[QF_ROW_MAX_IDS + 1];      // the plan's offsets
+  uint32_t pre[QF_ROW_MAX_IDS + 1];     // units of the groups before
+  uint32_t sums[16];                    // of each wave, while the table is built
 };
-__device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, int n, int unit);
-__device__ __forceinline__ GroupTable group_table(const int32_t* offsets, int n_ids, int n, int unit) {
-  GroupTable t = {0, 0, 0, 0, 0};
-  if (n_ids > 64) {
-    t.total = units_before(offsets, n_ids, n, unit);
-    return t;
-  }
-  const int g = threadIdx.x & 63;
-  if (g < n_ids) {
-    t.lo = group_offset(offsets, g, n);
-    t.hi = group_offset(offsets, g + 1, n);
-  }
-  t.mine = units_of(t.lo, t.hi, unit);
-  t.before = wave_before(t.mine, &t.total);
-  t.total = (uint32_t)__builtin_amdgcn_readfirstlane((int)t.total);
-  return t;
+// Fills the table with the whole workgroup (of `waves` waves, at least four).
+__device__ __forceinline__ void group_table(GroupTable& t, const int32_t* offsets, int n_ids, int n, int unit, int waves) {
+  const int threads = waves * 64, per = (n_ids + threads - 1) / threads, g0 = (int)threadIdx.x * per;
+  uint32_t mine[4] = {0, 0, 0, 0}, sum = 0, total;
+  int lo = group_offset(offsets, min(g0, n_ids), n);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < per && g0 + j < n_ids) {
+      const int hi = group_offset(offsets, g0 + j + 1, n);
+      t.off[g0 + j] = lo;
+      if (g0 + j + 1 == n_ids) t.off[n_ids] = hi;
+      mine[j] = units_of(lo, hi, unit);
+      sum += mine[j];
+      lo = hi;
+    }
+  uint32_t before = wave_before(sum, &total);
+  if ((threadIdx.x & 63) == 0) t.sums[threadIdx.x >> 6] = total;
+  __syncthreads();
+  for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) before += t.sums[w];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < per && g0 + j < n_ids) {
+      t.pre[g0 + j] = before;
+      before += mine[j];
+      if (g0 + j + 1 == n_ids) t.pre[n_ids] = before;
+    }
+  __syncthreads();
 }
-__device__ __forceinline__ GroupUnit unit_at(const GroupTable& t, const int32_t* offsets, int n_ids, int n, int unit, uint32_t u) {
-  if (n_ids > 64) return find_unit(offsets, n_ids, n, unit, u);
-  const uint64_t hit = __ballot(u >= t.before && u - t.before < t.mine);
+__device__ __forceinline__ GroupUnit unit_at(const GroupTable& t, int n_ids, int unit, uint32_t u) {
+  const int lane = threadIdx.x & 63, per = (n_ids + 63) / 64;
+  int g = 0;
+  if (per > 1) {                                     // runs of groups first
+    const uint64_t upto = __ballot(t.pre[min(lane * per, n_ids)] <= u && lane * per < n_ids);
+    g = (63 - __clzll((unsigned long long)upto)) * per;
+  }
+  // the last group of the run that begins at or before u, empty ones behind it left out
+  const bool in = (per == 1 || lane < per) && g + lane < n_ids;
+  const uint32_t lo = in ? t.pre[g + lane] : 0, hi = in ? t.pre[g + lane + 1] : 0;
+  const uint64_t hit = __ballot(lo <= u && u < hi);
   if (!hit) return GroupUnit{-1, 0, 0, 0};
-  const int g = __ffsll((unsigned long long)hit) - 1;
-  const int index = (int)(u - (uint32_t)__builtin_amdgcn_readlane((int)t.before, g));
-  const int first = __builtin_amdgcn_readlane(t.lo, g) + index * unit;
-  return GroupUnit{g, first, min(unit, __builtin_amdgcn_readlane(t.hi, g) - first), index};
+  const int at = __ffsll((unsigned long long)hit) - 1;
+  const int index = (int)(u - (uint32_t)__builtin_amdgcn_readlane((int)lo, at));
+  g += at;
+  const int first = __builtin_amdgcn_readfirstlane(t.off[g]) + index * unit;
+  return GroupUnit{g, first, min(unit, __builtin_amdgcn_readfirstlane(t.off[g + 1]) - first), index};
 }
 
 // Units of the groups before group g.

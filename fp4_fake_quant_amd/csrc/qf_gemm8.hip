@@ -15,6 +15,7 @@
 // them and cut below 2^(E - 13), and the sums of these groups are added in fp32.  Codes drawn from the
 // whole range lose up to 2^-13 of the terms' magnitudes, quantized normal values 2^-19 at the root mean square.
 #include "qf_fp8.h"
+#include <stdlib.h>
 
 namespace qf {
 namespace {
@@ -102,18 +103,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
   using S = Stage<BM, BN>;
   constexpr int PASSES = (BM * BN * 2 + S::BYTES - 1) / S::BYTES;      // in which a tile leaves through a stage
   static_assert(PASSES == 1 || PASSES == WM, "a pass takes the rows of one row of waves, or all");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::BYTES];
+  // (one array: with a second one the compiler waits for all loads in flight before it reads either)
+  constexpr int LDS = 2 * S::BYTES + (MODE == G8_DENSE ? 0 : (int)sizeof(GroupTable));
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
+  GroupTable& table = *reinterpret_cast<GroupTable*>(lds + (MODE == G8_DENSE ? 0 : 2 * S::BYTES));
 
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t frow = lane & 15, fk = lane >> 4;
   const uint32_t wm = wave / WN, wn = wave % WN;
 
   // tiles of this workgroup: t, t + step, ... below end, inside its XCD's run
-  GroupTable table;
   uint32_t tiles_m = (uint32_t)a.tiles_m, tiles_n = (uint32_t)a.tiles_n;
-  if (MODE == G8_ROWS) {
-    table = group_table(a.offsets, a.n_ids, a.n, BM);
-    tiles_m = table.total;
+  if (MODE != G8_DENSE && a.offsets) {
+    group_table(table, a.offsets, a.n_ids, a.n, MODE == G8_ROWS ? BM : FB, WAVES);
+    if (MODE == G8_ROWS) tiles_m = (uint32_t)uniform((int)table.pre[a.n_ids]);
   }
   const uint32_t total = tiles_m * tiles_n * (MODE == G8_BLOCKS ? (uint32_t)a.n_ids : 1u);
   const uint32_t xcd = blockIdx.x & 7;
@@ -129,8 +132,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
       o.group = (int)(t / (tiles_m * tiles_n));
       t -= (uint32_t)o.group * tiles_m * tiles_n;
       if (a.offsets) {
-        block0 = (int)units_before(a.offsets, o.group, a.n, FB);
-        blocks = (int)units_of(group_offset(a.offsets, o.group, a.n), group_offset(a.offsets, o.group + 1, a.n), FB);
+        block0 = uniform((int)table.pre[o.group]);
+        blocks = uniform((int)table.pre[o.group + 1]) - block0;
       }
     }
     // runs of G8_RUN tile rows, column by column
@@ -140,7 +143,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
     o.m0 = (int)tm * BM;
     o.rows = min(BM, a.M - o.m0);
     if (MODE == G8_ROWS) {
-      const GroupUnit g = unit_at(table, a.offsets, a.n_ids, a.n, BM, tm);
+      const GroupUnit g = unit_at(table, a.n_ids, BM, tm);
       o.group = g.group;
       o.m0 = g.first;
       o.rows = g.rows;
@@ -402,7 +405,7 @@ int64_t small_tiles(const Gemm8Args& a, int mode) {
 
 hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
   a.y_vec = a.ldy % 8 == 0 && (uintptr_t)a.y % 16 == 0 && a.N % 8 == 0 && a.ldy < QF_FP8_MAX_COLS ? 2 : 0;
-  if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
+  if (small_tiles(a, mode) >= 1024 && !getenv("G8S")) return launch_tiles<256, 256, 2, 4>(a, mode, s);
   return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
 
