@@ -15,7 +15,6 @@
 // them and cut below 2^(E - 13), and the sums of these groups are added in fp32.  Codes drawn from the
 // whole range lose up to 2^-13 of the terms' magnitudes, quantized normal values 2^-19 at the root mean square.
 #include "qf_fp8.h"
-#include <stdlib.h>
 
 namespace qf {
 namespace {
@@ -37,12 +36,12 @@ struct Gemm8Args {
   int64_t ws_tile, ws_blk, ws_group;     // of w: tile scales [tile][block], or [block][rows] with ws_blk
   uint16_t* y;
   int64_t ldy, y_group;
-  const int32_t* offsets;
+  const int32_t *offsets, *tiles;
   int32_t n_ids, n;                      // groups and rows of the plan
   int32_t M, N, K;                       // K: elements of a row-major row (panels: 0, every block whole)
   int32_t blocks;                        // blocks of the reduction (grouped over blocks: from the offsets)
   int32_t tiles_m, tiles_n;
-  int32_t y_vec;                         // 2: rows of y take whole stores of 16 bytes
+  int32_t y_vec;                         // rows of y take whole stores of 16 bytes (few rows: of 8)
 };
 enum { G8_DENSE, G8_ROWS, G8_BLOCKS };   // over what the groups go
 
@@ -320,51 +319,68 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
     for (int j = 0; j < TN; ++j) add(TM - 1, j);
     const TileAt o = {c_m0, c_rows, c_n0, c_cols, c_group, 0};
     uint16_t* y = out_of(o);
-    if (a.y_vec == 2) {
-      // 16-byte chunk c of a row lies at c ^ row: rows written by one instruction, and the chunks of a row
-      // read back, meet different banks
-      constexpr uint32_t CH = BN / 8, ROWS = BM / PASSES;
-      const __amdgpu_buffer_rsrc_t ry = make_buf(y, ((int64_t)(o.rows - 1) * a.ldy + o.cols) * 2);
+    // 16-byte chunk c of a row lies at c ^ row: rows written by one instruction, and the chunks of a row
+    // read back, meet different banks.  (The accesses are written out: the compiler would let each of them
+    // wait for the stores before it, as it does not tell those from loads that write LDS.)
+    constexpr uint32_t CH = BN / 8, ROWS = BM / PASSES, EACH = ROWS * CH / (64 * WAVES);
+    static_assert(EACH == 8, "read back by one instruction sequence");
+    const __amdgpu_buffer_rsrc_t ry = make_buf(y, ((int64_t)(o.rows - 1) * a.ldy + o.cols) * 2);
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr_t)st;
 #pragma unroll
-      for (int pass = 0; pass < PASSES; ++pass) {
-        if (PASSES == 1 || (int)wm == pass) {
+    for (int pass = 0; pass < PASSES; ++pass) {
+      if (PASSES == 1 || (int)wm == pass) {
 #pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const uint32_t r = (PASSES == 1 ? wm * TM * 16 : 0) + i * 16 + erow;
+        for (int i = 0; i < TM; ++i) {
+          const uint32_t r = (PASSES == 1 ? wm * TM * 16 : 0) + i * 16 + erow;
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-              const uint32_t c = (wn * TN + j) * 2 + (ek >> 1);
-              *reinterpret_cast<uint2*>(st + r * (BN * 2) + ((c ^ (r & (CH - 1))) << 4) + (ek & 1) * 8) =
-                  make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
-            }
+          for (int j = 0; j < TN; ++j) {
+            const uint32_t c = (wn * TN + j) * 2 + (ek >> 1);
+            const uint2 v = make_uint2(pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3]));
+            asm volatile("ds_write_b64 %0, %1" ::"v"(base + r * (BN * 2) + ((c ^ (r & (CH - 1))) << 4) + (ek & 1) * 8),
+                         "v"(__builtin_bit_cast(uint64_t, v))
+                         : "memory");
           }
         }
-        __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4) | (0 << 8));
-        G8_BARRIER();
-#pragma unroll
-        for (uint32_t k = 0; k < ROWS * CH / (64 * WAVES); ++k) {
-          const uint32_t u = k * 64 * WAVES + tid, r = u / CH, c = u % CH;
-          const uint4 v = *reinterpret_cast<const uint4*>(st + r * (BN * 2) + ((c ^ (r & (CH - 1))) << 4));
-          const uint32_t row = pass * ROWS + r;
-          buf_store16(ry, (int)row < o.rows && (int)(8 * c) < o.cols ? (row * (uint32_t)a.ldy + 8 * c) * 2 : BUF_OOR, v);
-        }
-        __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4) | (0 << 8));
-        G8_BARRIER();
       }
-    } else {
+      G8_WAIT(63);
+      G8_BARRIER();
+      // thread u of the workgroup: chunk u % CH of rows u / CH + k 64 WAVES / CH; the row's swizzle goes with k only
+      // above CH
+      const uint32_t r0 = tid / CH, c0 = tid % CH;
+      constexpr uint32_t DOWN = 64 * WAVES / CH;
+      u32x4_t v[EACH];
+      uint32_t from[EACH];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int r = (int)((wm * TM + i) * 16 + erow);
-        if (r >= o.rows) continue;
+      for (uint32_t k = 0; k < EACH; ++k) {
+        const uint32_t r = r0 + k * DOWN;
+        from[k] = base + r * (BN * 2) + ((c0 ^ (r & (CH - 1))) << 4);
+      }
+      asm volatile(
+          "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_b128 %2, %10\n\tds_read_b128 %3, %11\n\t"
+          "ds_read_b128 %4, %12\n\tds_read_b128 %5, %13\n\tds_read_b128 %6, %14\n\tds_read_b128 %7, %15\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+          : "v"(from[0]), "v"(from[1]), "v"(from[2]), "v"(from[3]), "v"(from[4]), "v"(from[5]), "v"(from[6]), "v"(from[7])
+          : "memory");
+      const int c = (int)(8 * c0);
+      if (a.y_vec) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const int c = (int)((wn * TN + j) * 16 + 4 * ek);
-          const uint32_t v[2] = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+        for (uint32_t k = 0; k < EACH; ++k) {
+          const uint32_t row = pass * ROWS + r0 + k * DOWN;
+          buf_store16(ry, (int)row < o.rows && c < o.cols ? (row * (uint32_t)a.ldy + (uint32_t)c) * 2 : BUF_OOR,
+                      __builtin_bit_cast(uint4, v[k]));
+        }
+      } else {                                                // rows off 16 bytes, or of any length
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c + e < o.cols) y[(int64_t)r * a.ldy + c + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        for (uint32_t k = 0; k < EACH; ++k) {
+          const uint32_t row = pass * ROWS + r0 + k * DOWN;
+          uint16_t* yr = y + (int64_t)row * a.ldy + c;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((int)row < o.rows && c + e < o.cols) yr[e] = (uint16_t)(v[k][e >> 1] >> (16 * (e & 1)));
         }
       }
+      G8_BARRIER();
     }
     if (--held == 0) return;
     c_m0 = n_m0, c_rows = n_rows, c_n0 = n_n0, c_cols = n_cols, c_group = n_group;
@@ -378,6 +394,108 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
     }
     before = 0.0f;
   }
+}
+
+// --------------------------------------------------------------- few rows ---
+// Up to 16 MT rows: the product streams w once, so the work is split over its columns (16 NJ a workgroup)
+// and over the blocks of the reduction, which the workgroup's waves take in turn and join in LDS in a
+// fixed order.  Operands go from memory into registers, several blocks ahead.
+constexpr int FEW_WAVES = 8;
+
+template <int MT, int NJ>
+__device__ __forceinline__ void few_rows(const Gemm8Args& a, int group, int m0, int rows, float* lds) {
+  constexpr int DEEP = MT + NJ <= 2 ? 4 : MT + NJ <= 4 ? 3 : 2;        // blocks in flight: 8 (MT + NJ) registers each
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t frow = lane & 15, fk = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16 * NJ, cols = min(16 * NJ, a.N - n0);
+  const uint8_t* x = a.x + (int64_t)m0 * a.x_row;
+  const uint8_t* w = a.w + (int64_t)group * a.w_group + (int64_t)n0 * a.w_row;
+  const __amdgpu_buffer_rsrc_t rx = make_buf(x, (int64_t)(rows - 1) * a.x_row + a.K);
+  const __amdgpu_buffer_rsrc_t rw = make_buf(w, (int64_t)(cols - 1) * a.w_row + a.K);
+  const float* ws = a.ws + (int64_t)group * a.ws_group + (int64_t)(n0 / FB) * a.ws_tile;
+  f32x4_t acc[MT][NJ];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+
+  for (int b0 = (int)wave; b0 < a.blocks; b0 += FEW_WAVES * DEEP) {
+    i32x8_t fw[DEEP][NJ], fx[DEEP][MT];
+    float sx[DEEP][MT], sw[DEEP];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int b = b0 + d * FEW_WAVES;
+      // chunks fk and fk + 4 of the row's 128 bytes; what lies behind K (and every block behind the last) reads as zeros
+      const uint32_t k0 = (uint32_t)b * FB + fk * 16, k1 = k0 + 64;
+      auto load = [&](__amdgpu_buffer_rsrc_t r, uint32_t row) {
+        const uint4 lo = buf_load16(r, k0 < (uint32_t)a.K ? row + k0 : BUF_OOR), hi = buf_load16(r, k1 < (uint32_t)a.K ? row + k1 : BUF_OOR);
+        return __builtin_shufflevector(__builtin_bit_cast(i32x4_t, lo), __builtin_bit_cast(i32x4_t, hi), 0, 1, 2, 3, 4, 5, 6, 7);
+      };
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) fw[d][j] = load(rw, (16 * j + frow) * (uint32_t)a.w_row);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[d][i] = load(rx, (16 * i + frow) * (uint32_t)a.x_row);
+      const int bs = min(b, a.blocks - 1);
+      sw[d] = ws[bs * a.ws_blk];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) sx[d][i] = a.xs[(int64_t)bs * a.xs_blk + m0 + min((int)(16 * i + frow), rows - 1)];
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      if (b0 + d * FEW_WAVES >= a.blocks) break;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const float s = sx[d][i] * sw[d];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const f32x4_t p = mfma_f8(fw[d][j], fx[d][i], f32x4_t{0, 0, 0, 0});
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(p[e], s, acc[i][j][e]);
+        }
+      }
+    }
+  }
+  // [wave][tile][lane]; the tiles are then dealt to the waves
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      *reinterpret_cast<f32x4_t*>(lds + ((wave * MT * NJ + i * NJ + j) * 64 + lane) * 4) = acc[i][j];
+  __syncthreads();
+  for (int u = (int)wave; u < MT * NJ; u += FEW_WAVES) {
+    f32x4_t y = {0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < FEW_WAVES; ++v) y += *reinterpret_cast<const f32x4_t*>(lds + ((v * MT * NJ + u) * 64 + lane) * 4);
+    const int r = 16 * (u / NJ) + (int)frow, c = 16 * (u % NJ) + 4 * (int)fk;
+    uint16_t* o = a.y + (int64_t)(m0 + r) * a.ldy + n0 + c;
+    const uint32_t lo = pack_bf16x2(y[0], y[1]), hi = pack_bf16x2(y[2], y[3]);
+    if (r >= rows) continue;
+    if (a.y_vec && c + 3 < cols) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
+    } else {
+      const uint16_t v[4] = {(uint16_t)lo, (uint16_t)(lo >> 16), (uint16_t)hi, (uint16_t)(hi >> 16)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < cols) o[e] = v[e];
+    }
+  }
+}
+
+// MT: 16-row tiles at most (grouped: of the plan's tiles of QF_ROW_TILE rows; those with up to 16 rows take
+// half).
+template <int MODE, int MT, int NJ>
+__global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gemm8_few(Gemm8Args a) {
+  __shared__ __attribute__((aligned(16))) float lds[FEW_WAVES * MT * NJ * 256];
+  if (MODE == G8_DENSE) {
+    few_rows<MT, NJ>(a, 0, 0, a.M, lds);
+    return;
+  }
+  const int group = uniform(a.tiles[2 * (int64_t)blockIdx.y]), m0 = uniform(a.tiles[2 * (int64_t)blockIdx.y + 1]);
+  if (group < 0 || group >= a.n_ids || m0 < 0) return;
+  const int rows = uniform(min(QF_ROW_TILE, group_offset(a.offsets, group + 1, a.n) - m0));
+  if (rows <= 0) return;
+  if (MT > 1 && rows > 16) few_rows<MT, NJ>(a, group, m0, rows, lds);
+  else few_rows<1, NJ>(a, group, m0, rows, lds);
 }
 
 bool bad_codes(int64_t K, int64_t ld) { return K < 1 || K % 16 != 0 || ld < K || ld >= QF_FP8_MAX_COLS; }
@@ -403,9 +521,31 @@ int64_t small_tiles(const Gemm8Args& a, int mode) {
   return m * ((a.N + 127) / 128) * (mode == G8_BLOCKS ? a.n_ids : 1);
 }
 
+template <int MODE, int MT>
+hipError_t launch_few(Gemm8Args a, int64_t tiles, int64_t likely, int nj, hipStream_t s) {
+  a.y_vec = a.ldy % 4 == 0 && (uintptr_t)a.y % 8 == 0;
+  // wide workgroups read x less often, but 192 workgroups are wanted
+  while (nj > 1 && (a.N + 16 * nj - 1) / (16 * nj) * likely < 192) nj /= 2;
+  const dim3 g((unsigned)((a.N + 16 * nj - 1) / (16 * nj)), (unsigned)tiles), wg(64 * FEW_WAVES);
+  if (nj == 4) k_gemm8_few<MODE, MT, 4><<<g, wg, 0, s>>>(a);
+  else if (nj == 2) k_gemm8_few<MODE, MT, 2><<<g, wg, 0, s>>>(a);
+  else k_gemm8_few<MODE, MT, 1><<<g, wg, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
-  a.y_vec = a.ldy % 8 == 0 && (uintptr_t)a.y % 16 == 0 && a.N % 8 == 0 && a.ldy < QF_FP8_MAX_COLS ? 2 : 0;
-  if (small_tiles(a, mode) >= 1024 && !getenv("G8S")) return launch_tiles<256, 256, 2, 4>(a, mode, s);
+  // Few rows stream w with columns and blocks split; more take tiles.  Microseconds few / tiles, with 64 rows: 4096 -> 6144
+  // 15.0 / 31.5, 4096 -> 28672 39 / 38, 14336 -> 4096 35 / 106; 128 groups of 2048 -> 1536 with 16 rows each 78 / 93, with 32
+  // 109 / 97.  Columns of a workgroup 16 / 32 / 64: 16 rows of 4096 -> 6144 11.4 / 9.5 / 12.5, 4096 -> 28672 32.5 / 28.7 /
+  // 26.3, 14336 -> 4096 17.7 / 23.7 / 35.9; 128 groups of 2048 -> 1536 with 4 rows each 73 / 66 / 70, with 16 106 / 88 / 78.
+  if (mode == G8_DENSE && a.M <= 64)
+    return a.M <= 16 ? launch_few<G8_DENSE, 1>(a, 1, 1, 4, s) : a.M <= 32 ? launch_few<G8_DENSE, 2>(a, 1, 1, 4, s)
+                                                                          : launch_few<G8_DENSE, 4>(a, 1, 1, 4, s);
+  const int64_t groups = a.M < a.n_ids ? a.M : a.n_ids;
+  if (mode == G8_ROWS && a.M <= 24 * (int64_t)a.n_ids)
+    return launch_few<G8_ROWS, 2>(a, (a.M + QF_ROW_TILE - 1) / QF_ROW_TILE + groups, groups, a.M < 8 * (int64_t)a.n_ids ? 2 : 4, s);
+  a.y_vec = a.ldy % 8 == 0 && (uintptr_t)a.y % 16 == 0 && a.N % 8 == 0 && a.ldy < QF_FP8_MAX_COLS;
+  if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
   return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
 
@@ -439,6 +579,7 @@ qf_status forward(const uint8_t* Xc, int64_t ldx, const float* Xs, int64_t ldxs,
   a.y = Y;
   a.ldy = ldy;
   a.offsets = offsets;
+  a.tiles = tiles;
   a.n_ids = n_ids;
   a.n = (int32_t)M;
   a.M = (int32_t)M;
