@@ -696,25 +696,31 @@ def _out16(t, name, rows, cols, device):
     return t, _mat(t, name)[2]
 
 
+def _positions(plan):
+    if _plan(plan).positions is None:
+        raise ValueError("the plan must be built with positions=True")
+    return plan.positions.data_ptr()
+
+
 def _x_rows(rows, n, rows_per_x):
     if rows_per_x < 1 or rows != (n + rows_per_x - 1) // rows_per_x:
         raise ValueError(f"x has {rows} rows for {n} rows of the plan and rows_per_x={rows_per_x}")
 
 
 def qf_moe_dispatch(X, plan, rows_per_x=1, out=None):
-    """out[p] = X[plan.order[p] // rows_per_x], bf16 [plan.n, H]: rows into the order of the plan's
+    """out[plan.positions[i]] = X[i // rows_per_x], bf16 [plan.n, H]: rows into the order of the plan's
     groups.  Rows behind the last group are left as they were (unspecified where out is new)."""
-    dev = _same_gpu(X, out, _plan(plan).order)
+    positions = _positions(plan)
+    dev = _same_gpu(X, out, plan.order)
     rows, H, ldx = _mat(_bf16(X, "X"), "X")
     _x_rows(rows, plan.n, rows_per_x)
     out, ldo = _out16(out, "out", plan.n, H, X.device)
-    _call(dev, "qf_moe_dispatch", X.data_ptr(), ldx, rows_per_x, plan.order.data_ptr(), plan.n, H, out.data_ptr(), ldo)
+    _call(dev, "qf_moe_dispatch", X.data_ptr(), ldx, rows_per_x, positions, plan.n, H, out.data_ptr(), ldo)
     return out
 
 
 def _combine(plan, R, weights, k):
-    if _plan(plan).positions is None:
-        raise ValueError("the plan must be built with positions=True")
+    _positions(plan)
     if weights is not None:
         if weights.dim() != 2 or k not in (None, weights.shape[1]):
             raise ValueError("weights must have shape [tokens, k]")
@@ -801,23 +807,23 @@ def _scales(t, name, blocks, rows):
 
 def qf_quant_fp8(x, plan=None, rows_per_x=None, codes=None, scales=None):
     """(codes uint8 [rows, cols], scales float32 [ceil(cols / 128), rows]): E4M3 codes of x bf16 in
-    blocks of 128 along its rows.  plan: with rows_per_x, row p is x[plan.order[p] // rows_per_x]
+    blocks of 128 along its rows.  plan: with rows_per_x, row plan.positions[i] is x[i // rows_per_x]
     (rows into expert order on the way); without, x's rows are in that order already.  Rows behind
     the plan's last group are left as they were (unspecified in new outputs)."""
     rows, cols, ldx = _mat(_bf16(x, "x"), "x")
     dev = _same_gpu(x, codes, scales, None if plan is None else _plan(plan).order)
-    order = used = None
+    positions = used = None
     if plan is not None:
         _x_rows(rows, plan.n, 1 if rows_per_x is None else rows_per_x)
         rows = plan.n
         if rows_per_x is None:
             used = plan.offsets.data_ptr() + 4 * plan.n_ids
         else:
-            order = plan.order.data_ptr()
+            positions = _positions(plan)
     elif rows_per_x is not None:
         raise ValueError("rows_per_x needs a plan")
     codes, ldc, scales, lds = _row_codes(rows, cols, x.device, codes, scales)
-    _call(dev, "qf_quant_fp8", x.data_ptr(), ldx, rows, cols, order, rows_per_x or 1, used, codes.data_ptr(), ldc,
+    _call(dev, "qf_quant_fp8", x.data_ptr(), ldx, rows, cols, positions, rows_per_x or 1, used, codes.data_ptr(), ldc,
           scales.data_ptr(), lds)
     return codes, scales
 

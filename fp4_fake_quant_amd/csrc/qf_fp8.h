@@ -154,6 +154,9 @@ __device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, 
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)total);
 }
 
+// Positions that a row is written to by one set of lanes; a row with more is read again.
+constexpr uint32_t SPREAD_MOST = 16;
+
 inline bool misaligned(const void* p, size_t a) { return (uintptr_t)p % a != 0; }
 inline bool plan_sizes_ok(int64_t n, int n_ids) { return n >= 0 && n < QF_ROW_MAX_ROWS && n_ids >= 1 && n_ids <= QF_ROW_MAX_IDS; }
 

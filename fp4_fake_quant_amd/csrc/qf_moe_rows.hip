@@ -1,10 +1,10 @@
-// Rows into expert order and back: dispatch (a gather), combine (a weighted sum over a token's
-// experts) and the gradients of both.
+// Rows into expert order and back: dispatch, combine (a weighted sum over a token's experts) and the
+// gradients of both.
 //
 // Nothing is computed that matters for time: each kernel reads every row once and writes every row
-// once, 16 bytes a lane.  Combine and its gradient go through the plan's positions (the inverse of
-// its order), so that a token's sum is formed in registers in a fixed order and no atomics are
-// needed.
+// once, 16 bytes a lane.  All go by token through the plan's positions (the inverse of its order), so
+// that a token's row is read once for all its experts, a token's sum is formed in registers in a
+// fixed order, and no atomics are needed.
 #include "qf_fp8.h"
 
 namespace qf {
@@ -18,7 +18,7 @@ struct MoeRowsArgs {
   const uint16_t* r;        // backward: R
   uint16_t* y;              // dispatch: out; combine: Y; backward: dR (null: not wanted)
   int64_t ldx, ldr, ldy;
-  const int32_t* index;     // order, or positions
+  const int32_t* index;     // positions
   const float* w;           // null: all 1
   float* dw;                // backward, null: not wanted
   int64_t n;                // rows in expert order
@@ -30,17 +30,33 @@ struct MoeRowsArgs {
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
 __device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
+// Lanes of a row of X: read once, written to each position that it has.
 __global__ __launch_bounds__(MR_WG) void k_moe_dispatch(MoeRowsArgs a) {
   const uint32_t lanes = 1u << a.lane_bits, rows = MR_WG >> a.lane_bits;
   const uint32_t first = threadIdx.x & (lanes - 1);
-  for (int64_t p0 = (int64_t)blockIdx.x * rows; p0 < a.n; p0 += (int64_t)gridDim.x * rows) {
-    const int64_t p = p0 + (threadIdx.x >> a.lane_bits);
-    if (p >= a.n) continue;
-    const uint32_t i = (uint32_t)a.index[p];
-    if (i >= (uint32_t)a.n) continue;                       // behind the last group
-    const uint16_t* src = a.x + (int64_t)(i / a.per) * a.ldx;
-    uint16_t* dst = a.y + p * a.ldy;
-    for (uint32_t c = first; c < a.chunks; c += lanes) store16(dst + 8 * c, load16(src + 8 * c));
+  const uint32_t parts = (a.per + SPREAD_MOST - 1) / SPREAD_MOST;
+  const int64_t total = a.tokens * parts;
+  for (int64_t u0 = (int64_t)blockIdx.x * rows; u0 < total; u0 += (int64_t)gridDim.x * rows) {
+    const int64_t u = u0 + (threadIdx.x >> a.lane_bits);
+    if (u >= total) continue;
+    const int64_t t = parts == 1 ? u : u / parts, i0 = t * a.per + (u - t * parts) * SPREAD_MOST;
+    const int64_t end = min((t + 1) * (int64_t)a.per, a.n);
+    const uint32_t mine = end <= i0 ? 0u : (uint32_t)min(end - i0, (int64_t)SPREAD_MOST);
+    const uint16_t* src = a.x + t * a.ldx;
+    for (uint32_t c0 = first; c0 < a.chunks; c0 += 4 * lanes) {
+      uint4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (c0 + q * lanes < a.chunks) v[q] = load16(src + 8 * (c0 + q * lanes));
+      for (uint32_t j = 0; j < mine; ++j) {
+        const uint32_t p = (uint32_t)a.index[i0 + j];
+        if (p >= (uint32_t)a.n) continue;                   // in no group
+        uint16_t* dst = a.y + (int64_t)p * a.ldy;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c0 + q * lanes < a.chunks) store16(dst + 8 * (c0 + q * lanes), v[q]);
+      }
+    }
   }
 }
 
@@ -119,25 +135,27 @@ using namespace qf;
 
 extern "C" {
 
-qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const int32_t* order, int64_t n, int64_t H,
+qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const int32_t* positions, int64_t n, int64_t H,
                           uint16_t* out, int64_t ldo, void* stream) {
   if (n < 0 || n >= QF_ROW_MAX_ROWS || bad_rows(H, ldx) || ldo < H) return QF_ERR_SHAPE;
   if (rows_per_x < 1) return QF_ERR_ARG;
   if (n == 0) return QF_OK;
-  if (!X || !order || !out) return QF_ERR_NULL;
-  if (bad_mat(X, ldx) || bad_mat(out, ldo) || misaligned(order, 4)) return QF_ERR_ALIGN;
+  if (!X || !positions || !out) return QF_ERR_NULL;
+  if (bad_mat(X, ldx) || bad_mat(out, ldo) || misaligned(positions, 4)) return QF_ERR_ALIGN;
   MoeRowsArgs a = {};
   a.x = X;
   a.ldx = ldx;
-  a.index = order;
+  a.index = positions;
   a.n = n;
   a.per = (uint32_t)(rows_per_x < n ? rows_per_x : n);
+  a.tokens = (n + a.per - 1) / a.per;
   a.chunks = (uint32_t)(H / 8);
   a.lane_bits = lane_bits_of(a.chunks);
   a.y = out;
   a.ldy = ldo;
   const int64_t rows = MR_WG >> a.lane_bits;
-  k_moe_dispatch<<<grid_of((n + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
+  const int64_t units = a.tokens * ((a.per + SPREAD_MOST - 1) / SPREAD_MOST);
+  k_moe_dispatch<<<grid_of((units + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
   return status_of(hipGetLastError());
 }
 

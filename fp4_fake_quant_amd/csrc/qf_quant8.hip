@@ -21,10 +21,10 @@ constexpr int RQ_DEEP = 4;                        // blocks loaded before the fi
 struct RowQuantArgs {
   const uint16_t* x;
   int64_t ldx;
-  const int32_t* order;     // null: row p of x
+  const int32_t* positions; // where each row of x goes (null: row p to p)
   const int32_t* used;      // null, or the rows in use
-  int64_t rows;
-  uint32_t per;             // rows in expert order per row of x
+  int64_t rows, n;          // rows (of x, times parts); positions
+  uint32_t per, parts;      // positions per row of x, and in how many parts it is taken
   uint32_t cols, blocks, part;   // part: blocks of a workgroup
   uint8_t* codes;
   int64_t ldc;
@@ -60,22 +60,25 @@ __device__ __forceinline__ float exp_neg(float g) {
 }
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(g)); }
 
-template <bool GATED>
+// SPREAD: row t of x has the `per` positions from positions[t * per] on; it is quantized once and written to
+// each.
+template <bool GATED, bool SPREAD>
 __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
   const uint32_t l = threadIdx.x & (RQ_LANES - 1), unit = threadIdx.x / RQ_LANES;
   const int64_t rows = a.used ? (int64_t)min((uint32_t)max(*a.used, 0), (uint32_t)a.rows) : a.rows;
   const uint32_t b0 = blockIdx.y * a.part, b1 = min(b0 + a.part, a.blocks);
   for (int64_t r0 = (int64_t)blockIdx.x * RQ_ROWS; r0 < rows; r0 += (int64_t)gridDim.x * RQ_ROWS) {
-    const int64_t row = r0 + unit;
+    int64_t row = r0 + unit, i0 = 0;
     if (row >= rows) continue;                    // whole units leave, so the eight lanes of a block stay together
-    int64_t src = row;
-    if (a.order) {
-      const uint32_t i = (uint32_t)a.order[row];
-      if (i >= (uint32_t)a.rows) continue;
-      src = i / a.per;
+    uint32_t mine = 1;
+    if constexpr (SPREAD) {
+      const int64_t t = a.parts == 1 ? row : row / a.parts;
+      i0 = t * a.per + (row - t * a.parts) * SPREAD_MOST;
+      const int64_t end = min((t + 1) * (int64_t)a.per, a.n);
+      mine = end <= i0 ? 0u : (uint32_t)min(end - i0, (int64_t)SPREAD_MOST);
+      row = t;
     }
-    const uint16_t* x = a.x + src * a.ldx;
-    uint8_t* codes = a.codes + row * a.ldc;
+    const uint16_t* x = a.x + row * a.ldx;
     for (uint32_t b = b0; b < b1; b += RQ_DEEP) {
       uint4 w[RQ_DEEP][2], u[GATED ? RQ_DEEP : 1][2];
 #pragma unroll
@@ -89,9 +92,9 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
           u[j][1] = in ? *reinterpret_cast<const uint4*>(x + a.cols + c + 8) : make_uint4(0, 0, 0, 0);
         }
       }
+      float scale[RQ_DEEP];
 #pragma unroll
       for (int j = 0; j < RQ_DEEP; ++j) {
-        if (b + j >= b1) break;
         const uint32_t c = (b + j) * FB + l * 16;
         float v[16];
         f32_of(w[j][0], v);
@@ -111,20 +114,33 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
           top = umax(amax_bits8(w[j][0]), amax_bits8(w[j][1])) << 16;
         }
         const F8Scale s = f8_scale(max8lanes(top));
-        if (l == 0) a.scales[(int64_t)(b + j) * a.lds + row] = s.scale;
-        if (c < a.cols) {
-          if constexpr (GATED) {
-            if (a.y) {
-              uint4* y = reinterpret_cast<uint4*>(a.y + row * a.ldy + c);
-              y[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-              y[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
-            }
+        scale[j] = s.scale;
+        if constexpr (GATED) {
+          if (a.y && b + j < b1 && c < a.cols) {
+            uint4* y = reinterpret_cast<uint4*>(a.y + row * a.ldy + c);
+            y[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            y[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
           }
-          uint32_t o[4];
+        }
+        uint32_t o[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = f8_pack4(v[4 * e] * s.inv, v[4 * e + 1] * s.inv, v[4 * e + 2] * s.inv, v[4 * e + 3] * s.inv);
-          *reinterpret_cast<uint4*>(codes + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int e = 0; e < 4; ++e)
+          o[e] = f8_pack4(v[4 * e] * s.inv, v[4 * e + 1] * s.inv, v[4 * e + 2] * s.inv, v[4 * e + 3] * s.inv);
+        w[j][0] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      for (uint32_t k = 0; k < mine; ++k) {
+        int64_t p = row;
+        if constexpr (SPREAD) {
+          const uint32_t at = (uint32_t)a.positions[i0 + k];
+          if (at >= (uint32_t)a.n) continue;      // in no group
+          p = at;
+        }
+        uint8_t* codes = a.codes + p * a.ldc;
+#pragma unroll
+        for (int j = 0; j < RQ_DEEP; ++j) {
+          const uint32_t c = (b + j) * FB + l * 16;
+          if (b + j < b1 && c < a.cols) *reinterpret_cast<uint4*>(codes + c) = w[j][0];
+          if (b + j < b1 && l == 0) a.scales[(int64_t)(b + j) * a.lds + p] = scale[j];
         }
       }
     }
@@ -140,8 +156,9 @@ hipError_t launch_rows(RowQuantArgs a, bool gated, hipStream_t s) {
   parts = parts < 1 ? 1 : parts > most ? most : parts;
   a.part = (uint32_t)((most + parts - 1) / parts * RQ_DEEP);
   const dim3 g((unsigned)(tiles < Q8_MAX_GRID / parts ? tiles : Q8_MAX_GRID / parts), (a.blocks + a.part - 1) / a.part);
-  if (gated) k_quant8_rows<true><<<g, Q8_WG, 0, s>>>(a);
-  else k_quant8_rows<false><<<g, Q8_WG, 0, s>>>(a);
+  if (gated) k_quant8_rows<true, false><<<g, Q8_WG, 0, s>>>(a);
+  else if (a.positions) k_quant8_rows<false, true><<<g, Q8_WG, 0, s>>>(a);
+  else k_quant8_rows<false, false><<<g, Q8_WG, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -366,11 +383,11 @@ unsigned grid_of(int64_t units) { return (unsigned)(units < Q8_MAX_GRID ? units 
 qf_status rows_args(const RowQuantArgs& a, int64_t rows, int64_t cols, int64_t wide, int64_t rows_per_x) {
   if (rows < 0 || rows >= QF_ROW_MAX_ROWS || bad_cols(cols, 16) || a.ldx < wide || a.ldc < cols || a.lds < rows)
     return QF_ERR_SHAPE;
-  if (a.order && rows_per_x < 1) return QF_ERR_ARG;
+  if (a.positions && rows_per_x < 1) return QF_ERR_ARG;
   if (rows == 0) return QF_OK;
   if (!a.x || !a.codes || !a.scales) return QF_ERR_NULL;
   if (misaligned(a.x, 16) || a.ldx % 8 || misaligned(a.codes, 16) || a.ldc % 16 || misaligned(a.scales, 4) ||
-      misaligned(a.order, 4) || misaligned(a.used, 4))
+      misaligned(a.positions, 4) || misaligned(a.used, 4))
     return QF_ERR_ALIGN;
   return QF_OK;
 }
@@ -382,22 +399,25 @@ using namespace qf;
 
 extern "C" {
 
-qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* order, int64_t rows_per_x,
-                       const int32_t* d_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream) {
+qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* positions,
+                       int64_t rows_per_x, const int32_t* d_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                       void* stream) {
   RowQuantArgs a = {};
   a.x = x;
   a.ldx = ldx;
-  a.order = order;
-  a.used = d_rows;
+  a.positions = positions;
+  a.used = positions ? nullptr : d_rows;
   a.codes = codes;
   a.ldc = ldc;
   a.scales = scales;
   a.lds = lds;
   const qf_status st = rows_args(a, rows, cols, cols, rows_per_x);
   if (st != QF_OK || rows == 0) return st;
-  a.rows = rows;
+  a.n = rows;
+  a.per = (uint32_t)(positions && rows_per_x < rows ? rows_per_x : positions ? rows : 1);
+  a.parts = (a.per + SPREAD_MOST - 1) / SPREAD_MOST;
+  a.rows = (rows + a.per - 1) / a.per * a.parts;
   a.cols = (uint32_t)cols;
-  a.per = (uint32_t)(rows_per_x < rows ? rows_per_x : rows);
   return status_of(launch_rows(a, false, (hipStream_t)stream));
 }
 

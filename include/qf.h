@@ -474,14 +474,14 @@ qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_
 /* ------------------------------------------- rows into expert order and back ---- */
 /* Tokens and experts: row i = t * k + j of a plan stands for expert j of token t (the ids that
  * qf_moe_route writes), position p of the plan for row order[p].  bf16 matrices with rows of H:
- *   dispatch           out[p] = X[order[p] / rows_per_x]
+ *   dispatch           out[positions[i]] = X[i / rows_per_x]
  *   combine            Y[t] = sum_j weights[t, j] R[positions[t k + j]]
  *   combine_backward   dR[p] = weights[t, j] dY[t] for p = positions[t k + j];
  *                      dW[t, j] = <R[p], dY[t]>
- * combine without weights (NULL: all 1) is the gradient of dispatch.  An order entry outside [0, n)
- * (behind the last group) leaves its row of out as it was, likewise rows of dR that no position
- * names; a positions entry outside [0, tokens * k) adds nothing to Y, whatever its weight, and gets
- * dW 0.  positions must name no row twice (a plan's do not).  Sums in fp32, j (dW: the columns) in a fixed order, one rounding to bf16:
+ * combine without weights (NULL: all 1) is the gradient of dispatch.  A positions entry outside
+ * [0, n) (a row in no group) is not written by dispatch, adds nothing to Y, whatever its weight, and
+ * gets dW 0; rows of out and dR that no entry names (those behind the last group) stay as they were.
+ * positions must name no row twice (a plan's do not).  Sums in fp32, j (dW: the columns) in a fixed order, one rounding to bf16:
  *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) gamma_k sum_j |w| |r|;  |dr - w dy| <= (2^-8 + 2^-24) |w dy|;
  *   |dw - dw_exact| <= gamma_H sum |r| |dy|;  gamma_n = n 2^-24 / (1 - n 2^-24).
  * Values that are NaN or infinite follow the formulas.  dR or dW may be NULL to skip it (R is
@@ -491,7 +491,7 @@ qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_
  * 16-byte aligned, leading dimensions multiples of 8 (QF_ERR_ALIGN).  X has ceil(n / rows_per_x)
  * rows, R and dR tokens * k.  Outputs must not overlap inputs.  One launch, no workspace. */
 #define QF_MOE_MAX_COLS (1 << 22)
-qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const int32_t* order, int64_t n, int64_t H,
+qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, const int32_t* positions, int64_t n, int64_t H,
                           uint16_t* out, int64_t ldo, void* stream);
 qf_status qf_moe_combine(const uint16_t* R, int64_t ldr, const int32_t* positions, const float* weights, int64_t tokens,
                          int64_t k, int64_t H, uint16_t* Y, int64_t ldy, void* stream);
@@ -725,13 +725,15 @@ qf_status qf_gemm_nvfp4(const uint16_t* X, int64_t ldx, const uint16_t* W, int64
  *
  * qf_quant_fp8         rows: codes [rows][ldc], block b of row p: columns 128 b ..; its scale is
  *   scales[b * lds + p] (block-major: the product reads one block's scales of many rows at a time).
- *   order NULL: row p of x.  Else row order[p] / rows_per_x of x (a plan's order: rows into expert
- *   order on the way); an entry outside [0, rows) leaves row p's codes and scales as they were.  d_rows (device int32, or NULL;
- *   e.g. a plan's offsets + n_ids): rows at and past *d_rows are left as they were.  cols a multiple of 16.
+ *   positions NULL: row p of x.  Else (a plan's) row i / rows_per_x of x goes to p = positions[i] for i in [0, rows),
+ *   rows into expert order on the way: each row of x is quantized once; entries outside [0, rows) are skipped,
+ *   and rows that no entry names stay as they were.  d_rows (device int32, or NULL; read without positions,
+ *   e.g. a plan's offsets + n_ids): rows at and past *d_rows stay as they were.  cols a multiple of 16.
  * qf_quant_fp8_panels  blocks of 128 rows of one group, transposed: codes [panels][cols][128], scales
  *   [panels][cols].  offsets (a plan's, n_ids groups) cut the rows into groups, each starts a panel
  *   of its own and the last one of a group is filled up with code 0; offsets NULL (n_ids 1): one group of
- *   all rows.  order, rows_per_x as above (an entry outside [0, rows) counts as a row of zeros).
+ *   all rows.  order NULL: position p holds row p of x; else (a plan's) row order[p] / rows_per_x, an entry
+ *   outside [0, rows) a row of zeros.
  *   qf_fp8_panels(rows, n_ids) panels always suffice; those behind the last are left as they were.  cols a multiple of 8.
  * qf_quant_fp8_tiles   128 x 128 tiles of count stacked matrices x [count][rows][ldx]: codes
  *   [count][rows][cols], scales [count][ceil(rows / 128)][ceil(cols / 128)], and the transpose, of
@@ -743,13 +745,14 @@ qf_status qf_gemm_nvfp4(const uint16_t* X, int64_t ldx, const uint16_t* W, int64
  * qf_swiglu_backward   dh [rows, 2 cols] = [da u s (1 + g (1 - s)), da g s], s = 1 / (1 + exp(-g)), bf16,
  *   fp32 arithmetic: error at most 2^-8 of the value plus 32 2^-24 |da u| (1 + |g|) or |da g|.
  * Limits: rows in [0, QF_ROW_MAX_ROWS) (tiles: below QF_FP8_MAX_COLS), cols in [1, QF_FP8_MAX_COLS), leading
- * dimensions at least the row length, lds >= rows (QF_ERR_SHAPE); rows_per_x >= 1 with order, n_ids in
+ * dimensions at least the row length, lds >= rows (QF_ERR_SHAPE); rows_per_x >= 1 with positions or order, n_ids in
  * 1..QF_ROW_MAX_IDS (QF_ERR_ARG); bf16 arrays 16-byte aligned with leading dimensions multiples of 8, codes 16-byte aligned with
  * ldc a multiple of 16 (QF_ERR_ALIGN).  Outputs must not overlap inputs.  One launch, no workspace. */
 #define QF_FP8_BLOCK 128
 #define QF_FP8_MAX_COLS (1 << 22)
-qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* order, int64_t rows_per_x,
-                       const int32_t* d_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds, void* stream);
+qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* positions,
+                       int64_t rows_per_x, const int32_t* d_rows, uint8_t* codes, int64_t ldc, float* scales, int64_t lds,
+                       void* stream);
 int64_t qf_fp8_panels(int64_t rows, int n_ids);           /* 0 for invalid arguments */
 qf_status qf_quant_fp8_panels(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* order,
                               int64_t rows_per_x, const int32_t* offsets, int n_ids, uint8_t* codes, float* scales,

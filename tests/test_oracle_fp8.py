@@ -117,9 +117,9 @@ NULL, SHAPE, ALIGN, ARG = 1, 2, 3, 7
 
 
 def call(name, good, **bad):
-    order = {"dispatch": "X ldx per order n H out ldo", "combine": "R ldr pos w T k H Y ldy",
+    order = {"dispatch": "X ldx per pos n H out ldo", "combine": "R ldr pos w T k H Y ldy",
              "combine_backward": "dY lddy R ldr pos w T k H dR lddr dW",
-             "quant_fp8": "x ldx rows cols order per used codes ldc scales lds",
+             "quant_fp8": "x ldx rows cols pos per used codes ldc scales lds",
              "quant_fp8_panels": "x ldx rows cols order per offsets n_ids codes scales",
              "quant_fp8_tiles": "x ldx count rows cols codes scales codes_t scales_t",
              "swiglu_quant_fp8": "x ldx rows cols used codes ldc scales lds y ldy",
@@ -135,9 +135,9 @@ def call(name, good, **bad):
     return f(*args, None)
 
 
-DISPATCH = dict(X=A, ldx=64, per=2, order=A, n=8, H=64, out=A, ldo=64)
+DISPATCH = dict(X=A, ldx=64, per=2, pos=A, n=8, H=64, out=A, ldo=64)
 COMBINE = dict(R=A, ldr=64, pos=A, w=A, T=4, k=2, H=64, Y=A, ldy=64, dY=A, lddy=64, dR=A, lddr=64, dW=A)
-QUANT = dict(x=A, ldx=64, rows=8, cols=64, order=0, per=1, used=0, codes=A, ldc=64, scales=A, lds=8, y=0, ldy=64)
+QUANT = dict(x=A, ldx=64, rows=8, cols=64, pos=0, per=1, used=0, codes=A, ldc=64, scales=A, lds=8, y=0, ldy=64)
 GATE = dict(QUANT, ldx=128)
 PANELS = dict(x=A, ldx=64, rows=8, cols=64, order=0, per=1, offsets=A, n_ids=3, codes=A, scales=A)
 TILES = dict(x=A, ldx=64, count=2, rows=32, cols=64, codes=A, scales=A, codes_t=A, scales_t=A)
@@ -147,12 +147,12 @@ WGRAD = dict(Dc=A, Ds=A, Xc=A, Xs=A, offsets=A, n_ids=2, rows=8, dW=A, N=32, K=6
 
 
 @pytest.mark.parametrize("name,good,bad,want", [
-    ("dispatch", DISPATCH, dict(X=0), NULL), ("dispatch", DISPATCH, dict(order=0), NULL), ("dispatch", DISPATCH, dict(out=0), NULL),
+    ("dispatch", DISPATCH, dict(X=0), NULL), ("dispatch", DISPATCH, dict(pos=0), NULL), ("dispatch", DISPATCH, dict(out=0), NULL),
     ("dispatch", DISPATCH, dict(H=60), SHAPE), ("dispatch", DISPATCH, dict(H=0), SHAPE), ("dispatch", DISPATCH, dict(ldx=56), SHAPE),
     ("dispatch", DISPATCH, dict(ldo=56), SHAPE), ("dispatch", DISPATCH, dict(n=-1), SHAPE), ("dispatch", DISPATCH, dict(n=1 << 30), SHAPE),
     ("dispatch", DISPATCH, dict(H=1 << 22, ldx=1 << 22, ldo=1 << 22), SHAPE), ("dispatch", DISPATCH, dict(per=0), ARG),
     ("dispatch", DISPATCH, dict(X=A + 8), ALIGN), ("dispatch", DISPATCH, dict(ldx=68), ALIGN), ("dispatch", DISPATCH, dict(ldo=68), ALIGN),
-    ("dispatch", DISPATCH, dict(order=A + 2), ALIGN), ("dispatch", DISPATCH, dict(out=A + 8), ALIGN),
+    ("dispatch", DISPATCH, dict(pos=A + 2), ALIGN), ("dispatch", DISPATCH, dict(out=A + 8), ALIGN),
     ("combine", COMBINE, dict(R=0), NULL), ("combine", COMBINE, dict(pos=0), NULL), ("combine", COMBINE, dict(Y=0), NULL),
     ("combine", COMBINE, dict(k=0), ARG), ("combine", COMBINE, dict(T=-1), SHAPE), ("combine", COMBINE, dict(T=1 << 29, k=2), SHAPE),
     ("combine", COMBINE, dict(k=1 << 40), ARG), ("combine", COMBINE, dict(H=12), SHAPE), ("combine", COMBINE, dict(ldr=56), SHAPE),
@@ -165,7 +165,7 @@ WGRAD = dict(Dc=A, Ds=A, Xc=A, Xs=A, offsets=A, n_ids=2, rows=8, dW=A, N=32, K=6
     ("quant_fp8", QUANT, dict(x=0), NULL), ("quant_fp8", QUANT, dict(codes=0), NULL), ("quant_fp8", QUANT, dict(scales=0), NULL),
     ("quant_fp8", QUANT, dict(cols=56), SHAPE), ("quant_fp8", QUANT, dict(cols=0), SHAPE), ("quant_fp8", QUANT, dict(lds=7), SHAPE),
     ("quant_fp8", QUANT, dict(ldc=48), SHAPE), ("quant_fp8", QUANT, dict(ldc=72), ALIGN), ("quant_fp8", QUANT, dict(ldx=66), ALIGN),
-    ("quant_fp8", QUANT, dict(rows=-1), SHAPE), ("quant_fp8", QUANT, dict(order=A, per=0), ARG), ("quant_fp8", QUANT, dict(codes=A + 8), ALIGN),
+    ("quant_fp8", QUANT, dict(rows=-1), SHAPE), ("quant_fp8", QUANT, dict(pos=A, per=0), ARG), ("quant_fp8", QUANT, dict(codes=A + 8), ALIGN),
     ("quant_fp8", QUANT, dict(used=A + 2), ALIGN), ("quant_fp8", QUANT, dict(scales=A + 2), ALIGN),
     ("quant_fp8_panels", PANELS, dict(x=0), NULL), ("quant_fp8_panels", PANELS, dict(codes=0), NULL), ("quant_fp8_panels", PANELS, dict(cols=60), SHAPE),
     ("quant_fp8_panels", PANELS, dict(n_ids=0), ARG), ("quant_fp8_panels", PANELS, dict(n_ids=1025), ARG),
