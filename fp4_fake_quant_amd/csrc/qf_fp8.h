@@ -4,6 +4,8 @@
 #include "qf_device.h"
 #include "qf_kernels.h"
 
+#include <type_traits>
+
 namespace qf {
 
 constexpr int FB = QF_FP8_BLOCK;
@@ -23,11 +25,11 @@ __device__ __forceinline__ F8Scale f8_scale(uint32_t top) {
   return o;
 }
 
-// Four codes of y[0..3] (already times inv): round to nearest even (v_cvt_pk_fp8_f32), at most 448.
-__device__ __forceinline__ float f8_clamp(float y) { return __builtin_amdgcn_fmed3f(y, -F8_TOP, F8_TOP); }
+// Four codes of y[0..3] (already times inv, so at most a rounding past 448, which rounds back to it):
+// v_cvt_pk_fp8_f32, to nearest even.
 __device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(f8_clamp(a), f8_clamp(b), 0, false);
-  v = __builtin_amdgcn_cvt_pk_fp8_f32(f8_clamp(c), f8_clamp(d), v, true);
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
   return (uint32_t)v;
 }
 
@@ -152,6 +154,27 @@ __device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, 
     sum += units_of(group_offset(offsets, i, n), group_offset(offsets, i + 1, n), unit);
   wave_before(sum, &total);
   return (uint32_t)__builtin_amdgcn_readfirstlane((int)total);
+}
+
+// 16 bytes, past the caches (NT) where they will not be read from there again.
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, uint4 v) {
+  u32x4_t* q = (u32x4_t*)p;
+  if constexpr (NT) __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), q);
+  else *q = __builtin_bit_cast(u32x4_t, v);
+}
+__device__ __forceinline__ uint4 load16(const void* p) { return *(const uint4*)p; }
+__device__ __forceinline__ uint4 load16_nt(const void* p) {
+  return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4_t*)p));
+}
+// Outputs of this many bytes and more are stored past the caches: the 256 MiB behind the L2s hold what comes
+// after them better.
+constexpr int64_t NT_BYTES = 64 << 20;
+// Calls f(std::true_type) or f(std::false_type).
+template <typename F>
+void with_nt(bool nt, F f) {
+  if (nt) f(std::integral_constant<bool, true>());
+  else f(std::integral_constant<bool, false>());
 }
 
 // Positions that a row is written to by one set of lanes; a row with more is read again.

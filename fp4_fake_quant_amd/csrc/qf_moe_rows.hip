@@ -27,10 +27,8 @@ struct MoeRowsArgs {
   uint32_t lane_bits;       // log2 of the lanes that share a row
 };
 
-__device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void store16(uint16_t* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
-
 // Lanes of a row of X: read once, written to each position that it has.
+template <bool NT>
 __global__ __launch_bounds__(MR_WG) void k_moe_dispatch(MoeRowsArgs a) {
   const uint32_t lanes = 1u << a.lane_bits, rows = MR_WG >> a.lane_bits;
   const uint32_t first = threadIdx.x & (lanes - 1);
@@ -54,38 +52,53 @@ __global__ __launch_bounds__(MR_WG) void k_moe_dispatch(MoeRowsArgs a) {
         uint16_t* dst = a.y + (int64_t)p * a.ldy;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (c0 + q * lanes < a.chunks) store16(dst + 8 * (c0 + q * lanes), v[q]);
+          if (c0 + q * lanes < a.chunks) store16<NT>(dst + 8 * (c0 + q * lanes), v[q]);
       }
     }
   }
 }
 
+template <bool NT>
 __global__ __launch_bounds__(MR_WG) void k_moe_combine(MoeRowsArgs a) {
+  constexpr int DEEP = 8;                                   // rows loaded before the first is added
   const int64_t total = a.tokens * a.chunks;
   for (int64_t u = (int64_t)blockIdx.x * MR_WG + threadIdx.x; u < total; u += (int64_t)gridDim.x * MR_WG) {
     const int64_t t = u / a.chunks;
     const uint32_t c = (uint32_t)(u - t * a.chunks);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (uint32_t j = 0; j < a.per; ++j) {
-      const int64_t i = t * a.per + j;
-      const uint32_t p = (uint32_t)a.index[i];
-      if (p >= (uint32_t)a.n) continue;                     // no expert: contributes nothing, whatever its weight
-      const float w = a.w ? a.w[i] : 1.0f;
-      const uint4 v = load16(a.x + (int64_t)p * a.ldx + 8 * c);
-      const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    for (uint32_t j0 = 0; j0 < a.per; j0 += DEEP) {
+      uint32_t p[DEEP];
+      float w[DEEP];
+      uint4 v[DEEP];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[2 * e] = __builtin_fmaf(w, bf16_lo(q[e]), acc[2 * e]);
-        acc[2 * e + 1] = __builtin_fmaf(w, bf16_hi(q[e]), acc[2 * e + 1]);
+      for (int j = 0; j < DEEP; ++j) {
+        const int64_t i = t * a.per + j0 + j;
+        p[j] = j0 + j < a.per ? (uint32_t)a.index[i] : 0xFFFFFFFFu;
+        w[j] = j0 + j < a.per && a.w ? a.w[i] : 1.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j)
+        if (p[j] < (uint32_t)a.n) v[j] = load16_nt(a.x + (int64_t)p[j] * a.ldx + 8 * c);
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j) {
+        if (p[j] >= (uint32_t)a.n) continue;                // no expert: adds nothing, whatever its weight
+        const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc[2 * e] = __builtin_fmaf(w[j], bf16_lo(q[e]), acc[2 * e]);
+          acc[2 * e + 1] = __builtin_fmaf(w[j], bf16_hi(q[e]), acc[2 * e + 1]);
+        }
       }
     }
-    store16(a.y + t * a.ldy + 8 * c, make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                                 pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])));
+    store16<NT>(a.y + t * a.ldy + 8 * c, make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7])));
   }
 }
 
 // Lanes of one pair (token, expert) after another; a pair's dot product is joined between its lanes.
+template <bool NT>
 __global__ __launch_bounds__(MR_WG) void k_moe_combine_backward(MoeRowsArgs a) {
+  constexpr int DEEP = 4;
   const uint32_t lanes = 1u << a.lane_bits, rows = MR_WG >> a.lane_bits;
   const uint32_t first = threadIdx.x & (lanes - 1);
   for (int64_t i0 = (int64_t)blockIdx.x * rows; i0 < a.n; i0 += (int64_t)gridDim.x * rows) {
@@ -95,24 +108,32 @@ __global__ __launch_bounds__(MR_WG) void k_moe_combine_backward(MoeRowsArgs a) {
     float dot = 0.0f;
     if (in) {
       const float w = a.w ? a.w[i] : 1.0f;
-      const uint16_t* dy = a.x + (int64_t)((uint64_t)i / a.per) * a.ldx;
-      for (uint32_t c = first; c < a.chunks; c += lanes) {
-        const uint4 g = load16(dy + 8 * c);
-        const uint32_t q[4] = {g.x, g.y, g.z, g.w};
-        if (a.dw) {
-          const uint4 v = load16(a.r + (int64_t)p * a.ldr + 8 * c);
-          const uint32_t s[4] = {v.x, v.y, v.z, v.w};
+      const uint16_t* dy = a.x + (int64_t)((uint32_t)i / a.per) * a.ldx;
+      const uint16_t* r = a.r + (int64_t)p * a.ldr;
+      uint16_t* y = a.y + (int64_t)p * a.ldy;
+      for (uint32_t c0 = first; c0 < a.chunks; c0 += DEEP * lanes) {
+        uint4 g[DEEP], v[DEEP];
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+          const uint32_t c = c0 + d * lanes;
+          g[d] = v[d] = make_uint4(0, 0, 0, 0);
+          if (c < a.chunks) {
+            g[d] = load16(dy + 8 * c);
+            if (a.dw) v[d] = load16_nt(r + 8 * c);
+          }
+        }
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+          const uint32_t c = c0 + d * lanes;
+          const uint32_t q[4] = {g[d].x, g[d].y, g[d].z, g[d].w}, s[4] = {v[d].x, v[d].y, v[d].z, v[d].w};
+          uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             dot = __builtin_fmaf(bf16_lo(q[e]), bf16_lo(s[e]), dot);
             dot = __builtin_fmaf(bf16_hi(q[e]), bf16_hi(s[e]), dot);
+            o[e] = pack_bf16x2(w * bf16_lo(q[e]), w * bf16_hi(q[e]));
           }
-        }
-        if (a.y) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack_bf16x2(w * bf16_lo(q[e]), w * bf16_hi(q[e]));
-          store16(a.y + (int64_t)p * a.ldy + 8 * c, make_uint4(o[0], o[1], o[2], o[3]));
+          if (a.y && c < a.chunks) store16<NT>(y + 8 * c, make_uint4(o[0], o[1], o[2], o[3]));
         }
       }
     }
@@ -155,7 +176,9 @@ qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, co
   a.ldy = ldo;
   const int64_t rows = MR_WG >> a.lane_bits;
   const int64_t units = a.tokens * ((a.per + SPREAD_MOST - 1) / SPREAD_MOST);
-  k_moe_dispatch<<<grid_of((units + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
+  with_nt(n * H * 2 >= NT_BYTES, [&](auto nt) {
+    k_moe_dispatch<decltype(nt)::value><<<grid_of((units + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
+  });
   return status_of(hipGetLastError());
 }
 
@@ -183,7 +206,9 @@ qf_status qf_moe_combine(const uint16_t* R, int64_t ldr, const int32_t* position
   a.chunks = (uint32_t)(H / 8);
   a.y = Y;
   a.ldy = ldy;
-  k_moe_combine<<<grid_of((tokens * a.chunks + MR_WG - 1) / MR_WG), MR_WG, 0, (hipStream_t)stream>>>(a);
+  with_nt(tokens * H * 2 >= NT_BYTES, [&](auto nt) {
+    k_moe_combine<decltype(nt)::value><<<grid_of((tokens * a.chunks + MR_WG - 1) / MR_WG), MR_WG, 0, (hipStream_t)stream>>>(a);
+  });
   return status_of(hipGetLastError());
 }
 
@@ -214,7 +239,9 @@ qf_status qf_moe_combine_backward(const uint16_t* dY, int64_t lddy, const uint16
   a.ldy = lddr;
   a.dw = dW;
   const int64_t rows = MR_WG >> a.lane_bits;
-  k_moe_combine_backward<<<grid_of((a.n + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
+  with_nt(a.n * H * 2 >= NT_BYTES, [&](auto nt) {
+    k_moe_combine_backward<decltype(nt)::value><<<grid_of((a.n + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
+  });
   return status_of(hipGetLastError());
 }
 

@@ -49,25 +49,28 @@ __device__ __forceinline__ uint32_t max8lanes(uint32_t m) {
   return umax(m, dpp_hmirror(m));
 }
 
-// exp(-g) to within a few units of rounding: the product with log2 e in two parts, v_exp_f32 for the first.
-__device__ __forceinline__ float exp_neg(float g) {
-  constexpr float L = 1.44269504088896340736f, LL = (float)(1.44269504088896340736 - (double)1.44269504088896340736f);
-  const float t = -g * L;
-  const float rest = __builtin_fmaf(-g, L, -t) - g * LL;
-  const float e = __builtin_amdgcn_exp2f(t);
-  // far out e is 0 or infinite and the correction has no say
-  return fabsf(t) < 126.0f ? __builtin_fmaf(e, rest * 0.693147180559945309f, e) : e;
+// 1 / (1 + exp(-g)) of a bf16 g.  log2 e is taken in two parts, the first of 16 bits, so that its product
+// with g is exact, and cut off rather than rounded, so that the second part's correction m of exp(-g)
+// (1 + m, |m| < 2^-10 where the result is not 0) is not negative where exp(-g) is infinite.
+__device__ __forceinline__ float sigmoid(float g) {
+  constexpr float HI = 0x1.7154p0f;
+  constexpr float LO = (float)((1.44269504088896340736 - (double)HI) * 0.69314718055994530942);
+  static_assert(LO > 0.0f, "cut off, not rounded");
+  const float e = __builtin_amdgcn_exp2f(-g * HI), m = -g * LO;
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, m, e));
 }
-__device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + exp_neg(g)); }
 
 // SPREAD: row t of x has the `per` positions from positions[t * per] on; it is quantized once and written to
 // each.
-template <bool GATED, bool SPREAD>
+template <bool GATED, bool SPREAD, bool NT>
 __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
-  const uint32_t l = threadIdx.x & (RQ_LANES - 1), unit = threadIdx.x / RQ_LANES;
+  // a wave's eight units: one block of eight rows, whose scales lie side by side, or eight blocks of one row, whose
+  // copies then leave in runs of 1 KiB
+  constexpr uint32_t WIDE = SPREAD ? 8 : 1, ROWS = RQ_ROWS / WIDE;
+  const uint32_t l = threadIdx.x & (RQ_LANES - 1), unit = threadIdx.x / RQ_LANES / WIDE, side = threadIdx.x / RQ_LANES % WIDE;
   const int64_t rows = a.used ? (int64_t)min((uint32_t)max(*a.used, 0), (uint32_t)a.rows) : a.rows;
   const uint32_t b0 = blockIdx.y * a.part, b1 = min(b0 + a.part, a.blocks);
-  for (int64_t r0 = (int64_t)blockIdx.x * RQ_ROWS; r0 < rows; r0 += (int64_t)gridDim.x * RQ_ROWS) {
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += (int64_t)gridDim.x * ROWS) {
     int64_t row = r0 + unit, i0 = 0;
     if (row >= rows) continue;                    // whole units leave, so the eight lanes of a block stay together
     uint32_t mine = 1;
@@ -79,12 +82,13 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
       row = t;
     }
     const uint16_t* x = a.x + row * a.ldx;
-    for (uint32_t b = b0; b < b1; b += RQ_DEEP) {
+    for (uint32_t bb = b0; bb < b1; bb += RQ_DEEP * WIDE) {
+      const uint32_t b = bb + side;
       uint4 w[RQ_DEEP][2], u[GATED ? RQ_DEEP : 1][2];
 #pragma unroll
       for (int j = 0; j < RQ_DEEP; ++j) {
-        const uint32_t c = (b + j) * FB + l * 16;
-        const bool in = b + j < b1 && c < a.cols;
+        const uint32_t c = (b + j * WIDE) * FB + l * 16;
+        const bool in = b + j * WIDE < b1 && c < a.cols;
         w[j][0] = in ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
         w[j][1] = in ? *reinterpret_cast<const uint4*>(x + c + 8) : make_uint4(0, 0, 0, 0);
         if constexpr (GATED) {
@@ -95,7 +99,7 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
       float scale[RQ_DEEP];
 #pragma unroll
       for (int j = 0; j < RQ_DEEP; ++j) {
-        const uint32_t c = (b + j) * FB + l * 16;
+        const uint32_t c = (b + j * WIDE) * FB + l * 16;
         float v[16];
         f32_of(w[j][0], v);
         f32_of(w[j][1], v + 8);
@@ -104,19 +108,20 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
           float up[16];
           f32_of(u[j][0], up);
           f32_of(u[j][1], up + 8);
-          top = 0;
+          float most = 0.0f;                       // (a NaN stays)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             v[e] = up[e] * (v[e] * sigmoid(v[e]));
-            top = umax(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+            most = __builtin_elementwise_maximum(most, fabsf(v[e]));
           }
+          top = __float_as_uint(most) & 0x7FFFFFFFu;
         } else {
           top = umax(amax_bits8(w[j][0]), amax_bits8(w[j][1])) << 16;
         }
         const F8Scale s = f8_scale(max8lanes(top));
         scale[j] = s.scale;
         if constexpr (GATED) {
-          if (a.y && b + j < b1 && c < a.cols) {
+          if (a.y && b + j * WIDE < b1 && c < a.cols) {
             uint4* y = reinterpret_cast<uint4*>(a.y + row * a.ldy + c);
             y[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             y[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]));
@@ -138,9 +143,9 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
         uint8_t* codes = a.codes + p * a.ldc;
 #pragma unroll
         for (int j = 0; j < RQ_DEEP; ++j) {
-          const uint32_t c = (b + j) * FB + l * 16;
-          if (b + j < b1 && c < a.cols) *reinterpret_cast<uint4*>(codes + c) = w[j][0];
-          if (b + j < b1 && l == 0) a.scales[(int64_t)(b + j) * a.lds + p] = scale[j];
+          const uint32_t c = (b + j * WIDE) * FB + l * 16;
+          if (b + j * WIDE < b1 && c < a.cols) store16<NT>(codes + c, w[j][0]);
+          if (b + j * WIDE < b1 && l == 0) a.scales[(int64_t)(b + j * WIDE) * a.lds + p] = scale[j];
         }
       }
     }
@@ -149,16 +154,20 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_rows(RowQuantArgs a) {
 
 hipError_t launch_rows(RowQuantArgs a, bool gated, hipStream_t s) {
   a.blocks = (a.cols + FB - 1) / FB;
-  const int64_t tiles = (a.rows + RQ_ROWS - 1) / RQ_ROWS;
+  const int wide = a.positions ? 8 : 1;
+  const int64_t rows = RQ_ROWS / wide, tiles = (a.rows + rows - 1) / rows;
   // few rows: their blocks over several workgroups, until there are 2048
   int64_t parts = (2048 + tiles - 1) / tiles;
-  const int64_t most = (a.blocks + RQ_DEEP - 1) / RQ_DEEP;
+  const int64_t most = (a.blocks + RQ_DEEP * wide - 1) / (RQ_DEEP * wide);
   parts = parts < 1 ? 1 : parts > most ? most : parts;
-  a.part = (uint32_t)((most + parts - 1) / parts * RQ_DEEP);
+  a.part = (uint32_t)((most + parts - 1) / parts * RQ_DEEP * wide);
   const dim3 g((unsigned)(tiles < Q8_MAX_GRID / parts ? tiles : Q8_MAX_GRID / parts), (a.blocks + a.part - 1) / a.part);
-  if (gated) k_quant8_rows<true, false><<<g, Q8_WG, 0, s>>>(a);
-  else if (a.positions) k_quant8_rows<false, true><<<g, Q8_WG, 0, s>>>(a);
-  else k_quant8_rows<false, false><<<g, Q8_WG, 0, s>>>(a);
+  with_nt((a.positions ? a.n : a.rows) * (int64_t)a.cols >= NT_BYTES, [&](auto nt) {
+    constexpr bool NT = decltype(nt)::value;
+    if (gated) k_quant8_rows<true, false, NT><<<g, Q8_WG, 0, s>>>(a);
+    else if (a.positions) k_quant8_rows<false, true, NT><<<g, Q8_WG, 0, s>>>(a);
+    else k_quant8_rows<false, false, NT><<<g, Q8_WG, 0, s>>>(a);
+  });
   return hipGetLastError();
 }
 
@@ -171,6 +180,7 @@ struct GateArgs {
   uint32_t cols, chunks;
 };
 
+template <bool NT>
 __global__ __launch_bounds__(Q8_WG) void k_swiglu_backward(GateArgs a) {
   const int64_t rows = a.used ? (int64_t)min((uint32_t)max(*a.used, 0), (uint32_t)a.rows) : a.rows;
   const int64_t total = rows * a.chunks;
@@ -196,8 +206,8 @@ __global__ __launch_bounds__(Q8_WG) void k_swiglu_backward(GateArgs a) {
       du[e] = pack_bf16x2(u[2 * e], u[2 * e + 1]);
     }
     uint16_t* o = a.dh + row * a.lddh + c;
-    *reinterpret_cast<uint4*>(o) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-    *reinterpret_cast<uint4*>(o + a.cols) = make_uint4(du[0], du[1], du[2], du[3]);
+    store16<NT>(o, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+    store16<NT>(o + a.cols, make_uint4(du[0], du[1], du[2], du[3]));
   }
 }
 
@@ -246,6 +256,7 @@ struct PanelArgs {
   float* scales;            // [blocks][cols]
 };
 
+template <bool NT>
 __global__ __launch_bounds__(Q8_WG) void k_quant8_panels(PanelArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t t[FB * FB];
   __shared__ uint32_t part[4][64];                // column pairs' maxima of each wave
@@ -310,7 +321,7 @@ __global__ __launch_bounds__(Q8_WG) void k_quant8_panels(PanelArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t at = j * Q8_WG + threadIdx.x, col = at >> 3;
-      if (c0 + col < a.cols) *reinterpret_cast<uint4*>(out + at * 16) = square_from_lds(t, col, at & 7);
+      if (c0 + col < a.cols) store16<NT>(out + at * 16, square_from_lds(t, col, at & 7));
     }
     __syncthreads();
   }
@@ -454,7 +465,9 @@ qf_status qf_swiglu_backward(const uint16_t* h, int64_t ldh, const uint16_t* da,
   if (misaligned(h, 16) || ldh % 8 || misaligned(da, 16) || ldda % 8 || misaligned(dh, 16) || lddh % 8 || misaligned(d_rows, 4))
     return QF_ERR_ALIGN;
   GateArgs a = {h, da, dh, ldh, ldda, lddh, rows, d_rows, (uint32_t)cols, (uint32_t)(cols / 8)};
-  k_swiglu_backward<<<grid_of((rows * a.chunks + Q8_WG - 1) / Q8_WG), Q8_WG, 0, (hipStream_t)stream>>>(a);
+  with_nt(rows * cols * 4 >= NT_BYTES, [&](auto nt) {
+    k_swiglu_backward<decltype(nt)::value><<<grid_of((rows * a.chunks + Q8_WG - 1) / Q8_WG), Q8_WG, 0, (hipStream_t)stream>>>(a);
+  });
   return status_of(hipGetLastError());
 }
 
@@ -485,7 +498,9 @@ qf_status qf_quant_fp8_panels(const uint16_t* x, int64_t ldx, int64_t rows, int6
   a.n_ids = n_ids;
   a.codes = codes;
   a.scales = scales;
-  k_quant8_panels<<<grid_of(a.blocks * a.col_tiles), Q8_WG, 0, (hipStream_t)stream>>>(a);
+  with_nt(rows * cols >= NT_BYTES, [&](auto nt) {
+    k_quant8_panels<decltype(nt)::value><<<grid_of(a.blocks * a.col_tiles), Q8_WG, 0, (hipStream_t)stream>>>(a);
+  });
   return status_of(hipGetLastError());
 }
 
