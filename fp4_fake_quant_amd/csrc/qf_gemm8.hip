@@ -487,7 +487,8 @@ template <int MODE, int MT, int NJ>
 __global__ __launch_bounds__(64 * FEW_WAVES, 2) void k_gemm8_few(Gemm8Args a) {
   __shared__ __attribute__((aligned(16))) float lds[FEW_WAVES * MT * NJ * 256];
   if (MODE == G8_DENSE) {
-    few_rows<MT, NJ>(a, 0, 0, a.M, lds);
+    const int m0 = (int)blockIdx.y * 16 * MT;
+    few_rows<MT, NJ>(a, 0, m0, min(16 * MT, a.M - m0), lds);
     return;
   }
   const int group = uniform(a.tiles[2 * (int64_t)blockIdx.y]), m0 = uniform(a.tiles[2 * (int64_t)blockIdx.y + 1]);
@@ -534,13 +535,18 @@ hipError_t launch_few(Gemm8Args a, int64_t tiles, int64_t likely, int nj, hipStr
 }
 
 hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
-  // Few rows stream w with columns and blocks split; more take tiles.  Microseconds few / tiles, with 64 rows: 4096 -> 6144
-  // 15.0 / 31.5, 4096 -> 28672 39 / 38, 14336 -> 4096 35 / 106; 128 groups of 2048 -> 1536 with 16 rows each 78 / 93, with 32
+  // Few rows stream w with columns and blocks split, 64 rows at a time; more take tiles, which need about a microsecond
+  // a block however few they are.  Microseconds few / tiles: 64 rows of 4096 -> 6144 15.0 / 31.5, 4096 -> 28672 39 / 38,
+  // 14336 -> 4096 35 / 106; 128 rows of 4096 -> 6144 19 / 31, 192 35 / 32, 128 of 4096 -> 28672 72 / 38; 256 of 14336 -> 4096
+  // 55 / 106, 512 106 / 106; 512 of 2048 -> 2048 11.3 / 14.4; 128 groups of 2048 -> 1536 with 16 rows each 78 / 93, with 32
   // 109 / 97.  Columns of a workgroup 16 / 32 / 64: 16 rows of 4096 -> 6144 11.4 / 9.5 / 12.5, 4096 -> 28672 32.5 / 28.7 /
   // 26.3, 14336 -> 4096 17.7 / 23.7 / 35.9; 128 groups of 2048 -> 1536 with 4 rows each 73 / 66 / 70, with 16 106 / 88 / 78.
-  if (mode == G8_DENSE && a.M <= 64)
-    return a.M <= 16 ? launch_few<G8_DENSE, 1>(a, 1, 1, 4, s) : a.M <= 32 ? launch_few<G8_DENSE, 2>(a, 1, 1, 4, s)
-                                                                          : launch_few<G8_DENSE, 4>(a, 1, 1, 4, s);
+  if (mode == G8_DENSE) {
+    const int64_t parts = (a.M + 63) / 64;
+    if (a.M <= 16) return launch_few<G8_DENSE, 1>(a, 1, 1, 4, s);
+    if (a.M <= 32) return launch_few<G8_DENSE, 2>(a, 1, 1, 4, s);
+    if (parts == 1 || (parts <= 8 && parts * a.N <= 16384)) return launch_few<G8_DENSE, 4>(a, parts, parts, 4, s);
+  }
   const int64_t groups = a.M < a.n_ids ? a.M : a.n_ids;
   if (mode == G8_ROWS && a.M <= 24 * (int64_t)a.n_ids)
     return launch_few<G8_ROWS, 2>(a, (a.M + QF_ROW_TILE - 1) / QF_ROW_TILE + groups, groups, a.M < 8 * (int64_t)a.n_ids ? 2 : 4, s);
