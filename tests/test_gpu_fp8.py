@@ -290,6 +290,29 @@ def test_gemm(M, N, K):
     assert torch.equal(full[:M, :N], Y) and bool((full[M:] == 7).all()) and bool((full[:, N:] == 7).all())
 
 
+@pytest.mark.parametrize("M,N,K", [(4200, 4100, 144), (4097, 4104, 16), (2100, 8200, 400)])
+def test_gemm_large_tiles(M, N, K):
+    test_gemm(M, N, K)
+
+
+def test_gemm_far_rows():
+    """Codes and results whose offsets pass 2^31."""
+    rng = np.random.default_rng(3)
+    M, N, K, ld = 40000, 264, 48, 1 << 16
+    x, y = torch.zeros((M, ld), dtype=torch.uint8, device="cuda"), torch.zeros((M, ld), dtype=torch.bfloat16, device="cuda")
+    xc = torch.from_numpy(codes_of(rng, (M, K))).cuda()
+    x[:, :K] = xc
+    xs, wc, ws = (torch.from_numpy(v).cuda() for v in (scales_of(rng, (1, M)), codes_of(rng, (N, K)), scales_of(rng, (3, 1))))
+    want = fq.qf_gemm_fp8(xc, xs, wc, ws)
+    fq.qf_gemm_fp8(x[:, :K], xs, wc, ws, Y=y[:, :N])
+    assert torch.equal(y[:, :N], want)
+    last = slice(M - 300, M)
+    Y, P = fp8.product(xc[last].cpu().numpy(), xs[:, last].cpu().numpy(), wc.cpu().numpy(), ws.cpu().numpy())
+    check_product(want[last], Y, P, K)
+    q = fq.qf_quant_fp8(y[:, :N // 16 * 16])
+    assert torch.equal(q[0], fq.qf_quant_fp8(want[:, :N // 16 * 16].contiguous())[0])
+
+
 @pytest.mark.parametrize("M", [3, 40, 200])
 def test_gemm_nan_stays_in_its_rows(M):
     rng = np.random.default_rng(M)
@@ -306,7 +329,7 @@ def test_gemm_nan_stays_in_its_rows(M):
 
 GROUPED = [(1, 1, 1, 8, 16, 0.0), (5, 2, 3, 40, 160, 0.2), (61, 8, 128, 136, 256, 0.0), (64, 8, 16, 520, 272, 0.1), (300, 3, 5, 300, 400, 0.0),
            (100, 4, 1000, 72, 144, 0.1), (9, 4, 1024, 24, 32, 1.1), (700, 2, 2, 264, 640, 0.0), (1, 8, 8, 1536, 2048, 0.0), (400, 8, 6, 384, 128, 0.5),
-           (31, 1, 1, 1000, 1040, 0.0)]
+           (31, 1, 1, 1000, 1040, 0.0), (1500, 2, 5, 4700, 144, 0.1), (2000, 2, 70, 2100, 272, 0.0)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K,none", GROUPED)
@@ -340,7 +363,7 @@ def test_gemm_grouped_one_group_is_the_dense_product(T):
 
 
 WGRAD = [(1, 1, 1, 8, 8, 0.0), (5, 2, 3, 40, 160, 0.2), (64, 8, 16, 136, 264, 0.1), (300, 3, 5, 520, 272, 0.0), (100, 4, 100, 72, 48, 0.1), (9, 4, 1024, 8, 16, 1.1),
-         (700, 2, 2, 264, 128, 0.0)]
+         (700, 2, 2, 264, 128, 0.0), (1000, 2, 45, 640, 648, 0.1), (40, 1, 70, 512, 520, 0.1)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K,none", WGRAD)
@@ -412,7 +435,9 @@ def test_refusals():
     f, b = torch.float32, torch.bfloat16
     plan = fq.qf_row_plan(z(8, t=torch.int32), 2, positions=True)
     X, Xs, W, Ws = z(8, 64), z(1, 8, t=f), z(32, 64), z(1, 1, t=f)
-    for call in (lambda: fq.qf_quant_fp8(z(8, 64, t=b), rows_per_x=1), lambda: fq.qf_quant_fp8(z(7, 64, t=b), plan=plan),
+    bare = fq.qf_row_plan(z(8, t=torch.int32), 2)
+    for call in (lambda: fq.qf_quant_fp8(z(8, 64, t=b), rows_per_x=1), lambda: fq.qf_quant_fp8(z(8, 64, t=b), plan=bare, rows_per_x=1),
+                 lambda: fq.qf_quant_fp8(z(7, 64, t=b), plan=plan),
                  lambda: fq.qf_quant_fp8(z(8, 64, t=b), plan=plan, rows_per_x=2), lambda: fq.qf_quant_fp8(z(8, 64, t=b), codes=z(8, 63)),
                  lambda: fq.qf_quant_fp8(z(8, 64, t=b), scales=z(8, 1, t=f)), lambda: fq.qf_quant_fp8_panels(z(7, 64, t=b), plan=plan),
                  lambda: fq.qf_quant_fp8_panels(z(8, 64, t=b), codes=z(2, 64, 128), plan=plan), lambda: fq.qf_quant_fp8_tiles(z(8, t=b)),

@@ -166,7 +166,7 @@ def test_refusals():
     plan, bare = fq.qf_row_plan(ids, 2, positions=True), fq.qf_row_plan(ids, 2)
     x, r, w = (torch.zeros(s, dtype=t, device="cuda") for s, t in (((4, 16), torch.bfloat16), ((8, 16), torch.bfloat16), ((4, 2), torch.float32)))
     for f in (lambda: fq.qf_moe_dispatch(x, plan, 3), lambda: fq.qf_moe_dispatch(x, plan, 0), lambda: fq.qf_moe_dispatch(x, plan, 2, out=x),
-              lambda: fq.qf_moe_combine(r, bare, w), lambda: fq.qf_moe_combine(r, plan), lambda: fq.qf_moe_combine(r, plan, k=3),
+              lambda: fq.qf_moe_combine(r, bare, w), lambda: fq.qf_moe_dispatch(x, bare, 2), lambda: fq.qf_moe_combine(r, plan), lambda: fq.qf_moe_combine(r, plan, k=3),
               lambda: fq.qf_moe_combine(x, plan, w), lambda: fq.qf_moe_combine(r, plan, w.t()), lambda: fq.qf_moe_combine(r, plan, w, k=4),
               lambda: fq.qf_moe_combine(r, plan, w, Y=r), lambda: fq.qf_moe_combine_backward(r, r, plan, w),
               lambda: fq.qf_moe_combine_backward(x, x, plan, w), lambda: fq.qf_moe_combine_backward(x, r, plan, w, d_rows=x),
