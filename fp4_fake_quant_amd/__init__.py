@@ -690,7 +690,7 @@ def _plan(plan):
 def _out16(t, name, rows, cols, device):
     """A bf16 output [rows, cols] and its row stride."""
     if t is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=device), cols
+        return torch.empty(rows, cols, dtype=torch.bfloat16, device=device), cols
     if tuple(_bf16(t, name).shape) != (rows, cols):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, want {(rows, cols)}")
     return t, _mat(t, name)[2]
@@ -762,7 +762,7 @@ def qf_moe_combine_backward(dY, R, plan, weights=None, k=None, d_rows=None, d_we
             raise ValueError(f"R has shape {tuple(R.shape)}, want {(plan.n, H)}")
         ldr = _mat(R, "R")[2]
         if d_weights is None:
-            d_weights = torch.empty((tokens, k), dtype=torch.float32, device=dY.device)
+            d_weights = torch.empty(tokens, k, dtype=torch.float32, device=dY.device)
         else:
             _dense(d_weights, "d_weights", torch.float32, (tokens, k))
     if want[0]:
@@ -789,11 +789,11 @@ def _row_codes(rows, cols, device, codes, scales):
     """Outputs of a row quantization, with their row strides."""
     blocks = (cols + FP8_BLOCK - 1) // FP8_BLOCK
     if codes is None:
-        codes, ldc = torch.empty((rows, cols), dtype=torch.uint8, device=device), cols
+        codes, ldc = torch.empty(rows, cols, dtype=torch.uint8, device=device), cols
     else:
         ldc = _codes(codes, "codes", (rows, cols))
     if scales is None:
-        return codes, ldc, torch.empty((blocks, rows), dtype=torch.float32, device=device), rows
+        return codes, ldc, torch.empty(blocks, rows, dtype=torch.float32, device=device), rows
     return codes, ldc, scales, _scales(scales, "scales", blocks, rows)
 
 
@@ -849,11 +849,11 @@ def qf_quant_fp8_panels(x, plan=None, rows_per_x=None, codes=None, scales=None):
         raise ValueError("rows_per_x needs a plan")
     panels = lib().qf_fp8_panels(rows, n_ids)
     if codes is None:
-        codes = torch.empty((panels, cols, FP8_BLOCK), dtype=torch.uint8, device=x.device)
+        codes = torch.empty(panels, cols, FP8_BLOCK, dtype=torch.uint8, device=x.device)
     else:
         _dense(codes, "codes", torch.uint8, (panels, cols, FP8_BLOCK))
     if scales is None:
-        scales = torch.empty((panels, cols), dtype=torch.float32, device=x.device)
+        scales = torch.empty(panels, cols, dtype=torch.float32, device=x.device)
     else:
         _dense(scales, "scales", torch.float32, (panels, cols))
     _call(dev, "qf_quant_fp8_panels", x.data_ptr(), ldx, rows, cols, order, rows_per_x or 1, offsets, n_ids,
