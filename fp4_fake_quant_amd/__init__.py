@@ -646,11 +646,16 @@ class RowPlan:
     def __init__(self, n, n_ids, device, positions=False):
         self.n, self.n_ids = n, n_ids
         t, self.ws_bytes = lib().qf_row_plan_tiles(n, n_ids), lib().qf_row_plan_workspace(n, n_ids)
-        sizes = (2 * t, self.ws_bytes // 4, n_ids + 1, n) + ((n,) if positions else ())   # what is 8-byte aligned first
-        tiles, self.ws, self.offsets, self.order, *rest = torch.empty(sum(sizes), dtype=torch.int32,
-                                                                      device=device).split_with_sizes(sizes)
+        sizes = (2 * t, self.ws_bytes // 4, n_ids + 1, n)        # what is 8-byte aligned first
+        if positions:
+            sizes += (n,)
+            tiles, self.ws, self.offsets, self.order, self.positions = torch.empty(
+                sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
+        else:
+            self.positions = None
+            tiles, self.ws, self.offsets, self.order = torch.empty(sum(sizes), dtype=torch.int32,
+                                                                   device=device).split_with_sizes(sizes)
         self.tiles = tiles.view(t, 2)
-        self.positions = rest[0] if positions else None
 
 
 def qf_row_plan(ids, n_ids, plan=None, ws=None, positions=False):

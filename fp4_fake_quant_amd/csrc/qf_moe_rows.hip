@@ -5,6 +5,10 @@
 // once, 16 bytes a lane.  All go by token through the plan's positions (the inverse of its order), so
 // that a token's row is read once for all its experts, a token's sum is formed in registers in a
 // fixed order, and no atomics are needed.
+//
+// Rows of 4096, 8 of 64 experts: 8192 tokens combined in 96 us (593 MB, 6.1 TB/s; 123 with one row at a time in flight,
+// 103 with eight, 97 with stores past the caches), the gradients of 4099 tokens of 6 in 80 us (436 MB, 5.4 TB/s; 98 at first).
+// A decode step takes what its call takes (7.8 us from Python, kernel 3.5).
 #include "qf_fp8.h"
 
 namespace qf {

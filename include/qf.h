@@ -473,7 +473,8 @@ qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_
 
 /* ------------------------------------------- rows into expert order and back ---- */
 /* Tokens and experts: row i = t * k + j of a plan stands for expert j of token t (the ids that
- * qf_moe_route writes), position p of the plan for row order[p].  bf16 matrices with rows of H:
+ * qf_moe_route writes), and positions[i] is its place in the plan's order.  bf16 matrices with
+ * rows of H:
  *   dispatch           out[positions[i]] = X[i / rows_per_x]
  *   combine            Y[t] = sum_j weights[t, j] R[positions[t k + j]]
  *   combine_backward   dR[p] = weights[t, j] dY[t] for p = positions[t k + j];
@@ -481,11 +482,12 @@ qf_status qf_row_plan_positions(const int32_t* ids, int64_t n, int n_ids, int32_
  * combine without weights (NULL: all 1) is the gradient of dispatch.  A positions entry outside
  * [0, n) (a row in no group) is not written by dispatch, adds nothing to Y, whatever its weight, and
  * gets dW 0; rows of out and dR that no entry names (those behind the last group) stay as they were.
- * positions must name no row twice (a plan's do not).  Sums in fp32, j (dW: the columns) in a fixed order, one rounding to bf16:
- *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) gamma_k sum_j |w| |r|;  |dr - w dy| <= (2^-8 + 2^-24) |w dy|;
- *   |dw - dw_exact| <= gamma_H sum |r| |dy|;  gamma_n = n 2^-24 / (1 - n 2^-24).
- * Values that are NaN or infinite follow the formulas.  dR or dW may be NULL to skip it (R is
- * not read without dW).
+ * positions must name no row twice (a plan's do not).  Sums in fp32, over j (dW: the columns) in a
+ * fixed order, one rounding to bf16; gamma_n = n 2^-24 / (1 - n 2^-24):
+ *   |y - y_exact| <= 2^-8 |y_exact| + (1 + 2^-8) gamma_k sum_j |w| |r|
+ *   |dr - w dy| <= (2^-8 + 2^-22) |w dy|,  |dw - dw_exact| <= gamma_H sum |r| |dy|
+ * NaN and infinities follow the formulas.  dR or dW may be NULL to skip it (R is not read without
+ * dW).
  * Limits: H a positive multiple of 8 below QF_MOE_MAX_COLS, leading dimensions >= H, n and
  * tokens * k in [0, QF_ROW_MAX_ROWS) (QF_ERR_SHAPE); rows_per_x >= 1, k >= 1 (QF_ERR_ARG); matrices
  * 16-byte aligned, leading dimensions multiples of 8 (QF_ERR_ALIGN).  X has ceil(n / rows_per_x)
@@ -719,35 +721,41 @@ qf_status qf_gemm_nvfp4(const uint16_t* X, int64_t ldx, const uint16_t* W, int64
  * QF_FP8_BLOCK elements, for products in 8 bits beside the 4-bit grids: activations in blocks along
  * a row, weights in square tiles, both operands of a weight gradient in blocks along the rows.
  * Per block, with a the largest |x|:
- *   scale = fl(a / 448);  code = E4M3(min(max(fl(x fl(448 / a)), -448), 448)), ties to even;
- * a block with a < 2^-100 gets scale 0 and codes of zeros (448 / a must stay in range); a block with
- * a NaN or an infinity gets scale NaN, so that whatever is made of it is NaN too, and unspecified codes.
+ *   scale = fl(a / 448);  code = E4M3(fl(x fl(448 / a))), to nearest, ties to even;
+ * a block with a < 2^-100 gets scale 0 and zero codes (448 / a must stay in range).  A block with a
+ * NaN or an infinity gets scale NaN, so that whatever is made of it is NaN too, and unspecified
+ * codes.
  *
- * qf_quant_fp8         rows: codes [rows][ldc], block b of row p: columns 128 b ..; its scale is
- *   scales[b * lds + p] (block-major: the product reads one block's scales of many rows at a time).
- *   positions NULL: row p of x.  Else (a plan's) row i / rows_per_x of x goes to p = positions[i] for i in [0, rows),
- *   rows into expert order on the way: each row of x is quantized once; entries outside [0, rows) are skipped,
- *   and rows that no entry names stay as they were.  d_rows (device int32, or NULL; read without positions,
- *   e.g. a plan's offsets + n_ids): rows at and past *d_rows stay as they were.  cols a multiple of 16.
- * qf_quant_fp8_panels  blocks of 128 rows of one group, transposed: codes [panels][cols][128], scales
- *   [panels][cols].  offsets (a plan's, n_ids groups) cut the rows into groups, each starts a panel
- *   of its own and the last one of a group is filled up with code 0; offsets NULL (n_ids 1): one group of
- *   all rows.  order NULL: position p holds row p of x; else (a plan's) row order[p] / rows_per_x, an entry
- *   outside [0, rows) a row of zeros.
- *   qf_fp8_panels(rows, n_ids) panels always suffice; those behind the last are left as they were.  cols a multiple of 8.
+ * qf_quant_fp8         rows: codes [rows][ldc]; block b of row p is its columns from 128 b on, its
+ *   scale scales[b * lds + p] (block-major: the product reads one block's scales of many rows at a
+ *   time).  positions NULL: row p of x.  Else (a plan's) row i / rows_per_x of x goes to p =
+ *   positions[i] for i in [0, rows): rows into expert order on the way, each row of x quantized
+ *   once; entries outside [0, rows) are skipped, and rows that no entry names stay as they were.
+ *   d_rows (device int32, or NULL; read without positions, e.g. a plan's offsets + n_ids): rows at
+ *   and past *d_rows stay as they were.  cols a multiple of 16.
+ * qf_quant_fp8_panels  blocks of 128 rows of one group, transposed: codes [panels][cols][128],
+ *   scales [panels][cols].  offsets (a plan's, n_ids groups) cut the rows into groups; each starts a
+ *   panel of its own, and the last of a group is filled up with code 0.  offsets NULL (n_ids 1): one
+ *   group of all rows.  order NULL: position p holds row p of x; else (a plan's) row order[p] /
+ *   rows_per_x, an entry outside [0, rows) a row of zeros.  qf_fp8_panels(rows, n_ids) panels always
+ *   suffice; those behind the last stay as they were.  cols a multiple of 8.
  * qf_quant_fp8_tiles   128 x 128 tiles of count stacked matrices x [count][rows][ldx]: codes
- *   [count][rows][cols], scales [count][ceil(rows / 128)][ceil(cols / 128)], and the transpose, of
- *   the same values: codes_t [count][cols][rows], scales_t [count][ceil(cols / 128)][ceil(rows / 128)]
- *   (each pair may be NULL, not both).  cols a multiple of 16, rows too with codes_t; count <= QF_ROW_MAX_IDS.
- * qf_swiglu_quant_fp8  a = u g / (1 + exp(-g)) of h [rows, 2 cols] = [g, u] (a fused gate/up product), codes
- *   and scales of a (held in fp32, not rounded in between) as qf_quant_fp8 lays them out; y: a in bf16 as well, or NULL.
- *   Error of a before rounding at most 16 2^-24 |a| + 2^-119 |u|.
- * qf_swiglu_backward   dh [rows, 2 cols] = [da u s (1 + g (1 - s)), da g s], s = 1 / (1 + exp(-g)), bf16,
- *   fp32 arithmetic: error at most 2^-8 of the value plus 32 2^-24 |da u| (1 + |g|) or |da g|.
- * Limits: rows in [0, QF_ROW_MAX_ROWS) (tiles: below QF_FP8_MAX_COLS), cols in [1, QF_FP8_MAX_COLS), leading
- * dimensions at least the row length, lds >= rows (QF_ERR_SHAPE); rows_per_x >= 1 with positions or order, n_ids in
- * 1..QF_ROW_MAX_IDS (QF_ERR_ARG); bf16 arrays 16-byte aligned with leading dimensions multiples of 8, codes 16-byte aligned with
- * ldc a multiple of 16 (QF_ERR_ALIGN).  Outputs must not overlap inputs.  One launch, no workspace. */
+ *   [count][rows][cols], scales [count][ceil(rows / 128)][ceil(cols / 128)]; and the transpose, of
+ *   the same values: codes_t [count][cols][rows], scales_t [count][ceil(cols / 128)][ceil(rows /
+ *   128)].  Each pair may be NULL, not both.  cols a multiple of 16, rows too with codes_t; count <=
+ *   QF_ROW_MAX_IDS.
+ * qf_swiglu_quant_fp8  a = u g / (1 + exp(-g)) of h [rows, 2 cols] = [g, u] (a fused gate/up
+ *   product): codes and scales of a as qf_quant_fp8 lays them out (a is held in fp32, not rounded in
+ *   between); y: a in bf16 as well, or NULL.  Error of a before it is rounded at most 16 2^-24 |a| +
+ *   2^-119 |u|.  cols a multiple of 16.
+ * qf_swiglu_backward   dh [rows, 2 cols] = [da u s (1 + g (1 - s)), da g s], s = 1 / (1 + exp(-g)),
+ *   bf16; fp32 arithmetic, error before it is rounded at most 32 2^-24 (|da u| (1 + |g|) or |da g|) +
+ *   2^-119 (|da u| or |da|).  cols a multiple of 8.
+ * Limits: rows in [0, QF_ROW_MAX_ROWS) (tiles: below QF_FP8_MAX_COLS), cols in [1,
+ * QF_FP8_MAX_COLS), leading dimensions at least the row length, lds >= rows (QF_ERR_SHAPE);
+ * rows_per_x >= 1 with positions or order, n_ids in 1..QF_ROW_MAX_IDS (QF_ERR_ARG); bf16 arrays
+ * 16-byte aligned with leading dimensions multiples of 8, codes 16-byte aligned with ldc a multiple
+ * of 16 (QF_ERR_ALIGN).  Outputs must not overlap inputs.  One launch, no workspace. */
 #define QF_FP8_BLOCK 128
 #define QF_FP8_MAX_COLS (1 << 22)
 qf_status qf_quant_fp8(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols, const int32_t* positions,

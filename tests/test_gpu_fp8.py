@@ -211,6 +211,21 @@ def test_swiglu_quant(n, cols):
     assert same(c2, c) and np.array_equal(s2.cpu().numpy(), s.astype(np.float32))
 
 
+def test_gate_at_every_value():
+    """The held product at every finite bf16 gate, read off the scale of a block with one element."""
+    v = np.arange(65536, dtype=np.uint16)
+    v = v[np.isfinite(f32(v))]
+    h = np.zeros((v.size, 32), np.uint16)
+    h[:, 0], h[:, 16] = v, prim.f32_to_bf16(np.float32([1.5]))[0]
+    _, s = fq.qf_swiglu_quant_fp8(dev(h))
+    a = np.abs(fp8.swiglu(f32(h).astype(np.float64))[:, 0])
+    top = s.cpu().numpy()[0].astype(np.float64) * 448
+    # a, the division and the scale's own rounding; values that the block drops, or past the range of fp32
+    keep = (a >= 2.0 ** -99) & (a < 2.0 ** 127)
+    within(top[keep], a[keep], 16 * 2.0 ** -24 * a[keep] + 2.0 ** -119 * 1.5 + 2.0 ** -23 * a[keep])
+    assert np.all(top[a < 2.0 ** -101] == 0)
+
+
 @pytest.mark.parametrize("n,cols", GATED + [(5, 24)])
 def test_swiglu_backward(n, cols):
     rng = np.random.default_rng(n + cols + 1)
@@ -329,7 +344,8 @@ def test_gemm_nan_stays_in_its_rows(M):
 
 GROUPED = [(1, 1, 1, 8, 16, 0.0), (5, 2, 3, 40, 160, 0.2), (61, 8, 128, 136, 256, 0.0), (64, 8, 16, 520, 272, 0.1), (300, 3, 5, 300, 400, 0.0),
            (100, 4, 1000, 72, 144, 0.1), (9, 4, 1024, 24, 32, 1.1), (700, 2, 2, 264, 640, 0.0), (1, 8, 8, 1536, 2048, 0.0), (400, 8, 6, 384, 128, 0.5),
-           (31, 1, 1, 1000, 1040, 0.0), (1500, 2, 5, 4700, 144, 0.1), (2000, 2, 70, 2100, 272, 0.0)]
+           (31, 1, 1, 1000, 1040, 0.0), (1500, 2, 5, 4700, 144, 0.1), (2000, 2, 70, 2100, 272, 0.0), (26000, 1, 1024, 40, 32, 0.0),
+           (3000, 1, 100, 264, 48, 0.3)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K,none", GROUPED)

@@ -78,6 +78,19 @@ def test_dispatch(T, k, H, E, none):
         assert np.array_equal(got[~live], before[~live]) and bool(ofull[:, H:].isnan().all())
 
 
+@pytest.mark.parametrize("n,per", [(10, 4), (100, 33), (70, 16), (33, 17), (5, 1000)])
+def test_dispatch_of_a_last_row_with_fewer(n, per):
+    rng = np.random.default_rng(n)
+    plan, _, order = plan_of(ids_of(rng, n, 1, 3, 0.2), 3)
+    x, live = bf(rng, (-(-n // per), 144)), order >= 0
+    out = torch.full((n, 144), 7.0, dtype=torch.bfloat16, device="cuda")
+    fq.qf_moe_dispatch(dev(x), plan, per, out=out)
+    assert np.array_equal(host(out)[live], x[order[live] // per]) and bool((out[torch.from_numpy(~live).cuda()] == 7).all())
+    c, s = fq.qf_quant_fp8(dev(x), plan=plan, rows_per_x=per)
+    codes, scales = fp8.quant_rows(f32(x)[order[live] // per])
+    assert np.array_equal(c.cpu().numpy()[live], codes) and np.array_equal(s.cpu().numpy()[:, live], scales)
+
+
 @pytest.mark.parametrize("weighted", [True, False])
 @pytest.mark.parametrize("T,k,H,E,none", CASES)
 def test_combine(T, k, H, E, none, weighted):
