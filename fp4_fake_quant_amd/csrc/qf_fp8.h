@@ -168,8 +168,16 @@ __device__ __forceinline__ uint4 load16_nt(const void* p) {
   return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4_t*)p));
 }
 // Outputs of this many bytes and more are stored past the caches: the 256 MiB behind the L2s hold what comes
-// after them better.
+// after them better.  Codes and sums of rows, through the caches / past them: 8192 x 4096 codes to 4 experts each (134 MB)
+// 39.2 / 37.9 us, half of that 20.6 / 18.8, 16.8 MB 9.3 / 9.3; panels of 134 MB 77.5 / 63.3, of 67 MB 34.0 / 32.9, of
+// 17 MB 13 / 10.3 but 118 / 123 with the product that reads them.
 constexpr int64_t NT_BYTES = 64 << 20;
+// bf16 rows are larger and the next kernel reads them, so they stay in the caches as long as they fit.  The rows'
+// gradients of a mixture with their quantization: called over and over 97 / 115 us at 134 MB, 132 / 146 at 196, 166 / 168
+// at 229, 226 / 206 at 268; after other work 123 / 146, 156 / 197, 182 / 217, 224 / 253.  A captured step of a mixture,
+// forward and backward, with rows of 67, 98, 134 and 537 MB: 1.175 / 1.189, 1.505 / 1.518, 2.03 / 2.03 and, all sides past the
+// caches at this size, 6.77 ms against 6.80 with none.
+constexpr int64_t NT_ROWS_BYTES = 224 << 20;
 // Calls f(std::true_type) or f(std::false_type).
 template <typename F>
 void with_nt(bool nt, F f) {

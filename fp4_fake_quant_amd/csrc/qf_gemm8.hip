@@ -41,7 +41,8 @@ struct Gemm8Args {
   int32_t M, N, K;                       // K: elements of a row-major row (panels: 0, every block whole)
   int32_t blocks;                        // blocks of the reduction (grouped over blocks: from the offsets)
   int32_t tiles_m, tiles_n;
-  int32_t y_vec;                         // rows of y take whole stores of 16 bytes (few rows: of 8)
+  int32_t most;                          // blocks that the panels hold, or tiles that a plan's groups make, at most
+  int32_t y_vec;                         // rows of y take whole stores of 16 bytes (few rows: of 8); 2: past the caches
 };
 enum { G8_DENSE, G8_ROWS, G8_BLOCKS };   // over what the groups go
 
@@ -57,8 +58,8 @@ __device__ __forceinline__ f32x4_t mfma_f8(i32x8_t a, i32x8_t b, f32x4_t c) {
 // its last fragments.
 //
 // 256 x 256 (two stages of 66 KiB, one workgroup per CU, two waves per SIMD, 228 to 251 registers): per step and wave
-// 32 products, 128 sums (256 where w has a scale per row) and 24 reads of 16 bytes.  32768 x 14336 x 4096 takes 1.72 ms
-// (2.23 PFLOP/s; a library product with one scale per tensor 1.27 ms): the matrix cores are busy 54% of 1.96 GHz,
+// 32 products, 128 sums (256 where w has a scale per row) and 24 reads of 16 bytes.  32768 x 14336 x 4096 takes 1.70 ms
+// (2.26 PFLOP/s; a library product with one scale per tensor 1.27 ms): the matrix cores are busy 54% of 1.96 GHz,
 // which is what the card's power leaves of 2.4, and the 940 MB of results, which all workgroups write at the same time, take
 // 0.18 ms of it (1.52 ms per 4096 of K without).  On the way: fragments straight from memory 6.99 ms; LDS with two
 // barriers a step 2.07; sums between the products and reads without conflicts 1.99; one barrier 1.89; workgroups that stay
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
   uint32_t tiles_m = (uint32_t)a.tiles_m, tiles_n = (uint32_t)a.tiles_n;
   if (MODE != G8_DENSE && a.offsets) {
     group_table(table, a.offsets, a.n_ids, a.n, MODE == G8_ROWS ? BM : FB, WAVES);
-    if (MODE == G8_ROWS) tiles_m = (uint32_t)uniform((int)table.pre[a.n_ids]);
+    if (MODE == G8_ROWS) tiles_m = min((uint32_t)uniform((int)table.pre[a.n_ids]), (uint32_t)a.most);
   }
   const uint32_t total = tiles_m * tiles_n * (MODE == G8_BLOCKS ? (uint32_t)a.n_ids : 1u);
   const uint32_t xcd = blockIdx.x & 7;
@@ -143,8 +144,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
       o.group = (int)(t / (tiles_m * tiles_n));
       t -= (uint32_t)o.group * tiles_m * tiles_n;
       if (a.offsets) {
-        block0 = uniform((int)table.pre[o.group]);
-        blocks = uniform((int)table.pre[o.group + 1]) - block0;
+        block0 = min(uniform((int)table.pre[o.group]), a.most);
+        blocks = min(uniform((int)table.pre[o.group + 1]), a.most) - block0;
       }
     }
     // runs of G8_RUN tile rows, column by column
@@ -376,12 +377,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
           : "memory");
       const int c = (int)(8 * c0);
       if (a.y_vec) {
+        auto store = [&](auto nt) {
 #pragma unroll
-        for (uint32_t k = 0; k < EACH; ++k) {
-          const uint32_t row = pass * ROWS + r0 + k * DOWN;
-          buf_store16(ry, (int)row < o.rows && c < o.cols ? (row * (uint32_t)a.ldy + (uint32_t)c) * 2 : BUF_OOR,
-                      __builtin_bit_cast(uint4, v[k]));
-        }
+          for (uint32_t k = 0; k < EACH; ++k) {
+            const uint32_t row = pass * ROWS + r0 + k * DOWN;
+            const uint32_t at = (int)row < o.rows && c < o.cols ? (row * (uint32_t)a.ldy + (uint32_t)c) * 2 : BUF_OOR;
+            __builtin_amdgcn_raw_buffer_store_b128(v[k], ry, (int)at, 0, decltype(nt)::value ? 2 : 0);
+          }
+        };
+        if (a.y_vec == 2) store(std::true_type());
+        else store(std::false_type());
       } else {                                                // rows off 16 bytes, or of any length
 #pragma unroll
         for (uint32_t k = 0; k < EACH; ++k) {
@@ -522,7 +527,8 @@ hipError_t launch_tiles(Gemm8Args a, int mode, hipStream_t s) {
   a.tiles_m = (int32_t)((a.M + BM - 1) / BM);
   a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
   // at most as many workgroups as the chip holds at once
-  const int64_t tiles = (a.tiles_m + (mode == G8_ROWS ? (a.M < a.n_ids ? a.M : a.n_ids) : 0)) * (int64_t)a.tiles_n * (mode == G8_BLOCKS ? a.n_ids : 1);
+  if (mode == G8_ROWS) a.most = a.tiles_m + (a.M < a.n_ids ? a.M : a.n_ids);
+  const int64_t tiles = (mode == G8_ROWS ? a.most : a.tiles_m) * (int64_t)a.tiles_n * (mode == G8_BLOCKS ? a.n_ids : 1);
   const int64_t most = G8_CUS * (160 * 1024 / (2 * Stage<BM, BN>::BYTES));
   const dim3 g((unsigned)(tiles < most ? tiles : most)), wg(64 * WM * WN);
   if (mode == G8_DENSE) k_gemm8<G8_DENSE, BM, BN, WM, WN><<<g, wg, 0, s>>>(a);
@@ -566,6 +572,9 @@ hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
   if (mode == G8_ROWS && a.M <= 24 * (int64_t)a.n_ids)
     return launch_few<G8_ROWS, 2>(a, (a.M + QF_ROW_TILE - 1) / QF_ROW_TILE + groups, groups, a.M < 8 * (int64_t)a.n_ids ? 2 : 4, s);
   a.y_vec = a.ldy % 8 == 0 && (uintptr_t)a.y % 16 == 0 && a.N % 8 == 0 && a.ldy < QF_FP8_MAX_COLS;
+  // through the caches / past them: 32768 x 14336 x 4096 1.73 / 1.70 ms; 32768 rows of 2048 -> 4096 for 16 groups 305 / 287 us
+  // (with the sum over a token's four rows that follows 360 / 341), half the rows 166 / 154 (188 / 185), a quarter 92 / 91 (107 / 109)
+  if (a.y_vec && (int64_t)a.M * a.N * 2 * (mode == G8_BLOCKS ? a.n_ids : 1) >= NT_ROWS_BYTES) a.y_vec = 2;
   if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
   return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
@@ -657,6 +666,7 @@ qf_status qf_gemm_fp8_wgrad(const uint8_t* Dc, const float* Ds, const uint8_t* X
   a.M = (int32_t)N;
   a.N = (int32_t)K;
   a.blocks = (int32_t)((rows + FB - 1) / FB);
+  a.most = (int32_t)qf_fp8_panels(rows, n_ids);
   if (small_tiles(a, G8_BLOCKS) > G8_MAX_TILES) return QF_ERR_SHAPE;
   return status_of(launch(a, G8_BLOCKS, (hipStream_t)stream));
 }

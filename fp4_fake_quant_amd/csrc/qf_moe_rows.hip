@@ -7,7 +7,8 @@
 // fixed order, and no atomics are needed.
 //
 // Rows of 4096, 8 of 64 experts: 8192 tokens combined in 96 us (593 MB, 6.1 TB/s; 123 with one row at a time in flight,
-// 103 with eight, 97 with stores past the caches), the gradients of 4099 tokens of 6 in 80 us (436 MB, 5.4 TB/s; 98 at first).
+// 103 with eight, 97 with stores past the caches), the gradients of 4099 tokens of 6 in 89 us (436 MB, 4.9 TB/s; 98 at first;
+// 80 past the caches, which the reader of these rows then pays for).
 // A decode step takes what its call takes (7.8 us from Python, kernel 3.5).
 #include "qf_fp8.h"
 
@@ -180,7 +181,7 @@ qf_status qf_moe_dispatch(const uint16_t* X, int64_t ldx, int64_t rows_per_x, co
   a.ldy = ldo;
   const int64_t rows = MR_WG >> a.lane_bits;
   const int64_t units = a.tokens * ((a.per + SPREAD_MOST - 1) / SPREAD_MOST);
-  with_nt(n * H * 2 >= NT_BYTES, [&](auto nt) {
+  with_nt(n * H * 2 >= NT_ROWS_BYTES, [&](auto nt) {
     k_moe_dispatch<decltype(nt)::value><<<grid_of((units + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
   });
   return status_of(hipGetLastError());
@@ -243,7 +244,7 @@ qf_status qf_moe_combine_backward(const uint16_t* dY, int64_t lddy, const uint16
   a.ldy = lddr;
   a.dw = dW;
   const int64_t rows = MR_WG >> a.lane_bits;
-  with_nt(a.n * H * 2 >= NT_BYTES, [&](auto nt) {
+  with_nt(a.n * H * 2 >= NT_ROWS_BYTES, [&](auto nt) {
     k_moe_combine_backward<decltype(nt)::value><<<grid_of((a.n + rows - 1) / rows), MR_WG, 0, (hipStream_t)stream>>>(a);
   });
   return status_of(hipGetLastError());

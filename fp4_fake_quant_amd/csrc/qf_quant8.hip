@@ -471,7 +471,9 @@ qf_status qf_swiglu_backward(const uint16_t* h, int64_t ldh, const uint16_t* da,
   if (misaligned(h, 16) || ldh % 8 || misaligned(da, 16) || ldda % 8 || misaligned(dh, 16) || lddh % 8 || misaligned(d_rows, 4))
     return QF_ERR_ALIGN;
   GateArgs a = {h, da, dh, ldh, ldda, lddh, rows, d_rows, (uint32_t)cols, (uint32_t)(cols / 8)};
-  with_nt(rows * cols * 4 >= NT_BYTES, [&](auto nt) {
+  // past the caches where twice NT_BYTES leave: 35.3 through / 35.1 past at 98 MB (67 / 70 with a quantization that reads
+  // them), 58.4 / 46.8 at 134 MB (100 / 99), 71.7 / 56.4 at 163 MB (125 / 118)
+  with_nt(rows * cols * 4 >= 2 * NT_BYTES, [&](auto nt) {
     k_swiglu_backward<decltype(nt)::value><<<grid_of((rows * a.chunks + Q8_WG - 1) / Q8_WG), Q8_WG, 0, (hipStream_t)stream>>>(a);
   });
   return status_of(hipGetLastError());
