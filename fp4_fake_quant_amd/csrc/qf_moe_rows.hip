@@ -149,7 +149,10 @@ __global__ __launch_bounds__(MR_WG) void k_moe_combine_backward(MoeRowsArgs a) {
   }
 }
 
-uint32_t lane_bits_of(uint32_t chunks) { return chunks > 16 ? 6 : chunks > 4 ? 4 : 2; }
+// Up to four chunks a lane.  The gradients of 65536 tokens of 4 (16384 of rows of 2048) with 4 / 8 / 16 / 32 / 64 lanes a row:
+// rows of 64 17.6 / 21 / 35 / 62 / 114 us, 128 32 / 29 / 39 / 66 / 118, 256 65 / 49 / 51 / 75 / 131, 512 148 / 99 / 94 / 98 / 150,
+// 2048 214 / 144 / 122 / 104 / 100; dispatch goes the same way, and with few rows all are alike or 64 the best.
+uint32_t lane_bits_of(uint32_t chunks) { return chunks > 64 ? 6 : chunks > 16 ? 4 : chunks > 8 ? 3 : 2; }
 dim3 grid_of(int64_t units) { return dim3((unsigned)(units < MR_MAX_GRID ? units : MR_MAX_GRID)); }
 bool bad_rows(int64_t H, int64_t ld) { return H < 1 || H % 8 != 0 || H >= QF_MOE_MAX_COLS || ld < H; }
 bool bad_mat(const void* p, int64_t ld) { return misaligned(p, 16) || ld % 8 != 0; }
