@@ -708,7 +708,7 @@ def _positions(plan):
 
 
 def _x_rows(rows, n, rows_per_x):
-    if rows_per_x < 1 or rows != (n + rows_per_x - 1) // rows_per_x:
+    if not 1 <= rows_per_x < 1 << 62 or rows != (n + rows_per_x - 1) // rows_per_x:
         raise ValueError(f"x has {rows} rows for {n} rows of the plan and rows_per_x={rows_per_x}")
 
 
@@ -724,7 +724,7 @@ def qf_moe_dispatch(X, plan, rows_per_x=1, out=None):
     return out
 
 
-def _combine(plan, R, weights, k):
+def _combine(plan, weights, k):
     _positions(plan)
     if weights is not None:
         if weights.dim() != 2 or k not in (None, weights.shape[1]):
@@ -740,7 +740,7 @@ def qf_moe_combine(R, plan, weights=None, k=None, Y=None):
     """Y[t] = sum_j weights[t, j] * R[plan.positions[t * k + j]], bf16 [tokens, H], from R [plan.n,
     H] in the order of the plan's groups: weights float32 [tokens, k], or None with k given (all 1:
     the gradient of qf_moe_dispatch with rows_per_x = k).  Rows in no group add nothing."""
-    tokens, k = _combine(plan, R, weights, k)
+    tokens, k = _combine(plan, weights, k)
     dev = _same_gpu(R, weights, Y, plan.order)
     rows, H, ldr = _mat(_bf16(R, "R"), "R")
     if rows != plan.n:
@@ -754,7 +754,7 @@ def qf_moe_combine_backward(dY, R, plan, weights=None, k=None, d_rows=None, d_we
     """(d_rows bf16 [plan.n, H], d_weights float32 [tokens, k]) of qf_moe_combine: d_rows[p] =
     weights * dY[t], d_weights = <R[p], dY[t]>; None for what is not wanted.  Rows of d_rows behind
     the last group are left as they were (unspecified where d_rows is new)."""
-    tokens, k = _combine(plan, R, weights, k)
+    tokens, k = _combine(plan, weights, k)
     if not want[1]:
         R = None
     dev = _same_gpu(dY, R, weights, d_rows, d_weights, plan.order)
@@ -806,8 +806,7 @@ def _scales(t, name, blocks, rows):
     """Block-major scales [blocks, rows]: their row stride."""
     if t.dtype != torch.float32 or tuple(t.shape) != (blocks, rows):
         raise ValueError(f"{name} must be a float32 tensor of shape {(blocks, rows)}")
-    ld = _mat(t, name)[2]
-    return max(ld, rows)
+    return _mat(t, name)[2]
 
 
 def qf_quant_fp8(x, plan=None, rows_per_x=None, codes=None, scales=None):

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import fp4_fake_quant_amd as fq
 from fp4_fake_quant_amd import _lib
 from oracle import fp8, rows
 from oracle import primitives as prim
@@ -214,3 +215,19 @@ def test_panels_bound():
         n, e = int(rng.integers(0, 2000)), int(rng.integers(1, 60))
         off = rows.plan(rng.integers(-1, e, n).astype(np.int32), e)[0]
         assert len(fp8.panel_blocks(off)) <= f(n, e)
+
+
+def test_binding_strides_and_counts():
+    """Scales that share one row of memory have a row stride below their rows, which the entry points
+    refuse; a count that does not fit the C argument is refused before it wraps around."""
+    assert fq._scales(torch.empty(3, 8), "scales", 3, 8) == 8
+    assert fq._scales(torch.empty(3, 12)[:, :8], "scales", 3, 8) == 12
+    assert fq._scales(torch.empty(1, 8), "scales", 1, 8) >= 8
+    shared = fq._scales(torch.empty(1, 8).expand(3, 8), "scales", 3, 8)
+    assert shared < 8
+    assert call("quant_fp8", QUANT, lds=shared) == SHAPE
+    assert call("gemm_fp8", GEMM, ldxs=shared) == SHAPE and call("gemm_fp8_grouped", GEMM, ldxs=shared) == SHAPE
+    fq._x_rows(1, 5, 1000)
+    for bad in (0, -1, 1 << 62, (1 << 64) + 1):
+        with pytest.raises(ValueError):
+            fq._x_rows(1, 5, bad)
