@@ -837,10 +837,16 @@ def qf_fp8_panels(rows, n_ids=1):
     return lib().qf_fp8_panels(int(rows), int(n_ids))
 
 
+def _panels(t, name, dtype, shape):
+    """Panels or their scales, with room for at least shape[0]."""
+    return _dense(t, name, dtype, (max(t.shape[0], shape[0]) if t.dim() else 0,) + shape[1:])
+
+
 def qf_quant_fp8_panels(x, plan=None, rows_per_x=None, codes=None, scales=None):
     """(codes uint8 [panels, cols, 128], scales float32 [panels, cols]): E4M3 codes of x bf16 in blocks
     of 128 rows of one group of the plan (None: all rows are one), transposed, the operands of
-    qf_gemm_fp8_wgrad.  rows_per_x as qf_quant_fp8.  Panels behind the last are left as they were."""
+    qf_gemm_fp8_wgrad.  rows_per_x as qf_quant_fp8.  codes and scales may hold more panels than
+    qf_fp8_panels says; panels behind the last are left as they were."""
     rows, cols, ldx = _mat(_bf16(x, "x"), "x")
     dev = _same_gpu(x, codes, scales, None if plan is None else _plan(plan).order)
     order = offsets = None
@@ -855,11 +861,11 @@ def qf_quant_fp8_panels(x, plan=None, rows_per_x=None, codes=None, scales=None):
     if codes is None:
         codes = torch.empty(panels, cols, FP8_BLOCK, dtype=torch.uint8, device=x.device)
     else:
-        _dense(codes, "codes", torch.uint8, (panels, cols, FP8_BLOCK))
+        _panels(codes, "codes", torch.uint8, (panels, cols, FP8_BLOCK))
     if scales is None:
         scales = torch.empty(panels, cols, dtype=torch.float32, device=x.device)
     else:
-        _dense(scales, "scales", torch.float32, (panels, cols))
+        _panels(scales, "scales", torch.float32, (panels, cols))
     _call(dev, "qf_quant_fp8_panels", x.data_ptr(), ldx, rows, cols, order, rows_per_x or 1, offsets, n_ids,
           codes.data_ptr(), scales.data_ptr())
     return codes, scales
@@ -961,19 +967,21 @@ def qf_gemm_fp8_grouped(Xc, Xs, Wc, Ws, plan, Y=None):
 
 def qf_gemm_fp8_wgrad(Dc, Ds, Xc, Xs, plan=None, dW=None):
     """dW bf16 [n_ids, N, K] (plan None: [N, K]) from the panels of dY (Dc [panels, N, 128], Ds
-    [panels, N]) and X (Xc [panels, K, 128], Xs) under the same plan (qf_quant_fp8_panels): the
-    gradient of qf_gemm_fp8_grouped's weights, zero for a group without rows."""
+    [panels, N]) and X (Xc [panels, K, 128], Xs) under the same plan (qf_quant_fp8_panels; panels behind
+    its last are not read, without a plan all are summed): the gradient of qf_gemm_fp8_grouped's weights,
+    zero for a group without rows."""
     dev = _same_gpu(Dc, Ds, Xc, Xs, dW, None if plan is None else _plan(plan).order)
     if Dc.dim() != 3 or Xc.dim() != 3:
         raise ValueError("Dc and Xc must be panels [panels, cols, 128]")
     panels, N, K = Dc.shape[0], Dc.shape[1], Xc.shape[1]
     rows = panels * FP8_BLOCK if plan is None else plan.n
     n_ids = 1 if plan is None else plan.n_ids
-    if plan is not None and panels != lib().qf_fp8_panels(rows, n_ids):
-        raise ValueError(f"{panels} panels for a plan of {rows} rows, {n_ids} ids")
+    check = _dense                                   # without a plan every panel is taken
+    if plan is not None:
+        panels, check = lib().qf_fp8_panels(rows, n_ids), _panels
     for c, s, cols, name in ((Dc, Ds, N, "D"), (Xc, Xs, K, "X")):
-        _dense(c, name + "c", torch.uint8, (panels, cols, FP8_BLOCK))
-        _dense(s, name + "s", torch.float32, (panels, cols))
+        check(c, name + "c", torch.uint8, (panels, cols, FP8_BLOCK))
+        check(s, name + "s", torch.float32, (panels, cols))
     shape = (N, K) if plan is None else (n_ids, N, K)
     if dW is None:
         dW = torch.empty(shape, dtype=torch.bfloat16, device=Dc.device)

@@ -1,5 +1,5 @@
 """Row and 8-bit operators at sizes whose outputs are stored past the caches (another form of each kernel):
-the same bits as in pieces that are not, or as the formula where it leaves no choice."""
+the same bits as in pieces that are not, or as the formula where it leaves no choice.  Panels in larger buffers."""
 
 import pytest
 import torch
@@ -113,3 +113,27 @@ def test_weight_gradients():
     dW = fq.qf_gemm_fp8_wgrad(dc, ds, xc, xs)
     for s in cuts(N, 4000):
         assert torch.equal(dW[s], fq.qf_gemm_fp8_wgrad(dc[:, s].contiguous(), ds[:, s].contiguous(), xc, xs))
+
+
+@pytest.mark.parametrize("n,E", [(1, 1), (130, 1), (300, 4)])
+def test_more_panels_than_needed(n, E):
+    """Panels in larger buffers, what lies behind the last (NaN) neither written nor read."""
+    ids = torch.zeros(n, dtype=torch.int32, device="cuda") if E == 1 else (torch.arange(n, device="cuda") % E).int()
+    plan = fq.qf_row_plan(ids, E, positions=True)
+    need = fq.qf_fp8_panels(n, E)
+    d, x = randn(13, n, 48), randn(14, n, 80)
+    panels, want = [], []
+    for t, extra in ((d, 1), (x, 3)):
+        codes = torch.full((need + extra, t.shape[1], 128), 0x7F, dtype=torch.uint8, device="cuda")
+        scales = torch.full((need + extra, t.shape[1]), float("nan"), device="cuda")
+        panels += fq.qf_quant_fp8_panels(t, plan=plan, codes=codes, scales=scales)
+        want += fq.qf_quant_fp8_panels(t, plan=plan)
+        assert bool((codes[need:] == 0x7F).all()) and bool(scales[need:].isnan().all())
+    dW = fq.qf_gemm_fp8_wgrad(*panels, plan)
+    assert torch.equal(dW, fq.qf_gemm_fp8_wgrad(*want, plan)) and not bool(dW.isnan().any())
+    with pytest.raises(ValueError):
+        fq.qf_gemm_fp8_wgrad(panels[0][:need - 1], *panels[1:], plan)
+    with pytest.raises(ValueError):
+        fq.qf_quant_fp8_panels(d, plan=plan, codes=panels[0][:need - 1])
+    with pytest.raises(ValueError):
+        fq.qf_gemm_fp8_wgrad(*panels)
