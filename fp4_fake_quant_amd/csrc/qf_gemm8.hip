@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
     issue(st);
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      p[j] = f32x4_t{0, 0, 0, 0};
+      p[j] = swr[j] = f32x4_t{0, 0, 0, 0};                    // (the scales too: 0 times a NaN of this tile is one in the next)
 #pragma unroll
       for (int i = 0; i < TM; ++i) acc[i][j] = f32x4_t{0, 0, 0, 0};
     }
