@@ -57,12 +57,13 @@ __device__ __forceinline__ uint32_t max8lanes(uint32_t m) {
 
 // 1 / (1 + exp(-g)) of a bf16 g.  log2 e is taken in two parts, the first of 16 bits, so that its product
 // with g is exact, and cut off rather than rounded, so that the second part's correction m of exp(-g)
-// (1 + m, |m| < 2^-10 where the result is not 0) is not negative where exp(-g) is infinite.
+// (1 + m, |m| < 2^-10 where the result is neither 0 nor 1) is not negative where exp(-g) is infinite.  Where
+// exp(-g) is 0, m is kept finite (g may be infinite).
 __device__ __forceinline__ float sigmoid(float g) {
   constexpr float HI = 0x1.7154p0f;
   constexpr float LO = (float)((1.44269504088896340736 - (double)HI) * 0.69314718055994530942);
   static_assert(LO > 0.0f, "cut off, not rounded");
-  const float e = __builtin_amdgcn_exp2f(-g * HI), m = -g * LO;
+  const float e = __builtin_amdgcn_exp2f(-g * HI), m = fmaxf(-g * LO, -1.0f);       // (a NaN stays one in e)
   return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, m, e));
 }
 

@@ -751,6 +751,7 @@ qf_status qf_gemm_nvfp4(const uint16_t* X, int64_t ldx, const uint16_t* W, int64
  * qf_swiglu_backward   dh [rows, 2 cols] = [da u s (1 + g (1 - s)), da g s], s = 1 / (1 + exp(-g)),
  *   bf16; fp32 arithmetic, error before it is rounded at most 32 2^-24 (|da u| (1 + |g|) or |da g|) +
  *   2^-119 (|da u| or |da|).  cols a multiple of 8.
+ *   Infinities and NaN follow the formulas in both, with s = 0 where exp(-g) is past the range of fp32.
  * Limits: rows in [0, QF_ROW_MAX_ROWS) (tiles: below QF_FP8_MAX_COLS), cols in [1,
  * QF_FP8_MAX_COLS), leading dimensions at least the row length, lds >= rows (QF_ERR_SHAPE);
  * rows_per_x >= 1 with positions or order, n_ids in 1..QF_ROW_MAX_IDS (QF_ERR_ARG); bf16 arrays
