@@ -204,7 +204,9 @@ __global__ __launch_bounds__(Q8_WG) void k_swiglu_backward(GateArgs a) {
     for (int e = 0; e < 8; ++e) {
       const float s = sigmoid(g[e]);
       const float m = g[e] * s;
-      g[e] = (d[e] * u[e]) * (s * (1.0f + (g[e] - m)));
+      const float f = s * (1.0f + (g[e] - m)), du = d[e] * u[e];
+      // da u past the range (both factors are above 1 then): a small f comes first
+      g[e] = fabsf(du) < __builtin_inff() ? du * f : (d[e] * f) * u[e];
       u[e] = d[e] * m;
     }
 #pragma unroll

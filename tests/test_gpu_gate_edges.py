@@ -65,3 +65,27 @@ def test_gradient_of_infinities(cols, da):
     same_non_finite(got[:, [0, cols]], want[:, [0, cols]])
     rest = np.delete(got, [0, cols], 1)
     assert not rest.any()
+
+
+def test_gradient_past_the_range():
+    """da u passes fp32's range, the gradient does not."""
+    cols = 16
+    g = np.array([-85.0, -80, -60, -40, -20, -1.28, 0, 5, 200])
+    pairs = [(1e30, 1e30), (-3e38, 2e5), (2.0, 3e38), (1e-30, -3e38), (3e38, 1e-38), (3.38e38, 1.0), (1e25, 1e15)]
+    rows = [(a, b, c) for a in g for b, c in pairs]
+    h, d = np.zeros((len(rows), 2 * cols)), np.zeros((len(rows), cols))
+    for i, (a, b, c) in enumerate(rows):
+        h[i, 0], h[i, cols], d[i, 0] = a, c, b
+    got = f32(host(fq.qf_swiglu_backward(dev(bits(h)), dev(bits(d))))).astype(np.float64)[:, 0]
+    hf, df = f32(bits(h)).astype(np.float64), f32(bits(d)).astype(np.float64)
+    want = fp8.swiglu_backward(hf, df)[:, 0]
+    # the sigmoid is off by at most 16 2^-24 of itself or by 2^-119, 1 + g (1 - s) by 20 2^-24 of 1 + |g|, and two products follow
+    g, p = hf[:, 0], np.abs(df[:, 0] * hf[:, cols])
+    off = (64 * 2.0 ** -24 * fp8.sigmoid(g) + 2.0 ** -119) * p * (1 + np.abs(g))
+    top = 2.0 ** 128 * (1 - 2.0 ** -9)              # what is larger rounds to an infinity
+    keep = np.abs(want) + off < top * (1 - 2.0 ** -8)
+    assert keep.sum() > 40 and np.any(keep & (p > top))
+    err = np.abs(got - want)
+    assert np.all((err <= 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * off + 2.0 ** -134)[keep]), np.argwhere(~(err <= off) & keep)
+    past = np.abs(want) - off > top * (1 + 2.0 ** -8)
+    assert past.any() and np.array_equal(got[past], np.copysign(INF, want[past]))
