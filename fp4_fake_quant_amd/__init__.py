@@ -880,8 +880,8 @@ def qf_quant_fp8_tiles(x, transpose=False, codes=None, scales=None, codes_t=None
     dev = _same_gpu(x, codes, scales, codes_t, scales_t)
     count = x.shape[0] if x.dim() == 3 else 1
     lead, (rows, cols) = tuple(x.shape[:-2]), x.shape[-2:]
-    ld = x.stride(-2) if rows > 1 else max(cols, x.stride(-2))
-    if (x.stride(-1) != 1 and cols > 1) or (count > 1 and x.stride(0) != rows * ld):
+    ld = x.stride(-2) if rows > 1 else x.stride(0) if rows and count > 1 else cols       # (a single row's own stride says nothing)
+    if (x.stride(-1) != 1 and cols > 1) or (rows and count > 1 and x.stride(0) != rows * ld):
         raise ValueError("x must have contiguous rows, and its matrices must follow one another")
     rt, ct = (rows + FP8_BLOCK - 1) // FP8_BLOCK, (cols + FP8_BLOCK - 1) // FP8_BLOCK
     outs = [(codes, "codes", torch.uint8, lead + (rows, cols)), (scales, "scales", torch.float32, lead + (rt, ct))]

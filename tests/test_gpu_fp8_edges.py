@@ -70,3 +70,32 @@ def test_product_keeps_a_scale_in_its_row_or_tile(M, N, K, grouped):
     want[:off[1], N // 128 * 128:] = True
     assert np.array_equal(not_finite(got), want)
     assert torch.equal(torch.where(torch.from_numpy(want).cuda(), clean, got), clean)
+
+
+# --------------------------------------------------- matrices of one row ----
+@pytest.mark.parametrize("count", [1, 3, 130])
+def test_tiles_of_single_rows(count):
+    """Matrices of one row, whose stride says nothing: any that lie one after another."""
+    x = torch.randn(count, 144, device="cuda").bfloat16()
+    want = [fp8.quant_tiles(x[e:e + 1].float().cpu().numpy()) for e in range(count)]
+    for v in (x[:, None], x.as_strided((count, 1, 144), (144, 1 << 20, 1)), x[None].transpose(0, 1)):
+        c, s = fq.qf_quant_fp8_tiles(v)
+        assert c.shape == (count, 1, 144) and s.shape == (count, 1, 2)
+        for e in range(count):
+            assert np.array_equal(c[e].cpu().numpy(), want[e][0]) and np.array_equal(s[e].cpu().numpy(), want[e][1])
+
+
+def test_tiles_of_single_rows_apart():
+    """Single rows with room between them: the row stride is the matrices'."""
+    full = torch.full((5, 160), float("nan"), dtype=torch.bfloat16, device="cuda")
+    full[:, :144] = torch.randn(5, 144, device="cuda").bfloat16()
+    c, s = fq.qf_quant_fp8_tiles(full[:, None, :144])
+    c2, s2 = fq.qf_quant_fp8_tiles(full[:, :144].contiguous()[:, None])
+    assert torch.equal(c, c2) and torch.equal(s, s2)
+    with pytest.raises(ValueError):
+        fq.qf_quant_fp8_tiles(full.view(5, 10, 16)[:, :9].transpose(0, 1))
+
+
+def test_tiles_without_rows():
+    c, s, ct, st = fq.qf_quant_fp8_tiles(torch.empty(3, 0, 64, dtype=torch.bfloat16, device="cuda"), transpose=True)
+    assert c.shape == (3, 0, 64) and s.shape == (3, 0, 1) and ct.shape == (3, 64, 0) and st.shape == (3, 1, 0)
