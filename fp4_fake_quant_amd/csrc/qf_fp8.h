@@ -147,15 +147,6 @@ __device__ __forceinline__ GroupUnit unit_at(const GroupTable& t, int n_ids, int
   return GroupUnit{g, first, min(unit, __builtin_amdgcn_readfirstlane(t.off[g + 1]) - first), index};
 }
 
-// Units of the groups before group g.
-__device__ __forceinline__ uint32_t units_before(const int32_t* offsets, int g, int n, int unit) {
-  uint32_t sum = 0, total;
-  for (int i = threadIdx.x & 63; i < g; i += 64)
-    sum += units_of(group_offset(offsets, i, n), group_offset(offsets, i + 1, n), unit);
-  wave_before(sum, &total);
-  return (uint32_t)__builtin_amdgcn_readfirstlane((int)total);
-}
-
 // 16 bytes, past the caches (NT) where they will not be read from there again.
 template <bool NT>
 __device__ __forceinline__ void store16(void* p, uint4 v) {
