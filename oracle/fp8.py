@@ -139,6 +139,13 @@ def product_bound(y, P, L):
     return 2.0 ** -8 * np.abs(y) + (1 + 2.0 ** -8) * (2.0 ** -10 + gamma(2 * L + 4 * blocks_of(L) + 64)) * P
 
 
+def block_sums_bound(y, S, blocks):
+    """The bound where no block's sum loses anything in the cores: S the sum of |s P_b|, P_b a block's sum, s its two
+    scales.  One rounding of the scales' product (or of P_b times a scale), one per block, and up to nine where
+    the waves of a workgroup join, then half a step of bf16."""
+    return 2.0 ** -8 * abs(y) + (1 + 2.0 ** -8) * gamma(blocks + 10) * S
+
+
 def swiglu(h):
     """u g sigmoid(g) of h = [g, u] in float64."""
     h = np.asarray(h, np.float64)

@@ -77,6 +77,44 @@ def test_product_by_blocks():
     assert np.allclose(y, want, rtol=1e-12, atol=1e-12 * P.max())
 
 
+def test_block_sums_bound_catches():
+    """Blocks in pairs that cancel, codes of 0, 1, 1.5 and 2: sums in fp32 pass; one term lost, sums held in bf16, or a
+    block counted with another one's scale do not."""
+    rng = np.random.default_rng(6)
+    codes = np.array([0x00, 0x38, 0x3C, 0x40, 0xB8, 0xBC, 0xC0], np.uint8)
+    M, N, pairs = 9, 11, 16
+    pick = lambda *shape: fp8.VALUES[codes[rng.integers(0, 7, shape)]]
+    a, b = pick(M, pairs, 128), pick(N, pairs, 128)
+    x = np.concatenate([np.stack([a, -a], 2).reshape(M, -1), pick(M, 16)], 1)
+    w = np.concatenate([np.stack([b, b], 2).reshape(N, -1), pick(N, 16)], 1)
+    sx = np.exp(np.concatenate([np.repeat(rng.standard_normal((pairs, M)), 2, 0), rng.standard_normal((1, M))])).astype(np.float32)
+    sw = np.exp(np.concatenate([np.repeat(rng.standard_normal(pairs), 2), rng.standard_normal(1)])).astype(np.float32)
+    blocks = 2 * pairs + 1
+    cut = [slice(128 * i, 128 * i + 128) for i in range(blocks)]
+    P = np.stack([x[:, c] @ w[:, c].T for c in cut])
+    t = P * (sx.astype(np.float64) * sw.astype(np.float64)[:, None])[:, :, None]
+    y, S = t.sum(0), np.abs(t).sum(0)
+
+    def fails(P, hold=lambda v: v, s=(sx * sw[:, None]).astype(np.float32)):
+        acc = np.zeros((M, N), np.float32)
+        for i in range(blocks):
+            acc = hold((acc + (P[i].astype(np.float32) * s[i][:, None])).astype(np.float32))
+        got = prim.bf16_to_f32(prim.f32_to_bf16(acc)).astype(np.float64)
+        return np.mean(~(np.abs(got - y) <= fp8.block_sums_bound(y, S, 2 * blocks)))
+
+    assert fails(P) == 0                               # (a product and a sum each rounded: two a block)
+    bound = fp8.block_sums_bound(y, S, 2 * blocks)
+    for k in (0, 128 * 5 + 77, x.shape[1] - 1):
+        lost, term = P.copy(), np.outer(x[:, k], w[:, k])
+        lost[k // 128] -= term
+        # the rounded rest is off from y by the term, less its own bound, at most the term's 2^-8 more than y's
+        seen = np.mean(np.abs(term * sx[k // 128][:, None] * float(sw[k // 128])) * (1 - 2.0 ** -7) > 2 * bound)
+        assert fails(lost) >= seen > 0.3
+    # (one result outside is enough for a test to fail)
+    assert fails(P, hold=lambda v: prim.bf16_to_f32(prim.f32_to_bf16(v))) > 0
+    assert fails(P, s=(sx * np.roll(sw, 1)[:, None]).astype(np.float32)) > 0
+
+
 def test_gradients_against_differences():
     rng = np.random.default_rng(5)
     h, da = rng.standard_normal((4, 12)) * 3, rng.standard_normal((4, 6))
