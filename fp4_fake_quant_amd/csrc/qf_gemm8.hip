@@ -546,8 +546,13 @@ int64_t small_tiles(const Gemm8Args& a, int mode) {
 template <int MODE, int MT>
 hipError_t launch_few(Gemm8Args a, int64_t tiles, int64_t likely, int nj, hipStream_t s) {
   a.y_vec = a.ldy % 4 == 0 && (uintptr_t)a.y % 8 == 0;
-  // wide workgroups read x less often, but 192 workgroups are wanted
-  while (nj > 1 && (a.N + 16 * nj - 1) / (16 * nj) * likely < 192) nj /= 2;
+  // wide workgroups read x less often; narrower ones share the work out as long as each has a CU to itself (the next
+  // one on a CU waits for the first's loads).  Microseconds with 16 / 32 / 64 columns, w from memory: 16 rows of 4096 -> 4096
+  // (256 / 128 / 64 workgroups) 7.5 / 9.2 / 12.8, -> 5120 (320 / 160 / 80) 11.4 / 9.4 / 12.9, -> 8192 12.0 / 10.9 / 13.3,
+  // -> 10240 14.6 / 15.9 / 13.7, -> 28672 31.9 / 30.3 / 27.5; 64 rows -> 4096 12.9 / 15.1 / 19.2, -> 5120 22.6 / 15.3 / 19.4,
+  // -> 10240 31.5 / 26.5 / 20.2; 14336 -> 5120 with 16 rows 31.5 / 25.2 / 36.8; 8 groups of 16 rows of 2048 -> 512 5.0 / 6.0 /
+  // 7.7, -> 1024 7.8 / 6.7 / 8.3, -> 1536 9.3 / 9.5 / 8.4.  (One row alone, 4096 -> 5120: 8.3 / 8.6 / 11.8.)
+  while (nj > 1 && (a.N + 8 * nj - 1) / (8 * nj) * likely <= G8_CUS) nj /= 2;
   const dim3 g((unsigned)((a.N + 16 * nj - 1) / (16 * nj)), (unsigned)tiles), wg(64 * FEW_WAVES);
   if (nj == 4) k_gemm8_few<MODE, MT, 4><<<g, wg, 0, s>>>(a);
   else if (nj == 2) k_gemm8_few<MODE, MT, 2><<<g, wg, 0, s>>>(a);

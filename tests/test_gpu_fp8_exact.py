@@ -139,6 +139,25 @@ def test_weight_gradients(E, N, K, pairs, tail):
         check(got[e], y, S, 2 * pairs + 1)
 
 
+# as many workgroups as CUs with 16, 32 and 64 columns each, and a few columns more
+@pytest.mark.parametrize("M,N", [(16, 4096), (16, 4100), (3, 8192), (16, 8200), (30, 10240), (64, 5120), (40, 8208), (130, 1360), (130, 2560), (384, 1536), (200, 4000)])
+def test_columns_of_few_rows(M, N):
+    """Few rows share their columns out in three widths: each column's bits are the same in all."""
+    g = rng(N)
+    x, w = paired(g, M, 4, 16, True), paired(g, N, 4, 16, False)
+    xs, ws = paired_scales(g, 4, M), paired_scales(g, 4, (N + 127) // 128).t().contiguous()
+    got = fq.qf_gemm_fp8(x, xs, w, ws)
+    y, S = by_blocks(x, xs, w, spread_tiles(ws, N))
+    check(got, y, S, 9)
+    for lo in range(0, N, 768):
+        cols = slice(lo, min(lo + 768, N))
+        assert torch.equal(got[:, cols], fq.qf_gemm_fp8(x, xs, w[cols], ws[lo // 128:(cols.stop + 127) // 128]))
+    E = 8                                            # and groups
+    plan = fq.qf_row_plan((torch.arange(M, device="cuda") * E // M).int(), E)
+    grouped = fq.qf_gemm_fp8_grouped(x, xs, w[None, :N // 4].expand(E, -1, -1).contiguous(), ws[None, :(N // 4 + 127) // 128].expand(E, -1, -1).contiguous(), plan)
+    check(grouped, y[:, :N // 4], S[:, :N // 4], 9)
+
+
 # ------------------------------------------------- one term each ----
 @pytest.mark.parametrize("M,N,K", [(7, 40, 4112), (16, 100, 272), (32, 1000, 2064), (64, 130, 14352), (64, 200, 64), (300, 260, 304), (512, 264, 528),
                                    (1500, 1300, 1040), (4200, 4100, 4112)])
