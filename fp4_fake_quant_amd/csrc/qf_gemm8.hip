@@ -562,16 +562,20 @@ hipError_t launch_few(Gemm8Args a, int64_t tiles, int64_t likely, int nj, hipStr
 
 hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
   // Few rows stream w with columns and blocks split, 64 rows at a time; more take tiles, which need about a microsecond
-  // a block however few they are.  Microseconds few / tiles: 64 rows of 4096 -> 6144 15.0 / 31.5, 4096 -> 28672 39 / 38,
-  // 14336 -> 4096 35 / 106; 128 rows of 4096 -> 6144 19 / 31, 192 35 / 32, 128 of 4096 -> 28672 72 / 38; 256 of 14336 -> 4096
-  // 55 / 106, 512 106 / 106; 512 of 2048 -> 2048 11.3 / 14.4; 128 groups of 2048 -> 1536 with 16 rows each 78 / 93, with 32
-  // 109 / 97.  Columns of a workgroup 16 / 32 / 64: 16 rows of 4096 -> 6144 11.4 / 9.5 / 12.5, 4096 -> 28672 32.5 / 28.7 /
-  // 26.3, 14336 -> 4096 17.7 / 23.7 / 35.9; 128 groups of 2048 -> 1536 with 4 rows each 73 / 66 / 70, with 16 106 / 88 / 78.
+  // a block however few they are.  Microseconds few / tiles: 64 rows of 4096 -> 6144 15.0 / 31.5, 14336 -> 4096 35 / 106; 128
+  // rows of 4096 -> 6144 19 / 31, 192 35 / 32, 128 of 4096 -> 28672 72 / 38; 256 of 14336 -> 4096 55 / 106, 512 106 / 106; 512
+  // of 2048 -> 2048 11.3 / 14.4; 128 groups of 2048 -> 1536 with 16 rows each 78 / 93, with 32 109 / 97; groups with 4 rows
+  // in 16 / 32 / 64 columns a workgroup 73 / 66 / 70, with 16 rows 106 / 88 / 78.
+  // From 33 rows on the border lies where the workgroups of 64 columns no longer fit the CUs: over one round a CU for
+  // several parts (128 rows of 4096 -> 8192 20.0 / 33.9, -> 10240 36.1 / 34.4, of 14336 59 / 110, 109 / 111), over two for
+  // 33 to 64 rows (64 rows of 2048 -> 16384 12.2 / 19.1, -> 28672 22.3 / 20.8, -> 45056 32.4 / 25.3, -> 65536 43.4 / 30.3; of
+  // 4096 -> 16384 21.9 / 35.2, -> 32768 41.0 / 42.3, -> 45056 59.4 / 49.9, -> 65536 79.6 / 69.4; of 14336 -> 32768 122 / 125, ->
+  // 45056 175 / 145).  Up to 32 rows they stay ahead (32 rows of 2048 -> 65536 30.8 / 29.6, 4096 -> 65536 59 / 68).
   if (mode == G8_DENSE) {
-    const int64_t parts = (a.M + 63) / 64;
+    const int64_t parts = (a.M + 63) / 64, wgs = parts * ((a.N + 63) / 64);
     if (a.M <= 16) return launch_few<G8_DENSE, 1>(a, 1, 1, 4, s);
     if (a.M <= 32) return launch_few<G8_DENSE, 2>(a, 1, 1, 4, s);
-    if (parts == 1 || (parts <= 8 && parts * a.N <= 16384)) return launch_few<G8_DENSE, 4>(a, parts, parts, 4, s);
+    if (parts <= 8 && wgs <= (parts == 1 ? 2 : 1) * G8_CUS) return launch_few<G8_DENSE, 4>(a, parts, parts, 4, s);
   }
   const int64_t groups = a.M < a.n_ids ? a.M : a.n_ids;
   if (mode == G8_ROWS && a.M <= 24 * (int64_t)a.n_ids)

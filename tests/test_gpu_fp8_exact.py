@@ -76,9 +76,11 @@ def spread_tiles(ws, N):
 # few rows (up to 16, 32, 64, several times 64), tiles of 128, tiles of 256
 DENSE = [(1, 40, 1, 16), (7, 300, 16, 16), (16, 1000, 56, 112), (32, 200, 16, 48), (64, 130, 16, 16), (64, 1500, 4, 80), (300, 260, 16, 16),
          (900, 1300, 16, 16), (700, 700, 56, 96), (4200, 4100, 16, 16)]
+# the last columns that few rows take in their own way, and the first that they take in tiles
+WIDE = [(33, 32768, 1, 16), (33, 32769, 1, 16), (64, 50000, 1, 96), (65, 8192, 1, 16), (100, 8200, 2, 16), (32, 70000, 1, 16)]
 
 
-@pytest.mark.parametrize("M,N,pairs,tail", DENSE)
+@pytest.mark.parametrize("M,N,pairs,tail", DENSE + WIDE)
 def test_dense(M, N, pairs, tail):
     g = rng(M + N)
     x, w = paired(g, M, pairs, tail, True), paired(g, N, pairs, tail, False)
