@@ -57,15 +57,15 @@ __device__ __forceinline__ f32x4_t mfma_f8(i32x8_t a, i32x8_t b, f32x4_t c) {
 // one is computed from, the next is on its way, and its place is refilled as soon as every wave has read
 // its last fragments.
 //
-// 256 x 256 (two stages of 66 KiB, one workgroup per CU, two waves per SIMD, 228 to 251 registers): per step and wave
+// 256 x 256 (two stages of 66 KiB, one workgroup per CU, two waves per SIMD, 228 to 255 registers): per step and wave
 // 32 products, 128 sums (256 where w has a scale per row) and 24 reads of 16 bytes.  32768 x 14336 x 4096 takes 1.70 ms
-// (2.26 PFLOP/s; a library product with one scale per tensor 1.27 ms): the matrix cores are busy 54% of 1.96 GHz,
+// (2.26 PFLOP/s; 1.68 to 1.81 by card; a library product with one scale per tensor 1.27 ms): the matrix cores are busy 54% of 1.96 GHz,
 // which is what the card's power leaves of 2.4, and the 940 MB of results, which all workgroups write at the same time, take
 // 0.18 ms of it (1.52 ms per 4096 of K without).  On the way: fragments straight from memory 6.99 ms; LDS with two
 // barriers a step 2.07; sums between the products and reads without conflicts 1.99; one barrier 1.89; workgroups that stay
 // 1.72.  Runs of 4 tile rows: 1 / 2 / 4 / 8 / 16 / 32 take 1.88 / 1.84 / 1.82 / 1.83 / 1.86 / 1.92 ms (before the last step).
 // 64 groups of about 512 rows, 4096 -> 4096, take 0.70 ms (1.57 PFLOP/s): a group's last tile is half empty.  Weight
-// gradients of 64 groups, 2048 x 2048, take 0.30 ms: 4 or 5 steps a tile, then 537 MB of results.
+// gradients of 64 groups, 2048 x 2048, take 0.27 to 0.30 ms: 4 or 5 steps a tile, then 537 MB of results.
 // 128 x 128 (four waves, two workgroups per CU) is for products of fewer than 1024 such tiles, which 256 x 256 would leave
 // CUs without: the large product takes 2.07 ms in it, 512 x 2048 x 2048 14 us.
 template <int BM, int BN>
@@ -417,8 +417,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void k_gemm8(Gemm8Args a) {
 // Up to 16 MT rows: the product streams w once, so the work is split over its columns (16 NJ a workgroup)
 // and over the blocks of the reduction, which the workgroup's waves take in turn and join in LDS in a
 // fixed order.  Operands go from memory into registers, several blocks ahead.  Bound by the bytes of w where
-// there are enough of them (61 tokens to 8 of 128 experts of 2048 -> 1536: 63 us, 6.3 TB/s; 16 rows of 4096 -> 28672 26 us,
-// 4.4 TB/s), else by the call (7 rows of 4096 -> 6144: 8.7 us, kernel 7.7 traced), and with more rows by x, which every
+// there are enough of them (61 tokens to 8 of 128 experts of 2048 -> 1536: 64 us, 6.2 TB/s; 16 rows of 4096 -> 28672 26 us,
+// 4.4 TB/s), else by the call (7 rows of 4096 -> 6144: 8.4 to 8.7 us, kernel 7.7 to 8.1 traced), and with more rows by x, which every
 // workgroup reads from the caches.
 constexpr int FEW_WAVES = 8;
 
