@@ -205,8 +205,10 @@ __global__ __launch_bounds__(Q8_WG) void k_swiglu_backward(GateArgs a) {
       const float s = sigmoid(g[e]);
       const float m = g[e] * s;
       const float f = s * (1.0f + (g[e] - m)), du = d[e] * u[e];
-      // da u past the range (both factors are above 1 then): a small f comes first
-      g[e] = fabsf(du) < __builtin_inff() ? du * f : (d[e] * f) * u[e];
+      // da u past the range with a finite u: a small f comes first (it loses nothing: both factors are above 1, or da is
+      // infinite)
+      const bool past = !(fabsf(du) < __builtin_inff()) && fabsf(u[e]) < __builtin_inff();
+      g[e] = past ? (d[e] * f) * u[e] : du * f;
       u[e] = d[e] * m;
     }
 #pragma unroll

@@ -89,3 +89,21 @@ def test_gradient_past_the_range():
     assert np.all((err <= 2.0 ** -8 * np.abs(want) + (1 + 2.0 ** -8) * off + 2.0 ** -134)[keep]), np.argwhere(~(err <= off) & keep)
     past = np.abs(want) - off > top * (1 + 2.0 ** -8)
     assert past.any() and np.array_equal(got[past], np.copysign(INF, want[past]))
+
+
+@pytest.mark.parametrize("u", [INF, -INF])
+@pytest.mark.parametrize("da", [1e-38, -2.0 ** -133, 3e38])
+def test_gradient_of_an_infinite_factor(u, da):
+    """An infinite u or da against a small other factor and a small sigmoid: the formula's infinity, no NaN."""
+    cols = 16
+    g = np.array([-85.0, -60, -20, -2, 0, 2, 200])
+    h, d = np.zeros((2 * g.size, 2 * cols)), np.zeros((2 * g.size, cols))
+    h[:, 0] = np.tile(g, 2)
+    h[:, cols] = np.repeat([u, da], g.size)
+    d[:, 0] = np.repeat([da, u], g.size)
+    got = f32(host(fq.qf_swiglu_backward(dev(bits(h)), dev(bits(d)))))
+    with np.errstate(all="ignore"):
+        want = fp8.swiglu_backward(f32(bits(h)), f32(bits(d)))
+    assert np.isinf(want[:, 0]).all()
+    want = np.where(np.abs(want) >= 2.0 ** 128, np.copysign(INF, want), want)
+    same_non_finite(got, want)
