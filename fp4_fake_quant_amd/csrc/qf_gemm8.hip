@@ -577,6 +577,8 @@ hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
     if (a.M <= 32) return launch_few<G8_DENSE, 2>(a, 1, 1, 4, s);
     if (parts <= 8 && wgs <= (parts == 1 ? 2 : 1) * G8_CUS) return launch_few<G8_DENSE, 4>(a, parts, parts, 4, s);
   }
+  // Groups go by their mean, as their sizes are on the device: few / tiles of 1536 rows of 2048 -> 4096 evenly in 64 groups
+  // 117 / 137, with half of them in one 132 / 161, with all 73 / 32; 2048 rows of 2048 -> 1536 in 128 groups 80 / 102, 93 / 123, 39 / 31.
   const int64_t groups = a.M < a.n_ids ? a.M : a.n_ids;
   if (mode == G8_ROWS && a.M <= 24 * (int64_t)a.n_ids)
     return launch_few<G8_ROWS, 2>(a, (a.M + QF_ROW_TILE - 1) / QF_ROW_TILE + groups, groups, a.M < 8 * (int64_t)a.n_ids ? 2 : 4, s);
@@ -584,6 +586,10 @@ hipError_t launch(Gemm8Args a, int mode, hipStream_t s) {
   // through the caches / past them: 32768 x 14336 x 4096 1.73 / 1.70 ms; 32768 rows of 2048 -> 4096 for 16 groups 305 / 287 us
   // (with the sum over a token's four rows that follows 360 / 341), half the rows 166 / 154 (188 / 185), a quarter 92 / 91 (107 / 109)
   if (a.y_vec && (int64_t)a.M * a.N * 2 * (mode == G8_BLOCKS ? a.n_ids : 1) >= NT_ROWS_BYTES) a.y_vec = 2;
+  // 128 / 256, codes drawn evenly: weight gradients of 64 groups of 512 rows, 2048 x 2048, 244 / 210 us, of 128 rows 113 / 109,
+  // of 64 groups of 1024 x 1024 61 / 62, one of 8192 rows, 4096 x 4096 (1024 tiles), 166 / 150, 512 rows, 14336 x 4096, 54 / 56;
+  // rows of 64 groups 4096 -> 4096, 512 a group 680 / 544, 300 494 / 498, 200 352 / 290, but 128 248 / 269; 8 groups of 256 rows
+  // 2048 -> 2048 (384 tiles) 19 / 32
   if (small_tiles(a, mode) >= 1024) return launch_tiles<256, 256, 2, 4>(a, mode, s);
   return launch_tiles<128, 128, 2, 2>(a, mode, s);
 }
